@@ -205,6 +205,82 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
                      void *stream);
 
 /*
+ * Rotary frequencies of a model, laid out on the device once: pa_rope_append
+ * turns dimension pair i of a row at position p by the angle p * inv_freq[i].
+ *   inv_freq      host, rot_dim / 2 finite frequencies in radians per position
+ *   rot_dim       rotated dimensions of a head, a multiple of 16 (16 .. 128); dimensions
+ *                 from rot_dim on pass through
+ *   interleaved   0: pair i is dimensions (i, i + rot_dim / 2); 1: (2i, 2i + 1)
+ *   scale         factor on every cosine and sine (1 for a plain rotation), finite
+ * The frequencies are kept as turns per position in 64-bit fixed point, so the
+ * angle is exact to p * 2^-64 turns (plus the frequency's own rounding, 2^-64
+ * turns per position) at any 32-bit position.
+ * Synchronises the device. Errors: PA_ERR_INVALID_ARG, PA_ERR_OOM, PA_ERR_CUDA.
+ */
+typedef struct pa_rope pa_rope;
+pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
+                         pa_rope **out);
+void pa_rope_destroy(pa_rope *rope);
+
+/*
+ * Rotate and append: for each token i, the q and k rows are rotated by
+ * positions[i]; rotated q goes to q_out, rotated k and v to the pool at
+ * slot_mapping[i], as pa_cache_write would put them (negative slots are
+ * skipped, q is still rotated; slots beyond the pool are skipped and flagged,
+ * PA_ERR_DEVICE_BOUNDS; two tokens with one slot: which one lands is
+ * unspecified). Rotation is fp32, rounded once to the model type; an FP8 pool's
+ * k codes are quantised from the fp32 values.
+ *   q, k, v       device rows [heads, head_dim] of the pool's dtype, 16-byte aligned; token i's
+ *                 starts i * stride elements behind the first (strides: multiples of 8, at least
+ *                 heads * head_dim), so the three may be slices of one projection's output
+ *   positions     device int32 [num_tokens], any sign
+ *   slot_mapping  device int64 [num_tokens]
+ *   num_q_heads   >= 0; 0 appends without a q (q and q_out are then ignored)
+ *   q_out         device rows, q_out_stride as above; may be q itself with the same stride,
+ *                 must not overlap the inputs otherwise
+ *   k_cache/v_cache  device pools to write, or NULL for the pool's own
+ * The rope's rot_dim is at most the pool's head_dim, and its device the pool's.
+ */
+pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                         const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                         int64_t q_out_stride, void *k_cache, void *v_cache, void *stream);
+
+/*
+ * Causal attention of packed prompts: num_seqs sequences with different numbers
+ * of new tokens, rows cu_q[b] .. cu_q[b+1] of q belonging to sequence b, their K
+ * and V already in the pool (pa_rope_append or pa_cache_write). Row i of
+ * sequence b's n_b sits at position context_lens[b] - n_b + i and attends to
+ * tokens 0..that position through the block table: whole prompts
+ * (context_lens[b] = n_b), prompts with a cached prefix, chunks and single
+ * tokens may be mixed. Values at positions a row does not see (later tokens,
+ * unwritten slots) do not reach it, whatever their words are.
+ *   q, out         device [num_tokens, num_q_heads, head_dim], not overlapping
+ *   cu_q           device int32 [num_seqs + 1], 0 <= cu_q[b] <= cu_q[b+1] <= num_tokens;
+ *                  rows before cu_q[0] and from cu_q[num_seqs] on are left as they are in out
+ *   block_tables   device int32 [num_seqs, block_table_stride]; entries at or beyond
+ *                  ceil(context_lens[b] / bs) are never read
+ *   context_lens   device int32 [num_seqs]; n_b <= context_lens[b] <= stride * bs
+ *   num_q_heads    a multiple of num_kv_heads, at most 128 per KV head
+ *   scale          softmax scale, finite and > 0
+ *   workspace      device, 16-byte aligned, at least pa_prefill_packed_workspace() bytes, written
+ *                  by this call alone while it runs
+ * Violations in cu_q, block_tables or context_lens are clamped and flagged
+ * (PA_ERR_DEVICE_BOUNDS at pa_pool_check); the sequence's outputs are then
+ * unspecified. 16-bit pools, head_dim 64 or 128 (PA_ERR_UNSUPPORTED
+ * otherwise), at most PA_PACKED_MAX_SEQS sequences. Nothing of the pool is written, so
+ * calls with workspaces of their own may run at the same time. Results are
+ * deterministic run to run.
+ */
+#define PA_PACKED_MAX_SEQS 2048
+pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t block_table_stride, uint64_t *bytes);
+pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, const void *v_cache,
+                            const int32_t *cu_q, const int32_t *block_tables, int32_t block_table_stride,
+                            const int32_t *context_lens, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                            float scale, void *workspace, uint64_t workspace_bytes, void *out, void *stream);
+
+/*
  * Synchronise the device, read and clear the pool's status word.
  * Returns PA_OK, PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT or PA_ERR_CUDA.
  */
@@ -292,6 +368,63 @@ pa_status pa_copy_blocks(pa_pool *pool, const int32_t *pairs, int32_t n, void *k
 pa_status pa_spec_verify(const float *p, const float *q, const int32_t *draft, const float *u, const float *v,
                          int32_t num_seqs, int32_t num_draft, int64_t vocab, int32_t *out, int32_t *n_out,
                          void *stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on logits
+ * (pa_adjust_logits), and the token distribution of the result
+ * (pa_token_probs), in the form pa_spec_verify takes as p. Row j of sequence b
+ * (rows_per_seq rows each; row j of a verify follows drafts 0..j-1), token t,
+ * in single fp32 steps in this order:
+ *   count = occurrences of t in history[b][prompt_lens[b]..history_lens[b]) and draft[b][0..j)
+ *   seen  = count > 0, or t occurs in history[b][0..prompt_lens[b])
+ *   x = logit;  if seen: x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   x = x - frequency[b] * count;  if count > 0: x = x - presence[b]
+ *   x = x + bias of t;  if t's mask bit is 0: x = -inf
+ *   pa_adjust_logits: out = x
+ *   pa_token_probs:   out = exp((x - max x) / temperature[b]) / sum; temperature 0: 1 at the largest
+ *                     x (the lowest index of equals), 0 elsewhere
+ * A row whose mask leaves nothing (or only -inf) gives all -inf, all 0 as
+ * probabilities (no mass: pa_spec_verify then draws no token). What a masked
+ * logit holds does not matter; a NaN that is not masked makes its row of
+ * probabilities NaN, and so does a +inf at a temperature above 0.
+ * Every list pointer may be NULL (and its count 0): that step is then left out.
+ */
+typedef enum pa_logits_dtype { PA_LOGITS_FP16 = 0, PA_LOGITS_BF16 = 1, PA_LOGITS_FP32 = 2 } pa_logits_dtype;
+
+typedef struct pa_logits_args {
+    const void *logits;        /* device; row (b, j) starts at b * seq_stride + j * row_stride elements */
+    int32_t dtype;             /* pa_logits_dtype */
+    int32_t num_seqs;          /* >= 0 */
+    int32_t rows_per_seq;      /* >= 1 (num_draft + 1 for a verify); num_seqs * rows_per_seq < 2^24 */
+    int32_t num_bias;          /* entries of a bias row, 0 .. PA_LOGITS_MAX_BIAS */
+    int64_t vocab;             /* 1 .. PA_LOGITS_MAX_VOCAB */
+    int64_t seq_stride, row_stride;   /* elements, >= 0; rows need not be aligned beyond an element */
+    const int32_t *history;    /* device [num_seqs, history_stride]: prompt tokens, then outputs */
+    int64_t history_stride;    /* 0 .. PA_LOGITS_MAX_HISTORY */
+    const int32_t *history_lens;  /* device [num_seqs], clamped to 0 .. history_stride; needed with history */
+    const int32_t *prompt_lens;   /* device [num_seqs]; NULL = 0 (every history token is an output) */
+    const int32_t *draft;      /* device [num_seqs, rows_per_seq - 1] */
+    const float *repetition;   /* device [num_seqs], > 0; 1 = none */
+    const float *presence;     /* device [num_seqs]; 0 = none */
+    const float *frequency;    /* device [num_seqs]; 0 = none */
+    const int32_t *bias_tokens;   /* device [num_seqs, num_bias]; the last entry naming a token counts */
+    const float *bias_values;  /* device [num_seqs, num_bias] */
+    const int32_t *mask;       /* device [num_seqs, rows_per_seq, ceil(vocab / 32)]: bit t % 32 of word
+                                  t / 32 allows token t */
+    const float *temperature;  /* device [num_seqs], >= 0 (pa_token_probs; ignored by pa_adjust_logits);
+                                  a negative or NaN one makes its rows NaN */
+    float *out;                /* device fp32 [num_seqs, rows_per_seq, vocab]; may be logits itself (fp32,
+                                  same strides), must not overlap the inputs otherwise */
+} pa_logits_args;
+
+/* Token ids outside the vocabulary (in history, draft or bias_tokens; -1 as padding) are ignored. No pool
+   is needed; work is launched on the current device. PA_ERR_INVALID_ARG / PA_ERR_UNSUPPORTED (sizes above
+   the limits) before anything is launched. */
+#define PA_LOGITS_MAX_VOCAB 393216
+#define PA_LOGITS_MAX_HISTORY 1000000
+#define PA_LOGITS_MAX_BIAS 2000
+pa_status pa_adjust_logits(const pa_logits_args *args, void *stream);
+pa_status pa_token_probs(const pa_logits_args *args, void *stream);
 
 /*
  * Self-test of failure detection. Every wait of the kernels' copy pipelines is

@@ -1,10 +1,11 @@
-// pa_api.cu -- the C ABI declared in include/pagedattn.h: pool lifecycle, argument
+// pa_api.cu -- the C ABI declared in include/pagedattn.h: pool and rope lifecycle, argument
 // validation, TMA descriptor encoding and kernel launches. No computation happens
-// here; every step of the path runs in the kernels of cache_write.cu and decode.cu.
+// here; every step of the path runs in the kernels of the other sources.
 #include <cudaTypedefs.h>
 
 #include <cmath>
 #include <mutex>
+#include <new>
 #include <unordered_map>
 
 #include "pa_internal.h"
@@ -30,6 +31,12 @@ struct pa_pool {
     cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
     std::mutex mu;
     std::unordered_map<const void *, CUtensorMap> maps;
+};
+
+struct pa_rope {
+    uint64_t *freq = nullptr;    // device [rot_dim / 2], 2^-64 turns per position
+    int rot = 0, interleaved = 0, device = 0;
+    float scale = 1.f;
 };
 
 namespace {
@@ -470,6 +477,235 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
     return launch_prefill(p, c.dtype, tmk, tmv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                                  : PA_ERR_CUDA;
 }
+
+pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
+                         pa_rope **out) {
+    if (!out) return PA_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!inv_freq || rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1) ||
+        !std::isfinite(scale) || device < 0)
+        return PA_ERR_INVALID_ARG;
+    uint64_t f[64];
+    // 1 / 2 pi as the sum of two doubles: the nearest double and what is left of it
+    const double inv_2pi = 0.15915494309189535, inv_2pi_lo = -9.839338337591243e-18;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double w = inv_freq[i];
+        if (!std::isfinite(w) || std::fabs(w) > 1e6) return PA_ERR_INVALID_ARG;
+        const double hi = w * inv_2pi;
+        const double lo = std::fma(w, inv_2pi, -hi) + w * inv_2pi_lo;
+        const double frac = hi - std::floor(hi);                      // [0, 1), exact
+        f[i] = (frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+    }
+    DeviceGuard g(device);
+    if (!g.ok) return PA_ERR_CUDA;
+    pa_rope *r = new (std::nothrow) pa_rope();
+    if (!r) return PA_ERR_OOM;
+    r->rot = rot_dim;
+    r->interleaved = interleaved;
+    r->scale = scale;
+    r->device = device;
+    if (cudaMalloc(&r->freq, sizeof(f)) != cudaSuccess) {
+        cudaGetLastError();
+        delete r;
+        return PA_ERR_OOM;
+    }
+    if (cudaMemcpy(r->freq, f, sizeof(uint64_t) * (rot_dim / 2), cudaMemcpyHostToDevice) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(r->freq);
+        delete r;
+        return PA_ERR_CUDA;
+    }
+    *out = r;
+    return PA_OK;
+}
+
+void pa_rope_destroy(pa_rope *rope) {
+    if (!rope) return;
+    DeviceGuard g(rope->device);
+    cudaFree(rope->freq);
+    delete rope;
+}
+
+pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                         const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                         int64_t q_out_stride, void *k_cache, void *v_cache, void *stream) {
+    if (!pool || !rope || num_tokens < 0 || num_q_heads < 0 || num_q_heads > 65536) return PA_ERR_INVALID_ARG;
+    const pa_pool_config &c = pool->cfg;
+    if (rope->rot > c.head_dim || rope->device != c.device) return PA_ERR_INVALID_ARG;
+    if ((k_cache == nullptr) != (v_cache == nullptr)) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!k || !v || !positions || !slot_mapping || (num_q_heads > 0 && (!q || !q_out))) return PA_ERR_INVALID_ARG;
+    if (!k_cache) {
+        k_cache = pool->k_cache;
+        v_cache = pool->v_cache;
+    }
+    const int64_t kv_row = (int64_t)c.num_kv_heads * c.head_dim, q_row = (int64_t)num_q_heads * c.head_dim;
+    if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 != 0 || q_out_stride % 8 != 0 ||
+                            (q == q_out && q_stride != q_out_stride) || !aligned16(q) || !aligned16(q_out)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PA_ERR_INVALID_ARG;
+    RopeParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.positions = positions;
+    p.slots = slot_mapping;
+    p.freq = rope->freq;
+    p.mscale = rope->scale;
+    p.rot = rope->rot;
+    p.interleaved = rope->interleaved;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.status = pool->status;
+    p.num_tokens = num_tokens;
+    p.num_blocks = c.num_blocks;
+    p.Hq = num_q_heads;
+    p.Hkv = c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.bs = c.block_size;
+    p.fp8 = c.kv_format == PA_KV_FP8_E4M3;
+    DeviceGuard g(c.device);
+    if (!g.ok) return PA_ERR_CUDA;
+    return launch_rope_append(p, c.dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The checks of pa_prefill_packed's sizes, shared with the workspace query.
+static pa_status packed_params(const pa_pool *pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t stride, PromptParams &p) {
+    const pa_pool_config &c = pool->cfg;
+    if (num_tokens < 0 || num_seqs < 0 || num_q_heads < 1 || num_q_heads % c.num_kv_heads != 0 || stride < 1)
+        return PA_ERR_INVALID_ARG;
+    if (c.kv_format != PA_KV_16BIT) return PA_ERR_UNSUPPORTED;
+    const int G = num_q_heads / c.num_kv_heads;
+    if (G > 128 || num_seqs > PA_PACKED_MAX_SEQS || (int64_t)num_tokens * num_q_heads >= (int64_t)1 << 31)
+        return PA_ERR_UNSUPPORTED;
+    int64_t max_ctx = (int64_t)stride * c.block_size;
+    if (max_ctx > 0x7fffff00) max_ctx = 0x7fffff00;
+    p.stride = stride;
+    p.num_tokens = num_tokens;
+    p.num_seqs = num_seqs;
+    p.Hq = num_q_heads;
+    p.Hkv = c.num_kv_heads;
+    p.G = G;
+    p.bs = c.block_size;
+    p.num_blocks = c.num_blocks;
+    p.max_ctx = (int)max_ctx;
+    p.status = pool->status;
+    p.wait_ns = pool->wait_ns;
+    return PA_OK;
+}
+
+pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t block_table_stride, uint64_t *bytes) {
+    if (!pool || !bytes) return PA_ERR_INVALID_ARG;
+    PromptParams p;
+    const pa_status st = packed_params(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, p);
+    if (st != PA_OK) return st;
+    *bytes = 256;
+    return PA_OK;
+}
+
+pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, const void *v_cache,
+                            const int32_t *cu_q, const int32_t *block_tables, int32_t block_table_stride,
+                            const int32_t *context_lens, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                            float scale, void *workspace, uint64_t workspace_bytes, void *out, void *stream) {
+    if (!pool || !std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+    if ((k_cache == nullptr) != (v_cache == nullptr)) return PA_ERR_INVALID_ARG;
+    PromptParams p;
+    const pa_status st = packed_params(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, p);
+    if (st != PA_OK) return st;
+    if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+    uint64_t need = 0;
+    pa_prefill_packed_workspace(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, &need);
+    if (!q || !out || !cu_q || !block_tables || !context_lens || !workspace || workspace_bytes < need)
+        return PA_ERR_INVALID_ARG;
+    const pa_pool_config &c = pool->cfg;
+    if (!k_cache) {
+        k_cache = pool->k_cache;
+        v_cache = pool->v_cache;
+    }
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_q) & 3u))
+        return PA_ERR_INVALID_ARG;
+    p.q = q;
+    p.out = out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.cu_q = cu_q;
+    p.context_lens = context_lens;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    DeviceGuard g(c.device);
+    if (!g.ok) return PA_ERR_CUDA;
+    return launch_prompt(p, c.dtype, c.head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                   : PA_ERR_CUDA;
+}
+
+static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) {
+    if (!a || a->num_seqs < 0 || a->rows_per_seq < 1 || a->num_bias < 0 || a->vocab < 1 || a->seq_stride < 0 ||
+        a->row_stride < 0 || a->history_stride < 0)
+        return PA_ERR_INVALID_ARG;
+    if (a->dtype != PA_LOGITS_FP16 && a->dtype != PA_LOGITS_BF16 && a->dtype != PA_LOGITS_FP32)
+        return PA_ERR_INVALID_ARG;
+    if (a->vocab > PA_LOGITS_MAX_VOCAB || a->history_stride > PA_LOGITS_MAX_HISTORY ||
+        a->num_bias > PA_LOGITS_MAX_BIAS || a->rows_per_seq > 4096 ||
+        (int64_t)a->num_seqs * a->rows_per_seq >= (int64_t)1 << 24)
+        return PA_ERR_UNSUPPORTED;
+    if (a->num_seqs == 0) return PA_OK;
+    const bool has_history = a->history && a->history_stride > 0;
+    if (!a->logits || !a->out || (probs && !a->temperature) || (has_history && !a->history_lens) ||
+        (a->num_bias > 0 && (!a->bias_tokens || !a->bias_values)))
+        return PA_ERR_INVALID_ARG;
+    const uintptr_t esize = a->dtype == PA_LOGITS_FP32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(a->logits) % esize != 0) return PA_ERR_INVALID_ARG;
+    const void *words[] = {a->history,     a->history_lens, a->prompt_lens, a->draft, a->repetition, a->presence, a->frequency,
+                           a->bias_tokens, a->bias_values,  a->mask,        a->temperature, a->out};
+    for (const void *x : words)
+        if (reinterpret_cast<uintptr_t>(x) & 3u) return PA_ERR_INVALID_ARG;
+    const int64_t V = a->vocab, R = a->rows_per_seq;
+    const bool in_place = a->logits == static_cast<const void *>(a->out);
+    if (in_place && (a->dtype != PA_LOGITS_FP32 || (R > 1 && a->row_stride != V) ||
+                     (a->num_seqs > 1 && a->seq_stride != R * V)))
+        return PA_ERR_INVALID_ARG;
+    LogitsParams p;
+    p.logits = a->logits;
+    p.dtype = a->dtype;
+    p.B = a->num_seqs;
+    p.R = a->rows_per_seq;
+    p.V = (int)V;
+    p.seq_stride = a->seq_stride;
+    p.row_stride = a->row_stride;
+    p.history = has_history ? a->history : nullptr;
+    p.history_stride = a->history_stride;
+    p.history_cap = (int)a->history_stride;
+    p.history_lens = a->history_lens;
+    p.prompt_lens = a->prompt_lens;
+    p.draft = R > 1 ? a->draft : nullptr;
+    p.repetition = a->repetition;
+    p.presence = a->presence;
+    p.frequency = a->frequency;
+    p.bias_tokens = a->bias_tokens;
+    p.bias_values = a->bias_values;
+    p.num_bias = a->num_bias;
+    p.mask = a->mask;
+    p.temperature = a->temperature;
+    p.out = a->out;
+    return launch_logits(p, probs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_adjust_logits(const pa_logits_args *args, void *stream) { return logits_call(args, false, stream); }
+
+pa_status pa_token_probs(const pa_logits_args *args, void *stream) { return logits_call(args, true, stream); }
 
 pa_status pa_copy_blocks(pa_pool *pool, const int32_t *pairs, int32_t n, void *k_cache, void *v_cache,
                          void *stream) {

@@ -107,6 +107,115 @@ def _dev(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> tor
     return t
 
 
+def _on(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    """The given stream's handle (a stream of `device`), else that device's current stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}, got {stream.device}")
+        return stream.cuda_stream
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _new(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A tensor that the call writes on `stream`: allocated there, and kept for work queued on the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, n: int, heads: Optional[int],
+                d: int) -> None:
+    """Token rows [n, heads, d]: heads and dimensions dense, tokens at any stride of whole 16-byte vectors."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    _on(t, name, device)
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
+    dense = t.stride(2) == 1 and (t.shape[1] <= 1 or t.stride(1) == d)
+    if t.numel() > 0 and (not dense or (n > 1 and (t.stride(0) < t.shape[1] * d or t.stride(0) % 8 != 0))):
+        raise ValueError(f"{name} must have dense heads and a token stride of whole 16-byte vectors, got strides "
+                         f"{t.stride()}")
+
+
+class Rope:
+    """Rotary frequencies on the device (pa_rope_create): pair i turns by position * inv_freq[i] radians.
+
+    inv_freq: rot_dim / 2 frequencies. interleaved: pairs are neighbouring dimensions (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2). scale: factor on every cosine and sine."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, scale: float = 1.0, device: int = 0):
+        f = [float(x) for x in inv_freq]
+        self.rot_dim, self.device = 2 * len(f), torch.device("cuda", device)
+        h = C.c_void_p()
+        self._h = None
+        _check(_serving_lib().pa_rope_create((C.c_double * max(1, len(f)))(*f), self.rot_dim, int(bool(interleaved)),
+                                             float(scale), device, C.byref(h)), "pa_rope_create")
+        self._h = h
+
+    @classmethod
+    def from_base(cls, rot_dim: int, base: float = 10000.0, **kw) -> "Rope":
+        """Frequencies base ** (-2i / rot_dim)."""
+        return cls([base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], **kw)
+
+    @property
+    def handle(self) -> C.c_void_p:
+        if self._h is None:
+            raise RuntimeError("rope is closed")
+        return self._h
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None:
+            _serving_lib().pa_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_serving_ready = False
+
+
+class PaLogitsArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int32), ("num_seqs", C.c_int32), ("rows_per_seq", C.c_int32),
+                ("num_bias", C.c_int32), ("vocab", C.c_int64), ("seq_stride", C.c_int64), ("row_stride", C.c_int64),
+                ("history", C.c_void_p), ("history_stride", C.c_int64), ("history_lens", C.c_void_p),
+                ("prompt_lens", C.c_void_p), ("draft", C.c_void_p), ("repetition", C.c_void_p),
+                ("presence", C.c_void_p), ("frequency", C.c_void_p), ("bias_tokens", C.c_void_p),
+                ("bias_values", C.c_void_p), ("mask", C.c_void_p), ("temperature", C.c_void_p), ("out", C.c_void_p)]
+
+
+def _serving_lib() -> C.CDLL:
+    global _serving_ready
+    L = lib()
+    if not _serving_ready:
+        P, I32, I64, U64 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64
+        L.pa_rope_create.argtypes = [C.POINTER(C.c_double), I32, I32, C.c_float, I32, C.POINTER(C.c_void_p)]
+        L.pa_rope_destroy.argtypes = [P]
+        L.pa_rope_destroy.restype = None
+        L.pa_rope_append.argtypes = [P, P, P, I64, P, I64, P, I64, P, P, I32, I32, P, I64, P, P, P]
+        L.pa_prefill_packed_workspace.argtypes = [P, I32, I32, I32, I32, C.POINTER(U64)]
+        L.pa_prefill_packed.argtypes = [P, P, P, P, P, P, I32, P, I32, I32, I32, C.c_float, P, U64, P, P]
+        L.pa_adjust_logits.argtypes = [C.POINTER(PaLogitsArgs), P]
+        L.pa_token_probs.argtypes = [C.POINTER(PaLogitsArgs), P]
+        for f in ("pa_rope_create", "pa_rope_append", "pa_prefill_packed_workspace", "pa_prefill_packed",
+                  "pa_adjust_logits", "pa_token_probs"):
+            getattr(L, f).restype = C.c_int
+        _serving_ready = True
+    return L
+
+
 class Pool:
     """One paged KV pool (pa_pool_create) with its caches.
 
@@ -243,6 +352,84 @@ class Pool:
                                 block_tables.shape[1], _ptr(context_lens), B, Hq, q_len, float(scale), _ptr(out),
                                 _stream(stream)), "pa_prefill")
         return out
+
+    def rope_append(self, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    slot_mapping: torch.Tensor, rope: "Rope", q_out: Optional[torch.Tensor] = None,
+                    k_cache: Optional[torch.Tensor] = None, v_cache: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+        """Rotate q [N, Hq, d] and k [N, Hkv, d] by positions (int32 [N]) and append k, v to the pool's slots
+        (pa_rope_append). Rows may be strided over tokens (slices of one projection's output). Returns the
+        rotated q [N, Hq, d] (q_out; may be q itself); q None appends only."""
+        hd = (self.geometry[1], self.geometry[3])
+        n = k.shape[0] if k.dim() == 3 else -1
+        for name, t, heads in (("q", q, None), ("k", k, hd[0]), ("v", v, hd[0]), ("q_out", q_out, None)):
+            if t is not None:
+                _token_rows(t, name, self.dtype, self.device, n, heads, hd[1])
+        for name, t, dt in (("positions", positions, torch.int32), ("slot_mapping", slot_mapping, torch.int64)):
+            _on(_dev(t, name, dt), name, self.device)
+            if t.dim() != 1 or t.shape[0] != n:
+                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+        self._check_caches(k_cache, v_cache)
+        hq = 0 if q is None else q.shape[1]
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+        elif q_out is None:
+            q_out = _new((n, hq, hd[1]), self.dtype, self.device, stream)
+        elif tuple(q_out.shape) != tuple(q.shape):
+            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        row = lambda t: 0 if t is None else t.stride(0) if n > 1 else t.shape[1] * hd[1]  # noqa: E731
+        _check(_serving_lib().pa_rope_append(
+            self.handle, rope.handle, _ptr(q), row(q), _ptr(k), row(k), _ptr(v), row(v), _ptr(positions),
+            _ptr(slot_mapping), n, hq, _ptr(q_out), row(q_out), _ptr(k_cache), _ptr(v_cache),
+            _stream_on(stream, self.device)), "pa_rope_append")
+        return q_out
+
+    def prefill_packed(self, q: torch.Tensor, cu_q: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                       k_cache: Optional[torch.Tensor] = None, v_cache: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Causal attention of packed prompts (pa_prefill_packed): rows cu_q[b]..cu_q[b+1] of q [T, Hq, d] are
+        sequence b's newest tokens, their K and V already in the pool. cu_q: int32 [B + 1]. The workspace
+        (uint8, packed_workspace() bytes) is allocated for the call unless given; calls that may run at the
+        same time need one each."""
+        d = self.geometry[3]
+        for name, t, dt in (("q", q, self.dtype), ("cu_q", cu_q, torch.int32),
+                            ("block_tables", block_tables, torch.int32), ("context_lens", context_lens, torch.int32)):
+            _on(_dev(t, name, dt), name, self.device)
+        if q.dim() != 3 or q.shape[2] != d:
+            raise ValueError(f"q must be [T, Hq, {d}], got {tuple(q.shape)}")
+        if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+            raise ValueError(f"cu_q must be [B + 1], got {tuple(cu_q.shape)}")
+        T, Hq, B = q.shape[0], q.shape[1], cu_q.shape[0] - 1
+        if block_tables.dim() != 2 or block_tables.shape[0] < B:
+            raise ValueError(f"block_tables must be [>= {B}, stride], got {tuple(block_tables.shape)}")
+        if context_lens.dim() != 1 or context_lens.shape[0] < B:
+            raise ValueError(f"context_lens must hold {B} entries, got {tuple(context_lens.shape)}")
+        if out is None:
+            out = _new(q.shape, self.dtype, self.device, stream)
+        _on(_dev(out, "out", self.dtype), "out", self.device)
+        if tuple(out.shape) != tuple(q.shape):
+            raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        self._check_caches(k_cache, v_cache)
+        if workspace is None:
+            workspace = _new((self.packed_workspace(T, B, Hq, block_tables.shape[1]),), torch.uint8, self.device,
+                             stream)
+        _on(_dev(workspace, "workspace", torch.uint8), "workspace", self.device)
+        _check(_serving_lib().pa_prefill_packed(
+            self.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_q), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), T, B, Hq, float(scale), _ptr(workspace), workspace.numel(), _ptr(out),
+            _stream_on(stream, self.device)), "pa_prefill_packed")
+        return out
+
+    def packed_workspace(self, num_tokens: int, num_seqs: int, num_q_heads: int, block_table_stride: int) -> int:
+        """Workspace bytes of prefill_packed for these sizes (pa_prefill_packed_workspace)."""
+        n = C.c_uint64()
+        _check(_serving_lib().pa_prefill_packed_workspace(self.handle, num_tokens, num_seqs, num_q_heads,
+                                                          block_table_stride, C.byref(n)),
+               "pa_prefill_packed_workspace")
+        return n.value
 
     def launches(self, block_table_stride: int, num_seqs: int, num_q_heads: int, q_len: int) -> int:
         return lib().pa_decode_launches(self.handle, block_table_stride, num_seqs, num_q_heads, q_len)
@@ -433,3 +620,83 @@ def spec_verify(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u: torch.
     _check(L.pa_spec_verify(_ptr(p), _ptr(q), _ptr(draft), _ptr(u), _ptr(v), B, K1 - 1, V, _ptr(out), _ptr(n_out),
                             _stream(stream)), "pa_spec_verify")
     return out, n_out
+
+
+_LOGITS_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _logits_call(name: str, logits: torch.Tensor, temperature: Optional[torch.Tensor], history, history_lens,
+                 prompt_lens, draft, repetition, presence, frequency, bias_tokens, bias_values, mask, out,
+                 stream) -> torch.Tensor:
+    if not logits.is_cuda or logits.dtype not in _LOGITS_DTYPE:
+        raise ValueError(f"logits must be a CUDA tensor of fp16, bf16 or fp32, got {logits.dtype} on {logits.device}")
+    if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
+        raise ValueError(f"logits must be [B, R, V], got {tuple(logits.shape)}")
+    if logits.shape[2] > 1 and logits.stride(2) != 1:
+        raise ValueError("logits must be dense over the vocabulary")
+    B, R, V = logits.shape
+    dev = logits.device
+    S = history.shape[1] if history is not None and history.dim() == 2 else 0
+    NB = bias_tokens.shape[1] if bias_tokens is not None and bias_tokens.dim() == 2 else 0
+    i32, f32 = torch.int32, torch.float32
+    for n, t, dt, shape in (("temperature", temperature, f32, (B,)), ("history", history, i32, (B, S)),
+                            ("history_lens", history_lens, i32, (B,)), ("prompt_lens", prompt_lens, i32, (B,)),
+                            ("draft", draft, i32, (B, R - 1)), ("repetition", repetition, f32, (B,)),
+                            ("presence", presence, f32, (B,)), ("frequency", frequency, f32, (B,)),
+                            ("bias_tokens", bias_tokens, i32, (B, NB)), ("bias_values", bias_values, f32, (B, NB)),
+                            ("mask", mask, i32, (B, R, (V + 31) // 32))):
+        if t is not None:
+            _on(_dev(t, n, dt), n, dev)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+    if (history is None) != (history_lens is None):
+        raise ValueError("pass both history and history_lens, or neither")
+    if prompt_lens is not None and history is None:
+        raise ValueError("prompt_lens without history")
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("pass both bias_tokens and bias_values, or neither")
+    if out is None:
+        out = _new((B, R, V), f32, dev, stream)
+    _on(_dev(out, "out", f32), "out", dev)
+    if tuple(out.shape) != (B, R, V):
+        raise ValueError(f"out must have shape {(B, R, V)}, got {tuple(out.shape)}")
+    a = PaLogitsArgs(_ptr(logits), _LOGITS_DTYPE[logits.dtype], B, R, NB, V, logits.stride(0) if B > 1 else 0,
+                     logits.stride(1) if R > 1 else 0, _ptr(history), S, _ptr(history_lens), _ptr(prompt_lens),
+                     _ptr(draft), _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens),
+                     _ptr(bias_values), _ptr(mask), _ptr(temperature), _ptr(out))
+    handle, call = _stream_on(stream, dev), getattr(_serving_lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(call(C.byref(a), handle), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(C.byref(a), handle), name)
+    return out
+
+
+def adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None,
+                  history_lens: Optional[torch.Tensor] = None, prompt_lens: Optional[torch.Tensor] = None,
+                  draft: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                  bias_tokens: Optional[torch.Tensor] = None, bias_values: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """pa_adjust_logits: penalties, biases and grammar masks on logits [B, R, V] (rows of any stride) -> fp32
+    [B, R, V]. history int32 [B, S] (prompt tokens, then outputs), draft int32 [B, R - 1], repetition /
+    presence / frequency fp32 [B], bias_tokens / bias_values [B, NB], mask int32 [B, R, ceil(V / 32)]."""
+    return _logits_call("pa_adjust_logits", logits, None, history, history_lens, prompt_lens, draft, repetition,
+                        presence, frequency, bias_tokens, bias_values, mask, out, stream)
+
+
+def token_probs(logits: torch.Tensor, temperature: torch.Tensor, history: Optional[torch.Tensor] = None,
+                history_lens: Optional[torch.Tensor] = None, prompt_lens: Optional[torch.Tensor] = None,
+                draft: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                bias_tokens: Optional[torch.Tensor] = None, bias_values: Optional[torch.Tensor] = None,
+                mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """pa_token_probs: the token distributions of adjusted logits (arguments as adjust_logits; temperature fp32
+    [B], 0 = greedy) -> fp32 [B, R, V], the p of spec_verify."""
+    if temperature is None:
+        raise ValueError("temperature is needed")
+    return _logits_call("pa_token_probs", logits, temperature, history, history_lens, prompt_lens, draft, repetition,
+                        presence, frequency, bias_tokens, bias_values, mask, out, stream)
