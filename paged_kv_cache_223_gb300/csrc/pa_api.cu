@@ -575,7 +575,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
     p.fp8 = c.kv_format == PA_KV_FP8_E4M3;
     DeviceGuard g(c.device);
     if (!g.ok) return PA_ERR_CUDA;
-    return launch_rope_append(p, c.dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_rope_append(p, c.dtype, pool->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // The checks of pa_prefill_packed's sizes, shared with the workspace query.

@@ -161,7 +161,7 @@ cudaError_t launch_wait_selftest(int *status, uint64_t limit_ns, cudaStream_t st
 cudaError_t launch_spec_verify(const float *p, const float *q, const int32_t *draft, const float *u, const float *v,
                                int B, int K, int64_t V, int32_t *out, int32_t *n_out, int *status,
                                cudaStream_t stream);
-cudaError_t launch_rope_append(const RopeParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams &p, int dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_logits(const LogitsParams &p, bool probs, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const int32_t *pairs, int32_t n, void *k_cache, void *v_cache, int64_t vec_per_block,

@@ -107,19 +107,20 @@ def _dev(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> tor
     return t
 
 
-def _on(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, index: int, shape: tuple) -> None:
+    """A contiguous tensor of this type and shape on device `index` (one test of each: this is on every call's path)."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
     """The given stream's handle (a stream of `device`), else that device's current stream."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream must be on {device}, got {stream.device}")
-        return stream.cuda_stream
-    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if stream is None:
+        return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    return stream.cuda_stream
 
 
 def _new(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
@@ -132,18 +133,19 @@ def _new(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch
     return t
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, n: int, heads: Optional[int],
-                d: int) -> None:
-    """Token rows [n, heads, d]: heads and dimensions dense, tokens at any stride of whole 16-byte vectors."""
-    if not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
-    _on(t, name, device)
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
-    dense = t.stride(2) == 1 and (t.shape[1] <= 1 or t.stride(1) == d)
-    if t.numel() > 0 and (not dense or (n > 1 and (t.stride(0) < t.shape[1] * d or t.stride(0) % 8 != 0))):
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, index: int, n: int, heads: int, d: int) -> int:
+    """Token rows [n, heads, d]: heads and dimensions dense, tokens at any stride of whole 16-byte vectors.
+    Returns that stride in elements."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(n, heads, d)} on cuda:{index}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    st, sh, sd = t.stride()
+    if n <= 1:
+        st = heads * d
+    if (sd != 1 or (sh != d and heads > 1) or st < heads * d or st % 8) and t.numel():
         raise ValueError(f"{name} must have dense heads and a token stride of whole 16-byte vectors, got strides "
                          f"{t.stride()}")
+    return st
 
 
 class Rope:
@@ -198,6 +200,8 @@ class PaLogitsArgs(C.Structure):
 
 def _serving_lib() -> C.CDLL:
     global _serving_ready
+    if _serving_ready:
+        return _lib
     L = lib()
     if not _serving_ready:
         P, I32, I64, U64 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64
@@ -360,28 +364,30 @@ class Pool:
         """Rotate q [N, Hq, d] and k [N, Hkv, d] by positions (int32 [N]) and append k, v to the pool's slots
         (pa_rope_append). Rows may be strided over tokens (slices of one projection's output). Returns the
         rotated q [N, Hq, d] (q_out; may be q itself); q None appends only."""
-        hd = (self.geometry[1], self.geometry[3])
-        n = k.shape[0] if k.dim() == 3 else -1
-        for name, t, heads in (("q", q, None), ("k", k, hd[0]), ("v", v, hd[0]), ("q_out", q_out, None)):
-            if t is not None:
-                _token_rows(t, name, self.dtype, self.device, n, heads, hd[1])
-        for name, t, dt in (("positions", positions, torch.int32), ("slot_mapping", slot_mapping, torch.int64)):
-            _on(_dev(t, name, dt), name, self.device)
-            if t.dim() != 1 or t.shape[0] != n:
-                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-        self._check_caches(k_cache, v_cache)
-        hq = 0 if q is None else q.shape[1]
-        if q is None:
-            if q_out is not None:
-                raise ValueError("q_out without q")
-        elif q_out is None:
-            q_out = _new((n, hq, hd[1]), self.dtype, self.device, stream)
-        elif tuple(q_out.shape) != tuple(q.shape):
-            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        row = lambda t: 0 if t is None else t.stride(0) if n > 1 else t.shape[1] * hd[1]  # noqa: E731
+        _, hkv, _, d = self.geometry
+        index, dt = self.device.index, self.dtype
+        n = k.shape[0]
+        ks = _token_rows(k, "k", dt, index, n, hkv, d)
+        vs = _token_rows(v, "v", dt, index, n, hkv, d)
+        _need(positions, "positions", torch.int32, index, (n,))
+        _need(slot_mapping, "slot_mapping", torch.int64, index, (n,))
+        if k_cache is not None or v_cache is not None:
+            self._check_caches(k_cache, v_cache)
+        hq = qs = os = 0
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError(f"q must be [{n}, Hq, {d}], got {tuple(q.shape)}")
+            hq = q.shape[1]
+            qs = _token_rows(q, "q", dt, index, n, hq, d)
+            if q_out is None:
+                q_out, os = _new((n, hq, d), dt, self.device, stream), hq * d
+            else:
+                os = _token_rows(q_out, "q_out", dt, index, n, hq, d)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
         _check(_serving_lib().pa_rope_append(
-            self.handle, rope.handle, _ptr(q), row(q), _ptr(k), row(k), _ptr(v), row(v), _ptr(positions),
-            _ptr(slot_mapping), n, hq, _ptr(q_out), row(q_out), _ptr(k_cache), _ptr(v_cache),
+            self.handle, rope.handle, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+            slot_mapping.data_ptr(), n, hq, _ptr(q_out), os, _ptr(k_cache), _ptr(v_cache),
             _stream_on(stream, self.device)), "pa_rope_append")
         return q_out
 
@@ -394,32 +400,33 @@ class Pool:
         sequence b's newest tokens, their K and V already in the pool. cu_q: int32 [B + 1]. The workspace
         (uint8, packed_workspace() bytes) is allocated for the call unless given; calls that may run at the
         same time need one each."""
-        d = self.geometry[3]
-        for name, t, dt in (("q", q, self.dtype), ("cu_q", cu_q, torch.int32),
-                            ("block_tables", block_tables, torch.int32), ("context_lens", context_lens, torch.int32)):
-            _on(_dev(t, name, dt), name, self.device)
-        if q.dim() != 3 or q.shape[2] != d:
-            raise ValueError(f"q must be [T, Hq, {d}], got {tuple(q.shape)}")
-        if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-            raise ValueError(f"cu_q must be [B + 1], got {tuple(cu_q.shape)}")
-        T, Hq, B = q.shape[0], q.shape[1], cu_q.shape[0] - 1
-        if block_tables.dim() != 2 or block_tables.shape[0] < B:
-            raise ValueError(f"block_tables must be [>= {B}, stride], got {tuple(block_tables.shape)}")
-        if context_lens.dim() != 1 or context_lens.shape[0] < B:
-            raise ValueError(f"context_lens must hold {B} entries, got {tuple(context_lens.shape)}")
+        index, dt = self.device.index, self.dtype
+        if q.dim() != 3 or cu_q.dim() != 1 or cu_q.shape[0] < 1 or block_tables.dim() != 2 or context_lens.dim() != 1:
+            raise ValueError(f"q must be [T, Hq, d], cu_q [B + 1], block_tables [>= B, stride], context_lens [>= B]: got "
+                             f"{tuple(q.shape)}, {tuple(cu_q.shape)}, {tuple(block_tables.shape)}, "
+                             f"{tuple(context_lens.shape)}")
+        (T, Hq, _), B = q.shape, cu_q.shape[0] - 1
+        rows, stride = block_tables.shape
+        lens = context_lens.shape[0]
+        if rows < B or lens < B:
+            raise ValueError(f"block_tables and context_lens must hold {B} sequences, got {rows} and {lens}")
+        _need(q, "q", dt, index, (T, Hq, self.geometry[3]))
+        _need(cu_q, "cu_q", torch.int32, index, (B + 1,))
+        _need(block_tables, "block_tables", torch.int32, index, (rows, stride))
+        _need(context_lens, "context_lens", torch.int32, index, (lens,))
         if out is None:
-            out = _new(q.shape, self.dtype, self.device, stream)
-        _on(_dev(out, "out", self.dtype), "out", self.device)
-        if tuple(out.shape) != tuple(q.shape):
-            raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-        self._check_caches(k_cache, v_cache)
+            out = _new(q.shape, dt, self.device, stream)
+        else:
+            _need(out, "out", dt, index, q.shape)
+        if k_cache is not None or v_cache is not None:
+            self._check_caches(k_cache, v_cache)
         if workspace is None:
-            workspace = _new((self.packed_workspace(T, B, Hq, block_tables.shape[1]),), torch.uint8, self.device,
-                             stream)
-        _on(_dev(workspace, "workspace", torch.uint8), "workspace", self.device)
+            workspace = _new((self.packed_workspace(T, B, Hq, stride),), torch.uint8, self.device, stream)
+        else:
+            _need(workspace, "workspace", torch.uint8, index, (workspace.numel(),))
         _check(_serving_lib().pa_prefill_packed(
-            self.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_q), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), T, B, Hq, float(scale), _ptr(workspace), workspace.numel(), _ptr(out),
+            self.handle, q.data_ptr(), _ptr(k_cache), _ptr(v_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
+            context_lens.data_ptr(), T, B, Hq, float(scale), workspace.data_ptr(), workspace.numel(), out.data_ptr(),
             _stream_on(stream, self.device)), "pa_prefill_packed")
         return out
 
@@ -628,48 +635,60 @@ _LOGITS_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 def _logits_call(name: str, logits: torch.Tensor, temperature: Optional[torch.Tensor], history, history_lens,
                  prompt_lens, draft, repetition, presence, frequency, bias_tokens, bias_values, mask, out,
                  stream) -> torch.Tensor:
-    if not logits.is_cuda or logits.dtype not in _LOGITS_DTYPE:
+    code, index = _LOGITS_DTYPE.get(logits.dtype), logits.get_device()
+    if code is None or index < 0:
         raise ValueError(f"logits must be a CUDA tensor of fp16, bf16 or fp32, got {logits.dtype} on {logits.device}")
     if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
         raise ValueError(f"logits must be [B, R, V], got {tuple(logits.shape)}")
-    if logits.shape[2] > 1 and logits.stride(2) != 1:
+    (B, R, V), (sb, sr, sv) = logits.shape, logits.stride()
+    if sv != 1 and V > 1:
         raise ValueError("logits must be dense over the vocabulary")
-    B, R, V = logits.shape
-    dev = logits.device
-    S = history.shape[1] if history is not None and history.dim() == 2 else 0
-    NB = bias_tokens.shape[1] if bias_tokens is not None and bias_tokens.dim() == 2 else 0
     i32, f32 = torch.int32, torch.float32
-    for n, t, dt, shape in (("temperature", temperature, f32, (B,)), ("history", history, i32, (B, S)),
-                            ("history_lens", history_lens, i32, (B,)), ("prompt_lens", prompt_lens, i32, (B,)),
-                            ("draft", draft, i32, (B, R - 1)), ("repetition", repetition, f32, (B,)),
-                            ("presence", presence, f32, (B,)), ("frequency", frequency, f32, (B,)),
-                            ("bias_tokens", bias_tokens, i32, (B, NB)), ("bias_values", bias_values, f32, (B, NB)),
-                            ("mask", mask, i32, (B, R, (V + 31) // 32))):
-        if t is not None:
-            _on(_dev(t, n, dt), n, dev)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
-    if (history is None) != (history_lens is None):
-        raise ValueError("pass both history and history_lens, or neither")
-    if prompt_lens is not None and history is None:
-        raise ValueError("prompt_lens without history")
-    if (bias_tokens is None) != (bias_values is None):
-        raise ValueError("pass both bias_tokens and bias_values, or neither")
+    S = NB = 0
+    if history is not None:
+        if history.dim() != 2 or history_lens is None:
+            raise ValueError("history must be [B, S], with history_lens")
+        S = history.shape[1]
+        _need(history, "history", i32, index, (B, S))
+        _need(history_lens, "history_lens", i32, index, (B,))
+        if prompt_lens is not None:
+            _need(prompt_lens, "prompt_lens", i32, index, (B,))
+    elif history_lens is not None or prompt_lens is not None:
+        raise ValueError("history_lens or prompt_lens without history")
+    if draft is not None:
+        _need(draft, "draft", i32, index, (B, R - 1))
+    if repetition is not None:
+        _need(repetition, "repetition", f32, index, (B,))
+    if presence is not None:
+        _need(presence, "presence", f32, index, (B,))
+    if frequency is not None:
+        _need(frequency, "frequency", f32, index, (B,))
+    if bias_tokens is not None:
+        if bias_tokens.dim() != 2 or bias_values is None:
+            raise ValueError("bias_tokens must be [B, NB], with bias_values")
+        NB = bias_tokens.shape[1]
+        _need(bias_tokens, "bias_tokens", i32, index, (B, NB))
+        _need(bias_values, "bias_values", f32, index, (B, NB))
+    elif bias_values is not None:
+        raise ValueError("bias_values without bias_tokens")
+    if mask is not None:
+        _need(mask, "mask", i32, index, (B, R, (V + 31) // 32))
+    if temperature is not None:
+        _need(temperature, "temperature", f32, index, (B,))
     if out is None:
-        out = _new((B, R, V), f32, dev, stream)
-    _on(_dev(out, "out", f32), "out", dev)
-    if tuple(out.shape) != (B, R, V):
-        raise ValueError(f"out must have shape {(B, R, V)}, got {tuple(out.shape)}")
-    a = PaLogitsArgs(_ptr(logits), _LOGITS_DTYPE[logits.dtype], B, R, NB, V, logits.stride(0) if B > 1 else 0,
-                     logits.stride(1) if R > 1 else 0, _ptr(history), S, _ptr(history_lens), _ptr(prompt_lens),
-                     _ptr(draft), _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens),
-                     _ptr(bias_values), _ptr(mask), _ptr(temperature), _ptr(out))
-    handle, call = _stream_on(stream, dev), getattr(_serving_lib(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(call(C.byref(a), handle), name)
+        out = _new((B, R, V), f32, logits.device, stream)
     else:
-        with torch.cuda.device(dev):
-            _check(call(C.byref(a), handle), name)
+        _need(out, "out", f32, index, (B, R, V))
+    a = PaLogitsArgs(logits.data_ptr(), code, B, R, NB, V, sb if B > 1 else 0, sr if R > 1 else 0, _ptr(history), S,
+                     _ptr(history_lens), _ptr(prompt_lens), _ptr(draft), _ptr(repetition), _ptr(presence),
+                     _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), _ptr(mask), _ptr(temperature),
+                     out.data_ptr())
+    handle, call = _stream_on(stream, logits.device), getattr(_serving_lib(), name)
+    if index == torch.cuda.current_device():
+        _check(call(a, handle), name)
+    else:
+        with torch.cuda.device(index):
+            _check(call(a, handle), name)
     return out
 
 
