@@ -31,6 +31,7 @@ struct pa_pool {
     cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
     std::mutex mu;
     std::unordered_map<const void *, CUtensorMap> maps;
+    std::unordered_map<const void *, CUtensorMap> block_maps;   // packed prompts: one box per block
 };
 
 struct pa_rope {
@@ -599,9 +600,60 @@ static pa_status packed_params(const pa_pool *pool, int32_t num_tokens, int32_t 
     p.bs = c.block_size;
     p.num_blocks = c.num_blocks;
     p.max_ctx = (int)max_ctx;
+    p.P = 128 / G;
+    // Items behind long contexts are cut along the keys only where the items alone do not fill two rounds of
+    // blocks (the lengths are on the device; num_tokens bounds the items from below), and not into key ranges
+    // of a few tiles.
+    const int64_t least_items = ((int64_t)num_tokens + 2 * p.P - 1) / (2 * p.P) * c.num_kv_heads;
+    p.max_units = least_items < 2 * pool->sm_count && max_ctx > 4 * 128 ? 2 * pool->sm_count : 0;
     p.status = pool->status;
     p.wait_ns = pool->wait_ns;
     return PA_OK;
+}
+
+// The pool as a 4-D tensor for copies of whole blocks: [8 tokens x 64 dimensions], the dimension halves, groups of
+// eight tokens. One box is a block's rows of one KV head, 128-byte swizzled.
+static pa_status block_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
+    std::lock_guard<std::mutex> lk(pool->mu);
+    auto it = pool->block_maps.find(cache);
+    if (it != pool->block_maps.end()) {
+        *out = it->second;
+        return PA_OK;
+    }
+    auto fn = encode_fn();
+    if (!fn) return PA_ERR_CUDA;
+    const pa_pool_config &c = pool->cfg;
+    const cuuint64_t row = (cuuint64_t)c.head_dim * 2, groups = (cuuint64_t)c.num_blocks * c.num_kv_heads * c.block_size / 8;
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)c.head_dim / 64, groups};
+    cuuint64_t strides[3] = {row, 128, 8 * row};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)c.head_dim / 64, (cuuint32_t)c.block_size / 8};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUtensorMap m;
+    if (fn(&m, c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+           const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PA_ERR_CUDA;
+    if (pool->block_maps.size() > 4096) pool->block_maps.clear();
+    pool->block_maps.emplace(cache, m);
+    *out = m;
+    return PA_OK;
+}
+
+// q [num_tokens, Hq, head_dim] for boxes of P positions x G heads x 64 dimensions.
+static pa_status q_map(const PromptParams &p, int dtype, int head_dim, CUtensorMap *out) {
+    auto fn = encode_fn();
+    if (!fn) return PA_ERR_CUDA;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)p.Hq, (cuuint64_t)p.num_tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)p.Hq * head_dim * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.P};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(out, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(p.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
@@ -610,7 +662,7 @@ pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, i
     PromptParams p;
     const pa_status st = packed_params(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, p);
     if (st != PA_OK) return st;
-    *bytes = 256;
+    *bytes = 256 + (uint64_t)p.max_units * (PROMPT_ITEM_BYTES + prompt_slot_bytes(pool->cfg.head_dim));
     return PA_OK;
 }
 
@@ -645,10 +697,21 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
     p.cu_q = cu_q;
     p.context_lens = context_lens;
     p.scale_log2 = scale * 1.4426950408889634f;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_total = reinterpret_cast<int *>(ws);
+    p.ws_items = reinterpret_cast<PromptItem *>(ws + 256);
+    p.ws_slots = ws + 256 + (size_t)p.max_units * PROMPT_ITEM_BYTES;
     DeviceGuard g(c.device);
     if (!g.ok) return PA_ERR_CUDA;
-    return launch_prompt(p, c.dtype, c.head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                                   : PA_ERR_CUDA;
+    CUtensorMap tmq, tmk, tmv;
+    pa_status ms;
+    if ((ms = q_map(p, c.dtype, c.head_dim, &tmq)) != PA_OK || (ms = block_map(pool, k_cache, &tmk)) != PA_OK ||
+        (ms = block_map(pool, v_cache, &tmv)) != PA_OK)
+        return ms;
+    return launch_prompt(p, c.dtype, c.head_dim, tmq, tmk, tmv, pool->sm_count, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) {

@@ -95,7 +95,12 @@ struct PromptParams {
     int num_tokens, num_seqs;
     int Hq, Hkv, G;
     int bs, num_blocks;
-    int max_ctx;                // longest context the tables (and the pool's limit) hold
+    int max_ctx;                // longest context the tables hold
+    int P;                      // positions of a row tile: 128 / G
+    int max_units;              // units that the workspace holds states for; 0: nothing is cut
+    int *ws_total;              // workspace: units of the call, their items, their states
+    struct PromptItem *ws_items;
+    uint8_t *ws_slots;
     float scale_log2;
     uint64_t wait_ns;
 };
@@ -162,7 +167,10 @@ cudaError_t launch_spec_verify(const float *p, const float *q, const int32_t *dr
                                int B, int K, int64_t V, int32_t *out, int32_t *n_out, int *status,
                                cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams &p, int dtype, int sm_count, cudaStream_t stream);
-cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const CUtensorMap &tmq,
+                          const CUtensorMap &tmk, const CUtensorMap &tmv, int sm_count, cudaStream_t stream);
+size_t prompt_slot_bytes(int head_dim);
+constexpr int PROMPT_ITEM_BYTES = 32;   // of the workspace per unit, beside its state
 cudaError_t launch_logits(const LogitsParams &p, bool probs, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const int32_t *pairs, int32_t n, void *k_cache, void *v_cache, int64_t vec_per_block,
                                int32_t num_blocks, int *status, int sm_count, cudaStream_t stream);

@@ -1,65 +1,792 @@
-// prompt.cu -- causal attention of packed prompts of different lengths through the block tables.
+// prompt.cu -- causal attention of packed prompts of different lengths through the block tables, on the
+// 5th-generation tensor cores (tcgen05.mma, accumulators in tensor memory).
 //
 // Sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] of q; row i of them sits at position
 // p = context_lens[b] - n_b + i and attends to tokens 0..p:
-//   out = sum_t softmax_t(scale q . K_t) V_t.
+//   out = sum_t softmax_t(scale q . K_t) V_t,
+// one pass over the keys with the running maximum and sum of the softmax.
 //
-// Simple form: one warp per (token, query head), one pass over its keys with the running maximum and
-// sum of the softmax.
+// Work. A query "row" is one (position, query head of the KV group) pair. A row tile holds the rows of
+// P = 128 / G positions (G query heads per KV head), position-major, so that all heads of a group share
+// one read of K and V; an item is two row tiles of one sequence and KV head. Items behind long contexts
+// are cut along the keys into units where there are too few to fill the GPU, and a second kernel joins
+// the units' (O, max, sum). The lengths live on the device, so every block of the persistent grid
+// computes the same plan (units per sequence, cut length) from them and takes every gridDim.x-th unit, a
+// sequence's longest first, the direction alternating from round to round so that descending lengths
+// even out. A captured call follows lengths that change between replays.
+//
+// One block per SM, 384 threads:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1: one row per thread = one tensor-memory lane
+//   warp 8, 11       K and V loads: one TMA copy per cache block, [8-key groups][64-dimension halves]
+//                    [8 keys][128 bytes] in shared memory, so that a whole block of tokens is one copy and
+//                    8-key groups stay a constant stride apart in the matrix descriptors
+//   warp 9           one thread issues every MMA: per key tile and row tile O += P V (P from tensor
+//                    memory, V MN-major), then S = Q K^T into the columns P came from
+//   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
+//                    [P positions][G heads][64 dimensions])
+// The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
+// issued, while the last softmax and the output of this one are still at work.
+//
+// Masks. Keys behind a row's position are excluded from its maximum and sum by selection, whatever the
+// scores are. Their weight is 0 in P V, but 0 times a value that is no number is none either: V rows behind
+// the unit's last position are zeroed, and the V tiles in which only some rows see a key are scanned; where
+// one holds a NaN or infinity, those words are zeroed and the rows that do see them get them added to their
+// outputs (each seen value has a weight > 0) in a slow path that real data never takes.
+//
+// Roundings. S, the softmax statistics and O are fp32. P is rounded once to the model's 16-bit type, as the
+// product with V takes it (half a step per weight, averaged over the keys: of the size of the output's own
+// rounding); the sum is of the unrounded weights. Keeping P in two 16-bit parts, as pa_prefill does for
+// bf16, costs half of the P V rate.
+#include <type_traits>
+
 #include "pa_device.cuh"
 
 namespace pa {
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) prompt_simple_kernel(const PromptParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    if (w >= (int64_t)p.num_tokens * p.Hq) return;
-    const int tok = (int)(w / p.Hq), h = (int)(w % p.Hq), g = h / p.G;
-    int b = 0;
-    while (b < p.num_seqs && __ldg(p.cu_q + b + 1) <= tok) ++b;
-    if (b == p.num_seqs || __ldg(p.cu_q + b) > tok) return;          // behind the last sequence
-    const int n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
-    int L = __ldg(p.context_lens + b);
-    if (L < n || L > p.max_ctx) {
-        if (lane == 0) set_status(p.status, STATUS_BOUNDS);
-        L = L > p.max_ctx ? p.max_ctx : L;
-    }
-    const int last = L - n + (tok - __ldg(p.cu_q + b));
-    const T *q = static_cast<const T *>(p.q) + w * D + lane * E;
-    float qv[E], o[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) qv[e] = (float)q[e], o[e] = 0.f;
-    for (int t = 0; t <= last; ++t) {
-        int id = __ldg(p.block_tables + (int64_t)b * p.stride + t / p.bs);
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) set_status(p.status, STATUS_BOUNDS);
-            id = 0;
-        }
-        const int64_t row = (((int64_t)id * p.Hkv + g) * p.bs + t % p.bs) * D + lane * E;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += qv[e] * (float)static_cast<const T *>(p.k_cache)[row + e];
-        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), a = exp2f(m - mn), x = exp2f(s - mn);
-        l = l * a + x;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + x * (float)static_cast<const T *>(p.v_cache)[row + e];
-        m = mn;
-    }
-    T *out = static_cast<T *>(p.out) + w * D + lane * E;
-    for (int e = 0; e < E; ++e) out[e] = (T)(l > 0.f ? o[e] / l : o[e]);
+constexpr int PR_BM = 128, PR_BN = 128;               // rows of a row tile, keys of a key tile
+constexpr int PR_THREADS = 384;
+constexpr int PR_K_WARP = 8, PR_SCHED_WARP = 10, PR_V_WARP = 11;    // warp 9: MMA
+// Register split: 2 x 128 x 216 + 128 x 72 = 384 x 168, the launch's registers.
+constexpr uint32_t PR_REGS_LAUNCH = 168, PR_REGS_SOFTMAX = 216, PR_REGS_OTHER = 72;
+static_assert(2 * 128 * PR_REGS_SOFTMAX + 128 * PR_REGS_OTHER <= PR_THREADS * PR_REGS_LAUNCH, "register split");
+constexpr int PR_UNITS = 4;                           // ring of decoded units
+constexpr float PR_RESCALE_LOG2 = 8.f;                // stale-maximum headroom (P <= 2^8)
+constexpr uint32_t PR_TMEM_COLS = 512;                // row tile t: S/P at 256 t, O at 256 t + 128
+
+template <int D>
+struct PromptShape {
+    static constexpr int HALVES = D / 64;
+    static constexpr int Q_BYTES = PR_BM * D * 2;     // HALVES x [128 rows x 128 B]
+    static constexpr int KV_BYTES = PR_BN * D * 2;    // 16 groups x HALVES x [8 keys x 128 B]
+    static constexpr int GROUP_BYTES = 1024 * HALVES;
+    static constexpr int KST = D == 128 ? 2 : 4, VST = KST;
+    static constexpr int OFF_K = 2 * Q_BYTES;
+    static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
+    static constexpr int OFF_STAGE = OFF_V + VST * KV_BYTES;          // 2 KB per softmax warp
+    static constexpr int OFF_PREF = OFF_STAGE + 8 * 2048;
+    static constexpr int OFF_UNITS = OFF_PREF + (PA_PACKED_MAX_SEQS + 4) * 4;
+    static constexpr int OFF_BAR = OFF_UNITS + PR_UNITS * 64;
+    static constexpr int NBAR = 2 * KST + 2 * VST + 12 + 2 * PR_UNITS + 2;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = 1024 + OFF_MISC + 32;
+    static_assert(SMEM <= (int)MAX_SMEM_PER_CTA, "shared memory");
+};
+
+struct alignas(16) PromptUnit {
+    int valid;                 // 0: no more units
+    int b, g;
+    int tok0;                  // row of q of the item's first position
+    int npos;                  // the sequence's positions from there on
+    int pos0;                  // that position
+    int kt0;                   // first key tile
+    int n0, n1;                // key tiles of row tile 0 and 1
+    int slot;                  // where the unit's state goes; -1: the output itself
+    int poison;                // V tiles of the unit held values that are no numbers
+    int pad[5];
+};
+static_assert(sizeof(PromptUnit) == 64, "unit ring");
+
+// Header of the workspace, written by the main kernel for the joining one.
+struct PromptItem {
+    int tok0, npos, g;
+    int splits0, splits1;      // units of row tile 0 and 1 (0: nothing to join)
+};
+
+size_t prompt_slot_bytes(int head_dim) { return (size_t)256 * (head_dim + 2) * 4; }
+
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite_probe(uint32_t x, uint32_t acc) {
+    // x * 0 + acc, two values at once: stays 0 while every x is finite
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ bool is_nonfinite16(uint32_t x) {
+    constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    return (x & E) == E;
 }
 
-cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(((int64_t)p.num_tokens * p.Hq + 3) / 4);
-    if (dtype == PA_FP16) {
-        if (head_dim == 64) prompt_simple_kernel<__half, 64><<<grid, 128, 0, stream>>>(p);
-        else prompt_simple_kernel<__half, 128><<<grid, 128, 0, stream>>>(p);
-    } else {
-        if (head_dim == 64) prompt_simple_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
-        else prompt_simple_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
+template <int RANK>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar,
+                                         uint64_t policy) {
+    if constexpr (RANK == 3)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+            : "memory");
+}
+
+// New tokens and context of sequence b, clamped to what q and the tables hold (flagged where `status` is given).
+__device__ __forceinline__ void sequence(const PromptParams &p, int b, int &first, int &n, int &L, int *status) {
+    first = __ldg(p.cu_q + b);
+    int end = __ldg(p.cu_q + b + 1);
+    L = __ldg(p.context_lens + b);
+    const bool bad = first < 0 || end < first || end > p.num_tokens || L > p.max_ctx || L < end - first;
+    if (bad && status) set_status(status, STATUS_BOUNDS);
+    first = first < 0 ? 0 : (first > p.num_tokens ? p.num_tokens : first);
+    end = end > p.num_tokens ? p.num_tokens : end;
+    n = end > first ? end - first : 0;
+    L = L < 0 ? 0 : (L > p.max_ctx ? p.max_ctx : L);
+}
+
+// The plan, by one warp: key tiles per unit, and the running number of units (of one KV head) per sequence.
+// Costs are in key tiles of work: a unit costs PLAN_UNIT more than its tiles, joining PLAN_JOIN.
+__device__ int make_plan(const PromptParams &p, int *pref, int lane) {
+    constexpr int PLAN_UNIT = 3, PLAN_JOIN = 4, PLAN_MIN = 4, WHOLE = 1 << 24;
+    const int rows2 = 2 * p.P, grid = (int)gridDim.x;
+    int chunk = WHOLE;
+    if (p.max_units > 0) {
+        int items = 0, longest = 0;
+        int64_t tiles = 0;
+        for (int b = lane; b < p.num_seqs; b += 32) {
+            int first, n, L;
+            sequence(p, b, first, n, L, nullptr);
+            if (n == 0) continue;
+            const int it = (n + rows2 - 1) / rows2, nt = (L + PR_BN - 1) / PR_BN;
+            const int e0 = (L - n + (n < rows2 ? n : rows2) + PR_BN - 1) / PR_BN;
+            items += it;
+            longest = nt > longest ? nt : longest;
+            tiles += (int64_t)it * (nt + (e0 > 0 ? e0 : 0)) / 2;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        }
+        // one candidate per lane: the longest context in k units
+        const int k = lane < 16 ? lane + 1 : 16 + (lane - 15) * 9;
+        int c = (longest + k - 1) / k;
+        if (c < PLAN_MIN) c = PLAN_MIN;
+        if (k == 1) c = WHOLE;
+        int64_t units = 0;
+        if ((int64_t)items * p.Hkv < 2 * grid) {
+            for (int b = 0; b < p.num_seqs; ++b) {
+                int first, n, L;
+                sequence(p, b, first, n, L, nullptr);
+                const int nt = (L + PR_BN - 1) / PR_BN;
+                units += (int64_t)((n + rows2 - 1) / rows2) * (nt > c ? (nt + c - 1) / c : 1);
+            }
+            units *= p.Hkv;
+            const int64_t unit = c < longest ? c : longest;
+            int64_t cost = units <= grid ? 2 * (unit + PLAN_UNIT)
+                                         : 2 * ((tiles * p.Hkv + units * PLAN_UNIT) / grid) + unit;
+            if (k > 1) cost += 2 * PLAN_JOIN;
+            if (k > 1 && (units > p.max_units || longest <= PLAN_MIN)) cost = (int64_t)1 << 40;
+            int64_t best = cost * 64 + lane;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+            chunk = __shfl_sync(0xffffffffu, c, (int)(best & 31));
+        }
     }
-    return cudaGetLastError();
+    int total = 0;
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        int first = 0, n = 0, L = 0;
+        if (b < p.num_seqs) sequence(p, b, first, n, L, nullptr);
+        const int nt = (L + PR_BN - 1) / PR_BN;
+        int x = (n + rows2 - 1) / rows2 * (nt > chunk ? (nt + chunk - 1) / chunk : 1);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (b < p.num_seqs) pref[b + 1] = total + x;
+        total += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) pref[0] = 0;
+    return chunk;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(PR_THREADS, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const PromptParams p) {
+    using S = PromptShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t base = (raw_u32 + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_u32);
+    const uint32_t k_full = base + S::OFF_BAR, k_empty = k_full + S::KST * 8;
+    const uint32_t v_full = k_empty + S::KST * 8, v_empty = v_full + S::VST * 8;
+    const uint32_t q_full = v_empty + S::VST * 8, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, o_free = o_done + 16;
+    const uint32_t u_full = o_free + 16, u_empty = u_full + PR_UNITS * 8;
+    const uint32_t v_raw = u_empty + PR_UNITS * 8, drain = v_raw + 8;
+    PromptUnit *units = reinterpret_cast<PromptUnit *>(smem + S::OFF_UNITS);
+    int *pref = reinterpret_cast<int *>(smem + S::OFF_PREF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_chunk = reinterpret_cast<int *>(tmem_slot + 2);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), PR_TMEM_COLS);
+    if (tid == 64) {
+        for (int s = 0; s < S::KST; ++s) mbar_init(k_full + s * 8, 1), mbar_init(k_empty + s * 8, 1);
+        for (int s = 0; s < S::VST; ++s) mbar_init(v_full + s * 8, 1), mbar_init(v_empty + s * 8, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(q_full + t * 8, 1);
+            mbar_init(q_empty + t * 8, 1);
+            mbar_init(s_full + t * 8, 1);
+            mbar_init(p_full + t * 8, PR_BM);
+            mbar_init(o_done + t * 8, 1);
+            mbar_init(o_free + t * 8, PR_BM);
+        }
+        for (int s = 0; s < PR_UNITS; ++s) {
+            mbar_init(u_full + s * 8, 1);
+            mbar_init(u_empty + s * 8, 11);           // K, V and MMA warps, 8 softmax warps
+        }
+        mbar_init(v_raw, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        const int c = make_plan(p, pref, lane);
+        if (lane == 0) *s_chunk = c;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int chunk = *s_chunk;
+
+    // A bounded wait that also ends when another role gave up.
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t i = 1;; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((i & 63u) == 0) {
+                if (*abort_flag) return false;
+                if (global_timer_ns() - t0 > p.wait_ns) {
+                    *abort_flag = 1;
+                    return false;
+                }
+            }
+        }
+    };
+
+    if (warp >= PR_K_WARP) {
+        setmaxnreg_dec<PR_REGS_OTHER>();
+        if (warp == PR_SCHED_WARP) {
+            // ------------------------------------------------------------ units and their Q tiles
+            if (lane == 0) {
+                const int total = pref[p.num_seqs] * p.Hkv, grid = (int)gridDim.x, rows2 = 2 * p.P;
+                const uint64_t policy = l2_policy_evict_first();
+                int published = 0, qn[2] = {0, 0};
+                bool ok = true;
+                if (p.max_units > 0 && blockIdx.x == 0) *p.ws_total = total;
+                for (int round = 0; ok; ++round) {
+                    const int u = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                    PromptUnit un = {};
+                    if (u < total && round * (int64_t)grid < total) {
+                        const int w = u / p.Hkv;
+                        int lo = 0, hi = p.num_seqs;  // pref[lo] <= w < pref[hi]
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) >> 1;
+                            if (pref[mid] <= w) lo = mid;
+                            else hi = mid;
+                        }
+                        int first, n, L;
+                        sequence(p, lo, first, n, L, p.status);
+                        const int items = (n + rows2 - 1) / rows2, nt = (L + PR_BN - 1) / PR_BN;
+                        const int splits = nt > chunk ? (nt + chunk - 1) / chunk : 1;
+                        const int r = w - pref[lo], i = items - 1 - r / splits, s = r % splits;
+                        un.valid = 1;
+                        un.b = lo;
+                        un.g = u - w * p.Hkv;
+                        un.tok0 = first + i * rows2;
+                        un.npos = n - i * rows2;
+                        un.pos0 = L - n + i * rows2;
+                        // key tiles of each row tile: up to its last position
+                        const int end0 = un.pos0 + min(un.npos, p.P), end1 = un.npos > p.P ? un.pos0 + min(un.npos, rows2) : 0;
+                        const int e0 = end0 > 0 ? (end0 + PR_BN - 1) / PR_BN : 0, e1 = end1 > 0 ? (end1 + PR_BN - 1) / PR_BN : 0;
+                        const int s0 = max(1, (e0 + chunk - 1) / chunk), s1 = (e1 + chunk - 1) / chunk;
+                        un.kt0 = s * chunk;
+                        un.n0 = max(0, min(e0 - un.kt0, chunk));
+                        un.n1 = max(0, min(e1 - un.kt0, chunk));
+                        const bool cut = max(s0, s1) > 1;
+                        un.slot = cut ? u : -1;
+                        if (u < p.max_units) {        // every unit's, where something may be cut
+                            const bool join = cut && s == 0;
+                            p.ws_items[u] = PromptItem{un.tok0, un.npos, un.g, join ? s0 : 0, join ? s1 : 0};
+                        }
+                        if (s > 0 && un.n0 == 0 && un.n1 == 0) continue;      // an early item of a cut sequence
+                    } else if (u < total || round * (int64_t)grid < total) {
+                        continue;                     // the last, partial round: the next one ends the list
+                    }
+                    const int st = published % PR_UNITS;
+                    if (published >= PR_UNITS && !(ok = wait(u_empty + st * 8, (uint32_t)(published / PR_UNITS - 1) & 1u)))
+                        break;
+                    units[st] = un;
+                    mbar_arrive(u_full + st * 8);
+                    ++published;
+                    if (!un.valid) break;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if ((t ? un.n1 : un.n0) == 0) continue;
+                        if (qn[t] > 0 && !(ok = wait(q_empty + t * 8, (uint32_t)(qn[t] - 1) & 1u))) break;
+                        mbar_arrive_expect_tx(q_full + t * 8, p.P * p.G * D * 2);
+#pragma unroll
+                        for (int h = 0; h < S::HALVES; ++h)
+                            tma_load<3>(base + t * S::Q_BYTES + h * (PR_BM * 128), &tmq, h * 64, un.g * p.G,
+                                        un.tok0 + t * p.P, 0, q_full + t * 8, policy);
+                        ++qn[t];
+                    }
+                }
+                // after a wait that ran out: no copy may land in shared memory that the block has given up
+                if (!ok)
+                    for (int t = 0; t < 2; ++t)
+                        if (qn[t] > 0) mbar_wait_bounded(q_full + t * 8, (uint32_t)(qn[t] - 1) & 1u, p.wait_ns);
+            }
+        } else if (warp == PR_K_WARP || warp == PR_V_WARP) {
+            // ------------------------------------------------------------ K or V tiles
+            const bool is_v = warp == PR_V_WARP;
+            const int nst = is_v ? S::VST : S::KST;
+            const uint32_t full0 = is_v ? v_full : k_full, empty0 = is_v ? v_empty : k_empty;
+            const uint32_t ring = base + (is_v ? S::OFF_V : S::OFF_K);
+            const CUtensorMap *map = is_v ? &tmv : &tmk;
+            const uint64_t policy = l2_policy_evict_last();   // other row tiles read it again
+            const int per_tile = PR_BN / p.bs;                // cache blocks per key tile
+            int issued = 0, raw = 0;
+            bool ok = true, to_raw = false;
+            for (int c = 0; ok; ++c) {
+                const int st_u = c % PR_UNITS;
+                ok = __all_sync(0xffffffffu, wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u));
+                if (!ok) break;
+                const PromptUnit &un = units[st_u];
+                const int valid = un.valid, b = un.b, g = un.g, kt0 = un.kt0, nt = max(un.n0, un.n1), pos0 = un.pos0;
+                const int seen = un.pos0 + min(un.npos, 2 * p.P);             // keys that any row of the unit sees
+                __syncwarp();
+                if (!valid) break;
+                const int32_t *table = p.block_tables + (int64_t)b * p.stride;
+                auto lookup = [&](int j) -> int {
+                    const int e = (kt0 + j) * per_tile + lane;
+                    return lane < per_tile && e * p.bs < seen ? __ldg(table + e) : 0;
+                };
+                int id_next = nt > 0 ? lookup(0) : 0;
+                for (int j = 0; j < nt; ++j) {
+                    const int st = issued % nst;
+                    if (issued >= nst) {
+                        ok = __all_sync(0xffffffffu, wait(empty0 + st * 8, (uint32_t)(issued / nst - 1) & 1u));
+                        if (!ok) break;
+                    }
+                    int id = id_next;
+                    if (j + 1 < nt) id_next = lookup(j + 1);
+                    const int t0 = (kt0 + j) * PR_BN, left = seen - t0;       // > 0
+                    const int nblk = min(per_tile, (left + p.bs - 1) / p.bs);
+                    // some row does not see some key of this tile: V is looked over before it is released
+                    const bool look = is_v && t0 + PR_BN - 1 > pos0;
+                    const uint32_t bar = look ? v_raw : full0 + st * 8, dst = ring + st * S::KV_BYTES;
+                    to_raw = look;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, nblk * p.bs * D * 2);
+                    __syncwarp();
+                    if (lane < nblk) {
+                        if (id < 0 || id >= p.num_blocks) {
+                            set_status(p.status, STATUS_BOUNDS);
+                            id = 0;
+                        }
+                        tma_load<4>(dst + lane * (p.bs / 8) * S::GROUP_BYTES, map, 0, 0, 0,
+                                    (id * p.Hkv + g) * (p.bs / 8), bar, policy);
+                    }
+                    ++issued;
+                    if (!look) continue;
+                    ok = __all_sync(0xffffffffu, wait(v_raw, (uint32_t)raw & 1u));
+                    if (!ok) break;
+                    ++raw;
+                    uint8_t *tile = smem + S::OFF_V + st * S::KV_BYTES;
+                    // rows behind the last position seen: other words of the pool, or what the stage held before.
+                    // Each 128-byte line is one key's half: [group][half][key in group]
+                    uint32_t acc = 0u;
+                    const int nline = PR_BN * S::HALVES;
+                    for (int l0 = 0; l0 < nline; l0 += 32) {                  // a line per lane and round
+                        const int l = l0 + lane;
+                        const int key = l / (8 * S::HALVES) * 8 + (l & 7);
+                        uint4 *line = reinterpret_cast<uint4 *>(tile + l * 128);
+                        if (key >= left) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) line[(i + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 w = line[(i + lane) & 7];
+                                acc = nonfinite_probe<T>(w.x, acc);
+                                acc = nonfinite_probe<T>(w.y, acc);
+                                acc = nonfinite_probe<T>(w.z, acc);
+                                acc = nonfinite_probe<T>(w.w, acc);
+                            }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, (acc & 0x7FFF7FFFu) != 0u)) {
+                        for (int l = lane; l < nline; l += 32) {
+                            uint16_t *w = reinterpret_cast<uint16_t *>(tile + l * 128);
+                            for (int i = 0; i < 64; ++i)
+                                if (is_nonfinite16<T>(w[i])) w[i] = 0;
+                        }
+                        if (lane == 0) units[st_u].poison = 1;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full0 + st * 8);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(u_empty + st_u * 8);
+            }
+            if (!ok) {                                // copies still in flight land before the block ends
+                for (int i = issued > nst ? issued - nst : 0; i < issued - (to_raw ? 1 : 0); ++i)
+                    mbar_wait_bounded(full0 + (i % nst) * 8, (uint32_t)(i / nst) & 1u, p.wait_ns);
+                if (to_raw) mbar_wait_bounded(v_raw, (uint32_t)raw & 1u, p.wait_ns);
+            }
+        } else {
+            // ------------------------------------------------------------ MMA issue (lane 0)
+            if (lane == 0) {
+                const uint32_t idesc_s = umma_idesc<T>(PR_BM, PR_BN, false);
+                const uint32_t idesc_o = umma_idesc<T>(PR_BM, D, true);
+                const uint64_t dq0 = umma_desc_sw128(base, 16, 1024);
+                const uint64_t dk0 = umma_desc_sw128(base + S::OFF_K, 16, S::GROUP_BYTES);
+                const uint64_t dv0 = umma_desc_sw128(base + S::OFF_V, 1024, S::GROUP_BYTES);
+                int kc = 0, vc = 0, v_seen = 0;       // K tiles, V tiles taken; V tiles waited for
+                int qc[2] = {0, 0}, pc[2] = {0, 0}, oc[2] = {0, 0};
+                bool pend[2] = {false, false}, pfirst[2] = {false, false}, plast[2] = {false, false};
+                bool ok = true, held = false;         // held: the V tile vc - 1 is not released yet
+                // O_t += P_t V of the step before
+                auto flush = [&](int t) -> bool {
+                    if (!pend[t]) return true;
+                    const int st = (vc - 1) % S::VST;
+                    if (v_seen < vc) {
+                        if (!wait(v_full + st * 8, (uint32_t)((vc - 1) / S::VST) & 1u)) return false;
+                        v_seen = vc;
+                    }
+                    if (!wait(p_full + t * 8, (uint32_t)pc[t] & 1u)) return false;
+                    ++pc[t];
+                    if (pfirst[t]) {                  // the output of the unit before has left tensor memory
+                        if (oc[t] > 0 && !wait(o_free + t * 8, (uint32_t)(oc[t] - 1) & 1u)) return false;
+                        ++oc[t];
+                    }
+                    tc_fence_after();
+                    const uint64_t dv = dv0 + (uint64_t)(st * (S::KV_BYTES >> 4));
+                    const uint32_t pt = tmem + t * 256, ot = pt + 128;
+#pragma unroll
+                    for (int ks = 0; ks < PR_BN / 16; ++ks)
+                        umma_f16_tmem_a(ot, pt + ks * 8, dv + (uint64_t)((ks * 2 * S::GROUP_BYTES) >> 4), idesc_o,
+                                        ks > 0 || !pfirst[t] ? 1u : 0u);
+                    if (plast[t]) umma_commit(o_done + t * 8);
+                    pend[t] = false;
+                    return true;
+                };
+                auto issue_s = [&](int t) {           // S_t = Q_t K^T
+                    const uint64_t dk = dk0 + (uint64_t)((kc % S::KST) * (S::KV_BYTES >> 4));
+                    const uint64_t dq = dq0 + (uint64_t)(t * (S::Q_BYTES >> 4));
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_f16(tmem + t * 256, dq + (uint64_t)(((ks >> 2) * (PR_BM * 128) + (ks & 3) * 32) >> 4),
+                                 dk + (uint64_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+                    umma_commit(s_full + t * 8);
+                };
+                for (int c = 0; ok; ++c) {
+                    const int st_u = c % PR_UNITS;
+                    if (!(ok = wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u))) break;
+                    const int valid = units[st_u].valid, n0 = units[st_u].n0, n1 = units[st_u].n1;
+                    if (!valid) break;
+                    mbar_arrive(u_empty + st_u * 8);
+                    const int nt = max(n0, n1);
+                    for (int j = 0; j < nt; ++j) {
+                        if (!(ok = flush(0))) break;
+                        if (!(ok = wait(k_full + (kc % S::KST) * 8, (uint32_t)(kc / S::KST) & 1u))) break;
+                        if (j < n0) {
+                            if (j == 0) {
+                                if (!(ok = wait(q_full, (uint32_t)qc[0] & 1u))) break;
+                                ++qc[0];
+                            }
+                            issue_s(0);
+                            if (j == n0 - 1) umma_commit(q_empty);
+                        }
+                        if (!(ok = flush(1))) break;
+                        if (held) umma_commit(v_empty + ((vc - 1) % S::VST) * 8);
+                        if (j < n1) {
+                            if (j == 0) {
+                                if (!(ok = wait(q_full + 8, (uint32_t)qc[1] & 1u))) break;
+                                ++qc[1];
+                            }
+                            issue_s(1);
+                            if (j == n1 - 1) umma_commit(q_empty + 8);
+                        }
+                        umma_commit(k_empty + (kc % S::KST) * 8);
+                        ++kc;
+                        ++vc;
+                        held = true;
+                        pend[0] = j < n0;
+                        pend[1] = j < n1;
+                        pfirst[0] = pfirst[1] = j == 0;
+                        plast[0] = j == n0 - 1;
+                        plast[1] = j == n1 - 1;
+                    }
+                }
+                if (ok) ok = flush(0) && flush(1);
+                if (!ok) {
+                    umma_commit(drain);
+                    mbar_wait_bounded(drain, 0u, p.wait_ns);
+                }
+            }
+        }
+    } else {
+        setmaxnreg_inc<PR_REGS_SOFTMAX>();
+        // ---------------------------------------------------------------- softmax of row tile t
+        const int t = tid >> 7, r = tid & (PR_BM - 1);
+        const int rp = r / p.G, rh = r - rp * p.G;    // position and head of this thread's row
+        const bool in_tile = r < p.P * p.G;
+        const uint32_t tmem_s = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16), tmem_o = tmem_s + 128;
+        uint8_t *stage = smem + S::OFF_STAGE + warp * 2048;
+        int sc = 0, oc = 0;
+        bool ok = true;
+        for (int c = 0; ok; ++c) {
+            const int st_u = c % PR_UNITS;
+            ok = __all_sync(0xffffffffu, wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u));
+            if (!ok || !units[st_u].valid) break;
+            const PromptUnit &un = units[st_u];
+            const int nt = t ? un.n1 : un.n0, key0 = un.kt0 * PR_BN;
+            const bool live = in_tile && t * p.P + rp < un.npos;
+            const int lim = live ? un.pos0 + t * p.P + rp : 0x7fffffff;      // last key this row sees
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j) {
+                ok = __all_sync(0xffffffffu, wait(s_full + t * 8, (uint32_t)sc & 1u));
+                if (!ok) break;
+                ++sc;
+                tc_fence_after();
+                float sv[PR_BN];
+                tmem_ld_cols(tmem_s, sv);
+                const int t0 = key0 + j * PR_BN;
+                float m8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
+                if (t0 + PR_BN - 1 > lim) {
+#pragma unroll
+                    for (int i = 0; i < PR_BN; ++i) sv[i] = t0 + i <= lim ? sv[i] : -INFINITY;
+                }
+                // raw-score maximum (the scale is positive, so it commutes with it)
+#pragma unroll
+                for (int i = 0; i < PR_BN; ++i) m8[i & 7] = fmaxf(m8[i & 7], sv[i]);
+                const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                       fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mx > m_ref + PR_RESCALE_LOG2 || (m_ref == -INFINITY && mx > -INFINITY)) {
+                    alpha = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
+                    m_ref = mx;
+                    rescale = true;
+                }
+                // P(j-1) V was issued before S(j), so the commit of S(j) covers it: O is at rest
+                if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float a[32];
+                        tmem_ld32(tmem_o + c0, a);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) a[i] *= alpha;
+                        tmem_st32(tmem_o + c0, a);
+                    }
+                }
+                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                float r8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r8[i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < PR_BN; ++i) {
+                    sv[i] = ex2_approx(fmaf(sv[i], p.scale_log2, nm));
+                    r8[i & 7] += sv[i];
+                }
+                l = l * alpha + ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = pack2<T>(sv[64 * h + 2 * i], sv[64 * h + 2 * i + 1]);
+                    tmem_st32_raw(tmem_s + 32 * h, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + t * 8);
+            }
+            if (!ok) break;
+            float o[D];
+            if (nt > 0) {
+                ok = __all_sync(0xffffffffu, wait(o_done + t * 8, (uint32_t)oc & 1u));
+                if (!ok) break;
+                ++oc;
+                tc_fence_after();
+                tmem_ld_cols(tmem_o, o);
+                tc_fence_before();
+                mbar_arrive(o_free + t * 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < D; ++i) o[i] = 0.f;
+            }
+            if (un.poison && live) {                  // values that are no numbers, at keys this row sees
+                const int end = min(lim + 1, key0 + nt * PR_BN);
+                for (int k = max(key0, un.pos0 / PR_BN * PR_BN); k < end; ++k) {
+                    int id = __ldg(p.block_tables + (int64_t)un.b * p.stride + k / p.bs);
+                    if (id < 0 || id >= p.num_blocks) id = 0;
+                    const uint4 *v = reinterpret_cast<const uint4 *>(
+                        static_cast<const T *>(p.v_cache) + (((int64_t)id * p.Hkv + un.g) * p.bs + k % p.bs) * D);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 x = __ldg(v + i);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t bits = (w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+                            if (is_nonfinite16<T>(bits)) {
+                                if constexpr (std::is_same<T, __half>::value)
+                                    o[8 * i + e] += __half2float(__ushort_as_half((unsigned short)bits));
+                                else
+                                    o[8 * i + e] += __uint_as_float(bits << 16);
+                            }
+                        }
+                    }
+                }
+            }
+            const int tok = un.tok0 + t * p.P + rp, slot = un.slot;
+            const int64_t orow = live ? (int64_t)tok * p.Hq + un.g * p.G + rh : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_empty + st_u * 8);
+            if (slot >= 0) {
+                // unnormalised state, [D / 4][256 rows] float4, then [256 rows] (max, sum)
+                uint8_t *ws = p.ws_slots + (size_t)slot * 256 * (D + 2) * 4;
+                if (live && nt > 0) {
+                    float4 *dst = reinterpret_cast<float4 *>(ws) + t * PR_BM + r;
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i)
+                        dst[i * 256] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    reinterpret_cast<float2 *>(ws + (size_t)256 * D * 4)[t * PR_BM + r] = make_float2(m_ref, l);
+                }
+            } else {
+                // the warp's 32 rows in rounds of 32 dimensions through 2 KB: 64 bytes of a row per four lanes
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                int64_t row4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) row4[k] = __shfl_sync(0xffffffffu, orow, 8 * k + (lane >> 2));
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float *x = o + c0 + 8 * i;
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
+                                       pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = 8 * k + (lane >> 2), i = lane & 3;
+                        const uint4 x =
+                            *reinterpret_cast<const uint4 *>(stage + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+                        if (row4[k] >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row4[k] * D + c0 + 8 * i) = x;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) set_status(p.status, STATUS_TIMEOUT);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, PR_TMEM_COLS);
+    }
+}
+
+// Joins the units of the items that were cut: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s. One block
+// per unit index and 32 rows; a lane is a row, so the states are read in whole lines; the rows leave through
+// shared memory.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
+    __shared__ __align__(16) T rows[32][D + 8];
+    pdl_wait();
+    const int u = blockIdx.x;
+    if (u >= *p.ws_total) return;
+    const PromptItem it = p.ws_items[u];
+    if (it.splits0 == 0) return;
+    const int r0 = blockIdx.y * 32, t = r0 / PR_BM, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int splits = t ? it.splits1 : it.splits0;
+    auto row_of = [&](int i) -> int64_t {             // output row of row i of this block, or -1
+        const int r = (r0 & (PR_BM - 1)) + i, rp = r / p.G, pos = t * p.P + rp;
+        return r < p.P * p.G && pos < it.npos ? (int64_t)(it.tok0 + pos) * p.Hq + it.g * p.G + (r - rp * p.G) : -1;
+    };
+    const bool live = row_of(lane) >= 0;
+    const size_t slot_bytes = (size_t)256 * (D + 2) * 4, step = (size_t)p.Hkv * slot_bytes;
+    const uint8_t *ws = p.ws_slots + (size_t)u * slot_bytes;
+    float M = -INFINITY, sum = 0.f;
+    float4 acc[D / 32] = {};
+    if (live) {
+        const float2 *ml = reinterpret_cast<const float2 *>(ws + (size_t)256 * D * 4) + r0 + lane;
+        for (int s = 0; s < splits; ++s)
+            M = fmaxf(M, reinterpret_cast<const float2 *>(reinterpret_cast<const uint8_t *>(ml) + s * step)->x);
+        for (int s = 0; s < splits; ++s) {
+            const float2 x = *reinterpret_cast<const float2 *>(reinterpret_cast<const uint8_t *>(ml) + s * step);
+            const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - M);
+            sum += w * x.y;
+            const float4 *o = reinterpret_cast<const float4 *>(ws + s * step) + r0 + lane;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const float4 y = o[(warp * (D / 32) + i) * 256];
+                acc[i].x += w * y.x;
+                acc[i].y += w * y.y;
+                acc[i].z += w * y.z;
+                acc[i].w += w * y.w;
+            }
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        *reinterpret_cast<uint2 *>(&rows[lane][(warp * (D / 32) + i) * 4]) =
+            make_uint2(pack2<T>(acc[i].x * inv, acc[i].y * inv), pack2<T>(acc[i].z * inv, acc[i].w * inv));
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
+        const int64_t row = row_of(i / (D / 8));
+        if (row >= 0)
+            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * D + i % (D / 8) * 8) =
+                *reinterpret_cast<const uint4 *>(&rows[i / (D / 8)][i % (D / 8) * 8]);
+    }
+}
+
+template <typename T, int D>
+static cudaError_t launch_prompt_t(const PromptParams &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
+                                   const CUtensorMap &tmv, int sm_count, cudaStream_t stream) {
+    // set on every call: the attribute belongs to the current device, and callers may use several
+    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PromptShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(prompt_kernel<T, D>, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream,
+                   tmq, tmk, tmv, p);
+    if (e != cudaSuccess || p.max_units == 0) return e;
+    return launch_pdl(prompt_join_kernel<T, D>, dim3((unsigned)p.max_units, 8u), dim3(256), 0, stream, p);
+}
+
+cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const CUtensorMap &tmq,
+                          const CUtensorMap &tmk, const CUtensorMap &tmv, int sm_count, cudaStream_t stream) {
+    if (dtype == PA_FP16)
+        return head_dim == 64 ? launch_prompt_t<__half, 64>(p, tmq, tmk, tmv, sm_count, stream)
+                              : launch_prompt_t<__half, 128>(p, tmq, tmk, tmv, sm_count, stream);
+    return head_dim == 64 ? launch_prompt_t<__nv_bfloat16, 64>(p, tmq, tmk, tmv, sm_count, stream)
+                          : launch_prompt_t<__nv_bfloat16, 128>(p, tmq, tmk, tmv, sm_count, stream);
 }
 
 }  // namespace pa
