@@ -66,7 +66,7 @@ struct PromptShape {
     static constexpr int OFF_PREF = OFF_STAGE + 8 * 2048;
     static constexpr int OFF_UNITS = OFF_PREF + (PA_PACKED_MAX_SEQS + 4) * 4;
     static constexpr int OFF_BAR = OFF_UNITS + PR_UNITS * 64;
-    static constexpr int NBAR = 2 * KST + 2 * VST + 12 + 2 * PR_UNITS + 2;
+    static constexpr int NBAR = 2 * KST + 2 * VST + 14 + 2 * PR_UNITS + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 32;
     static_assert(SMEM <= (int)MAX_SMEM_PER_CTA, "shared memory");
@@ -108,6 +108,54 @@ template <typename T>
 __device__ __forceinline__ bool is_nonfinite16(uint32_t x) {
     constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
     return (x & E) == E;
+}
+
+// Two fp32 operations at once (register pairs).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// tcgen05.mma with descriptors as a constant upper word (128-byte swizzle, version, stride between 8-row groups)
+// and a lower word (address / 16, leading offset / 16 << 16).
+__host__ __device__ constexpr uint32_t desc_hi(int group_stride) { return (uint32_t)(group_stride >> 4) | 1u << 14 | 2u << 29; }
+
+template <uint32_t HA, uint32_t HB>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HA), "n"(HB));
+}
+
+// A in tensor memory.
+template <uint32_t HB>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HB));
 }
 
 template <int RANK>
@@ -221,7 +269,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t k_full = base + S::OFF_BAR, k_empty = k_full + S::KST * 8;
     const uint32_t v_full = k_empty + S::KST * 8, v_empty = v_full + S::VST * 8;
     const uint32_t q_full = v_empty + S::VST * 8, q_empty = q_full + 16;
-    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, o_free = o_done + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32, o_free = o_done + 16;
     const uint32_t u_full = o_free + 16, u_empty = u_full + PR_UNITS * 8;
     const uint32_t v_raw = u_empty + PR_UNITS * 8, drain = v_raw + 8;
     PromptUnit *units = reinterpret_cast<PromptUnit *>(smem + S::OFF_UNITS);
@@ -239,7 +287,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             mbar_init(q_full + t * 8, 1);
             mbar_init(q_empty + t * 8, 1);
             mbar_init(s_full + t * 8, 1);
-            mbar_init(p_full + t * 8, PR_BM);
+            mbar_init(p_full + 2 * t * 8, PR_BM);
+            mbar_init(p_full + (2 * t + 1) * 8, PR_BM);
             mbar_init(o_done + t * 8, 1);
             mbar_init(o_free + t * 8, PR_BM);
         }
@@ -452,51 +501,67 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
         } else {
             // ------------------------------------------------------------ MMA issue (lane 0)
+            // One thread feeds the tensor cores, so what it does besides counts: descriptors are a constant upper
+            // word and a lower one (address and leading offset) to which constants are added.
             if (lane == 0) {
-                const uint32_t idesc_s = umma_idesc<T>(PR_BM, PR_BN, false);
-                const uint32_t idesc_o = umma_idesc<T>(PR_BM, D, true);
-                const uint64_t dq0 = umma_desc_sw128(base, 16, 1024);
-                const uint64_t dk0 = umma_desc_sw128(base + S::OFF_K, 16, S::GROUP_BYTES);
-                const uint64_t dv0 = umma_desc_sw128(base + S::OFF_V, 1024, S::GROUP_BYTES);
-                int kc = 0, vc = 0, v_seen = 0;       // K tiles, V tiles taken; V tiles waited for
-                int qc[2] = {0, 0}, pc[2] = {0, 0}, oc[2] = {0, 0};
-                bool pend[2] = {false, false}, pfirst[2] = {false, false}, plast[2] = {false, false};
-                bool ok = true, held = false;         // held: the V tile vc - 1 is not released yet
+                constexpr uint32_t idesc_s = umma_idesc<T>(PR_BM, PR_BN, false);
+                constexpr uint32_t idesc_o = umma_idesc<T>(PR_BM, D, true);
+                constexpr uint32_t hi_q = desc_hi(1024), hi_kv = desc_hi(S::GROUP_BYTES);
+                const uint32_t q_lo = base >> 4 | 1u << 16, k_lo = (base + S::OFF_K) >> 4 | 1u << 16;
+                const uint32_t v_lo = (base + S::OFF_V) >> 4 | (1024u >> 4) << 16;
+                int ks = 0, vs = 0, last_vs = 0;      // stages of the next K and V tile; the V stage not released yet
+                uint32_t kph = 0, vph = 0;            // and their phases
+                uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {1, 1};
+                int pj = 0, pn0 = 0, pn1 = 0;         // the step before: its index, key tiles of its unit
+                bool ok = true, v_here = true, held = false;
                 // O_t += P_t V of the step before
-                auto flush = [&](int t) -> bool {
-                    if (!pend[t]) return true;
-                    const int st = (vc - 1) % S::VST;
-                    if (v_seen < vc) {
-                        if (!wait(v_full + st * 8, (uint32_t)((vc - 1) / S::VST) & 1u)) return false;
-                        v_seen = vc;
+                auto flush = [&](auto tc, int pn) -> bool {
+                    constexpr int t = decltype(tc)::value;
+                    if (pj >= pn) return true;
+                    if (!v_here) {
+                        if (!wait(v_full + last_vs * 8, vph)) return false;
+                        v_here = true;
                     }
-                    if (!wait(p_full + t * 8, (uint32_t)pc[t] & 1u)) return false;
-                    ++pc[t];
-                    if (pfirst[t]) {                  // the output of the unit before has left tensor memory
-                        if (oc[t] > 0 && !wait(o_free + t * 8, (uint32_t)(oc[t] - 1) & 1u)) return false;
-                        ++oc[t];
+                    if (!wait(p_full + 2 * t * 8, pph[t])) return false;
+                    if (pj == 0) {                    // the output of the unit before has left tensor memory
+                        if (!wait(o_free + t * 8, oph[t])) return false;
+                        oph[t] ^= 1u;
                     }
                     tc_fence_after();
-                    const uint64_t dv = dv0 + (uint64_t)(st * (S::KV_BYTES >> 4));
-                    const uint32_t pt = tmem + t * 256, ot = pt + 128;
+                    const uint32_t v = v_lo + last_vs * (S::KV_BYTES >> 4), pt = tmem + t * 256, ot = pt + 128;
+                    umma_ts<hi_kv>(ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int ks = 0; ks < PR_BN / 16; ++ks)
-                        umma_f16_tmem_a(ot, pt + ks * 8, dv + (uint64_t)((ks * 2 * S::GROUP_BYTES) >> 4), idesc_o,
-                                        ks > 0 || !pfirst[t] ? 1u : 0u);
-                    if (plast[t]) umma_commit(o_done + t * 8);
-                    pend[t] = false;
+                    for (int k = 1; k < PR_BN / 32; ++k)
+                        umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
+                    if (!wait(p_full + (2 * t + 1) * 8, pph[t])) return false;       // the second half of the keys
+                    pph[t] ^= 1u;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = PR_BN / 32; k < PR_BN / 16; ++k)
+                        umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
+                    if (pj == pn - 1) umma_commit(o_done + t * 8);
                     return true;
                 };
-                auto issue_s = [&](int t) {           // S_t = Q_t K^T
-                    const uint64_t dk = dk0 + (uint64_t)((kc % S::KST) * (S::KV_BYTES >> 4));
-                    const uint64_t dq = dq0 + (uint64_t)(t * (S::Q_BYTES >> 4));
+                // S_t = Q_t K^T
+                auto issue_s = [&](auto tc, int j, int n) -> bool {
+                    constexpr int t = decltype(tc)::value;
+                    if (j >= n) return true;
+                    if (j == 0) {
+                        if (!wait(q_full + t * 8, qph[t])) return false;
+                        qph[t] ^= 1u;
+                    }
+                    const uint32_t k = k_lo + ks * (S::KV_BYTES >> 4), q = q_lo + t * (S::Q_BYTES >> 4);
                     tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        umma_f16(tmem + t * 256, dq + (uint64_t)(((ks >> 2) * (PR_BM * 128) + (ks & 3) * 32) >> 4),
-                                 dk + (uint64_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_ss<hi_q, hi_kv>(tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
+                                             k + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc_s, i > 0 ? 1u : 0u);
                     umma_commit(s_full + t * 8);
+                    if (j == n - 1) umma_commit(q_empty + t * 8);
+                    return true;
                 };
+                constexpr std::integral_constant<int, 0> T0{};
+                constexpr std::integral_constant<int, 1> T1{};
                 for (int c = 0; ok; ++c) {
                     const int st_u = c % PR_UNITS;
                     if (!(ok = wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u))) break;
@@ -505,38 +570,23 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     mbar_arrive(u_empty + st_u * 8);
                     const int nt = max(n0, n1);
                     for (int j = 0; j < nt; ++j) {
-                        if (!(ok = flush(0))) break;
-                        if (!(ok = wait(k_full + (kc % S::KST) * 8, (uint32_t)(kc / S::KST) & 1u))) break;
-                        if (j < n0) {
-                            if (j == 0) {
-                                if (!(ok = wait(q_full, (uint32_t)qc[0] & 1u))) break;
-                                ++qc[0];
-                            }
-                            issue_s(0);
-                            if (j == n0 - 1) umma_commit(q_empty);
-                        }
-                        if (!(ok = flush(1))) break;
-                        if (held) umma_commit(v_empty + ((vc - 1) % S::VST) * 8);
-                        if (j < n1) {
-                            if (j == 0) {
-                                if (!(ok = wait(q_full + 8, (uint32_t)qc[1] & 1u))) break;
-                                ++qc[1];
-                            }
-                            issue_s(1);
-                            if (j == n1 - 1) umma_commit(q_empty + 8);
-                        }
-                        umma_commit(k_empty + (kc % S::KST) * 8);
-                        ++kc;
-                        ++vc;
+                        if (!(ok = flush(T0, pn0) && wait(k_full + ks * 8, kph) && issue_s(T0, j, n0) && flush(T1, pn1)))
+                            break;
+                        if (held) umma_commit(v_empty + last_vs * 8);
+                        if (!(ok = issue_s(T1, j, n1))) break;
+                        umma_commit(k_empty + ks * 8);
+                        if (++ks == S::KST) ks = 0, kph ^= 1u;
+                        last_vs = vs;                 // the V tile that goes with this step's scores
+                        if (held && vs == 0) vph ^= 1u;
+                        if (++vs == S::VST) vs = 0;
                         held = true;
-                        pend[0] = j < n0;
-                        pend[1] = j < n1;
-                        pfirst[0] = pfirst[1] = j == 0;
-                        plast[0] = j == n0 - 1;
-                        plast[1] = j == n1 - 1;
+                        v_here = false;
+                        pj = j;
+                        pn0 = n0;
+                        pn1 = n1;
                     }
                 }
-                if (ok) ok = flush(0) && flush(1);
+                if (ok) ok = flush(T0, pn0) && flush(T1, pn1);
                 if (!ok) {
                     umma_commit(drain);
                     mbar_wait_bounded(drain, 0u, p.wait_ns);
@@ -570,18 +620,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 float sv[PR_BN];
                 tmem_ld_cols(tmem_s, sv);
                 const int t0 = key0 + j * PR_BN;
-                float m8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
                 if (t0 + PR_BN - 1 > lim) {
 #pragma unroll
                     for (int i = 0; i < PR_BN; ++i) sv[i] = t0 + i <= lim ? sv[i] : -INFINITY;
                 }
                 // raw-score maximum (the scale is positive, so it commutes with it)
+                float m4[4];
 #pragma unroll
-                for (int i = 0; i < PR_BN; ++i) m8[i & 7] = fmaxf(m8[i & 7], sv[i]);
-                const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                       fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+                for (int i = 0; i < 4; ++i) m4[i] = max3(sv[3 * i], sv[3 * i + 1], sv[3 * i + 2]);
+#pragma unroll
+                for (int i = 12; i + 2 <= PR_BN; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], sv[i], sv[i + 1]);
+                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.scale_log2;
                 float alpha = 1.f;
                 bool rescale = false;
                 if (mx > m_ref + PR_RESCALE_LOG2 || (m_ref == -INFINITY && mx > -INFINITY)) {
@@ -601,25 +650,31 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                 }
                 const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-                float r8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r8[i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < PR_BN; ++i) {
-                    sv[i] = ex2_approx(fmaf(sv[i], p.scale_log2, nm));
-                    r8[i & 7] += sv[i];
-                }
-                l = l * alpha + ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+                const uint64_t sc2 = pair(p.scale_log2, p.scale_log2), nm2 = pair(nm, nm);
+                // the weights of the first 64 keys are handed over while those of the others are computed
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) w[i] = pack2<T>(sv[64 * h + 2 * i], sv[64 * h + 2 * i + 1]);
+                    for (int i = 0; i < 32; ++i) {
+                        float &x = sv[64 * h + 2 * i], &y = sv[64 * h + 2 * i + 1];
+                        unpair(fma_pair(pair(x, y), sc2, nm2), x, y);
+                        x = ex2_approx(x);
+                        y = ex2_approx(y);
+                        w[i] = pack2<T>(x, y);
+                    }
                     tmem_st32_raw(tmem_s + 32 * h, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full + (2 * t + h) * 8);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_full + t * 8);
+                // the sum is nobody's to wait for
+                uint64_t r4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                for (int i = 0; i < PR_BN / 2; ++i) r4[i & 3] = add_pair(r4[i & 3], pair(sv[2 * i], sv[2 * i + 1]));
+                float ra, rb;
+                unpair(add_pair(add_pair(r4[0], r4[1]), add_pair(r4[2], r4[3])), ra, rb);
+                l = l * alpha + (ra + rb);
             }
             if (!ok) break;
             float o[D];
