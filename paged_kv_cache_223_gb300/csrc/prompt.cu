@@ -21,9 +21,17 @@
 //                    [8 keys][128 bytes] in shared memory, so that a whole block of tokens is one copy and
 //                    8-key groups stay a constant stride apart in the matrix descriptors
 //   warp 9           one thread issues every MMA: per key tile and row tile O += P V (P from tensor
-//                    memory, V MN-major), then S = Q K^T into the columns P came from
+//                    memory, V MN-major), then S = Q K^T into the columns P came from, the row tiles in turn
+//                    so that one's products run while the other's softmax does
 //   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
 //                    [P positions][G heads][64 dimensions])
+// The MMA thread bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
+// costs it 100 to 170, while the softmax is done 1000 cycles before its weights are asked for. So it waits for K
+// and the weights alone: one thread of each row tile's softmax waits for V before it hands the weights over, and
+// tells the loaders when a K tile (and the V tile before it) has been read. Measured, 4 x 4096 tokens, 64/8 heads
+// of 128, bf16: 780 us, 1410 TFLOP/s, against 1003 us with the waits, divisions and descriptors in that thread.
+// Not kept: an MMA thread per row tile, in turns or not (820, 940 us: their products interleave, or each turn
+// costs two waits), two softmax threads per row (936 us and more), weights handed over in halves (840 us).
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
 //
@@ -66,7 +74,7 @@ struct PromptShape {
     static constexpr int OFF_PREF = OFF_STAGE + 8 * 2048;
     static constexpr int OFF_UNITS = OFF_PREF + (PA_PACKED_MAX_SEQS + 4) * 4;
     static constexpr int OFF_BAR = OFF_UNITS + PR_UNITS * 64;
-    static constexpr int NBAR = 2 * KST + 2 * VST + 14 + 2 * PR_UNITS + 2;
+    static constexpr int NBAR = 2 * KST + VST + 12 + 2 * PR_UNITS + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 32;
     static_assert(SMEM <= (int)MAX_SMEM_PER_CTA, "shared memory");
@@ -108,6 +116,10 @@ template <typename T>
 __device__ __forceinline__ bool is_nonfinite16(uint32_t x) {
     constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
     return (x & E) == E;
+}
+
+__device__ __forceinline__ void mbar_arrive_count(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
 // Two fp32 operations at once (register pairs).
@@ -267,9 +279,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t base = (raw_u32 + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw_u32);
     const uint32_t k_full = base + S::OFF_BAR, k_empty = k_full + S::KST * 8;
-    const uint32_t v_full = k_empty + S::KST * 8, v_empty = v_full + S::VST * 8;
-    const uint32_t q_full = v_empty + S::VST * 8, q_empty = q_full + 16;
-    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32, o_free = o_done + 16;
+    const uint32_t v_full = k_empty + S::KST * 8, q_full = v_full + S::VST * 8, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, o_free = o_done + 16;
     const uint32_t u_full = o_free + 16, u_empty = u_full + PR_UNITS * 8;
     const uint32_t v_raw = u_empty + PR_UNITS * 8, drain = v_raw + 8;
     PromptUnit *units = reinterpret_cast<PromptUnit *>(smem + S::OFF_UNITS);
@@ -281,14 +292,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), PR_TMEM_COLS);
     if (tid == 64) {
-        for (int s = 0; s < S::KST; ++s) mbar_init(k_full + s * 8, 1), mbar_init(k_empty + s * 8, 1);
-        for (int s = 0; s < S::VST; ++s) mbar_init(v_full + s * 8, 1), mbar_init(v_empty + s * 8, 1);
+        for (int s = 0; s < S::KST; ++s) mbar_init(k_full + s * 8, 1), mbar_init(k_empty + s * 8, 2);
+        for (int s = 0; s < S::VST; ++s) mbar_init(v_full + s * 8, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full + t * 8, 1);
             mbar_init(q_empty + t * 8, 1);
             mbar_init(s_full + t * 8, 1);
-            mbar_init(p_full + 2 * t * 8, PR_BM);
-            mbar_init(p_full + (2 * t + 1) * 8, PR_BM);
+            mbar_init(p_full + t * 8, PR_BM);
             mbar_init(o_done + t * 8, 1);
             mbar_init(o_free + t * 8, PR_BM);
         }
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             // ------------------------------------------------------------ K or V tiles
             const bool is_v = warp == PR_V_WARP;
             const int nst = is_v ? S::VST : S::KST;
-            const uint32_t full0 = is_v ? v_full : k_full, empty0 = is_v ? v_empty : k_empty;
+            const uint32_t full0 = is_v ? v_full : k_full;
             const uint32_t ring = base + (is_v ? S::OFF_V : S::OFF_K);
             const CUtensorMap *map = is_v ? &tmv : &tmk;
             const uint64_t policy = l2_policy_evict_last();   // other row tiles read it again
@@ -430,7 +440,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 for (int j = 0; j < nt; ++j) {
                     const int st = issued % nst;
                     if (issued >= nst) {
-                        ok = __all_sync(0xffffffffu, wait(empty0 + st * 8, (uint32_t)(issued / nst - 1) & 1u));
+                        // K(i) takes the stage of K(i - nst), V(i) that of V(i - nst), which P V reads before the scores
+                        // of tile i - nst + 1 are issued: one release per key tile frees both
+                        const int free = issued - nst + (is_v ? 1 : 0);
+                        ok = __all_sync(0xffffffffu, wait(k_empty + free % S::KST * 8, (uint32_t)(free / S::KST) & 1u));
                         if (!ok) break;
                     }
                     int id = id_next;
@@ -510,19 +523,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 const uint32_t q_lo = base >> 4 | 1u << 16, k_lo = (base + S::OFF_K) >> 4 | 1u << 16;
                 const uint32_t v_lo = (base + S::OFF_V) >> 4 | (1024u >> 4) << 16;
                 int ks = 0, vs = 0, last_vs = 0;      // stages of the next K and V tile; the V stage not released yet
-                uint32_t kph = 0, vph = 0;            // and their phases
+                uint32_t kph = 0;                     // and the K stage's phase
                 uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {1, 1};
                 int pj = 0, pn0 = 0, pn1 = 0;         // the step before: its index, key tiles of its unit
-                bool ok = true, v_here = true, held = false;
+                bool ok = true;
                 // O_t += P_t V of the step before
                 auto flush = [&](auto tc, int pn) -> bool {
                     constexpr int t = decltype(tc)::value;
                     if (pj >= pn) return true;
-                    if (!v_here) {
-                        if (!wait(v_full + last_vs * 8, vph)) return false;
-                        v_here = true;
-                    }
-                    if (!wait(p_full + 2 * t * 8, pph[t])) return false;
+                    if (!wait(p_full + t * 8, pph[t])) return false;
+                    pph[t] ^= 1u;
                     if (pj == 0) {                    // the output of the unit before has left tensor memory
                         if (!wait(o_free + t * 8, oph[t])) return false;
                         oph[t] ^= 1u;
@@ -531,13 +541,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     const uint32_t v = v_lo + last_vs * (S::KV_BYTES >> 4), pt = tmem + t * 256, ot = pt + 128;
                     umma_ts<hi_kv>(ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 1; k < PR_BN / 32; ++k)
-                        umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
-                    if (!wait(p_full + (2 * t + 1) * 8, pph[t])) return false;       // the second half of the keys
-                    pph[t] ^= 1u;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = PR_BN / 32; k < PR_BN / 16; ++k)
+                    for (int k = 1; k < PR_BN / 16; ++k)
                         umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
                     if (pj == pn - 1) umma_commit(o_done + t * 8);
                     return true;
@@ -551,7 +555,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         qph[t] ^= 1u;
                     }
                     const uint32_t k = k_lo + ks * (S::KV_BYTES >> 4), q = q_lo + t * (S::Q_BYTES >> 4);
-                    tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
                         umma_ss<hi_q, hi_kv>(tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
@@ -570,17 +573,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     mbar_arrive(u_empty + st_u * 8);
                     const int nt = max(n0, n1);
                     for (int j = 0; j < nt; ++j) {
-                        if (!(ok = flush(T0, pn0) && wait(k_full + ks * 8, kph) && issue_s(T0, j, n0) && flush(T1, pn1)))
-                            break;
-                        if (held) umma_commit(v_empty + last_vs * 8);
-                        if (!(ok = issue_s(T1, j, n1))) break;
-                        umma_commit(k_empty + ks * 8);
+                        if (!(ok = wait(k_full + ks * 8, kph) && flush(T0, pn0))) break;
+                        // the scores of a step tell that all products with the V tile before are done: they are the
+                        // last to be issued, so where row tile 1 has none, its product goes first
+                        if (j < n1) {
+                            if (!(ok = issue_s(T0, j, n0) && flush(T1, pn1) && issue_s(T1, j, n1))) break;
+                        } else {
+                            if (!(ok = flush(T1, pn1) && issue_s(T0, j, n0))) break;
+                        }
                         if (++ks == S::KST) ks = 0, kph ^= 1u;
                         last_vs = vs;                 // the V tile that goes with this step's scores
-                        if (held && vs == 0) vph ^= 1u;
                         if (++vs == S::VST) vs = 0;
-                        held = true;
-                        v_here = false;
                         pj = j;
                         pn0 = n0;
                         pn1 = n1;
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const bool in_tile = r < p.P * p.G;
         const uint32_t tmem_s = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16), tmem_o = tmem_s + 128;
         uint8_t *stage = smem + S::OFF_STAGE + warp * 2048;
-        int sc = 0, oc = 0;
+        int sc = 0, oc = 0, tiles = 0;                // scores and outputs taken; key tiles of the units before
         bool ok = true;
         for (int c = 0; ok; ++c) {
             const int st_u = c % PR_UNITS;
@@ -616,6 +619,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 ok = __all_sync(0xffffffffu, wait(s_full + t * 8, (uint32_t)sc & 1u));
                 if (!ok) break;
                 ++sc;
+                const int i_k = tiles + j;            // this key tile in the block's sequence of them
+                // K (and the V of the step before, whose product comes before these scores) is read: the row tiles
+                // that work on it release it
+                if (r == 0) mbar_arrive_count(k_empty + i_k % S::KST * 8, j < min(un.n0, un.n1) ? 1u : 2u);
                 tc_fence_after();
                 float sv[PR_BN];
                 tmem_ld_cols(tmem_s, sv);
@@ -651,7 +658,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                 const uint64_t sc2 = pair(p.scale_log2, p.scale_log2), nm2 = pair(nm, nm);
-                // the weights of the first 64 keys are handed over while those of the others are computed
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[32];
@@ -664,10 +670,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         w[i] = pack2<T>(x, y);
                     }
                     tmem_st32_raw(tmem_s + 32 * h, w);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_full + (2 * t + h) * 8);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                // the MMA thread asks for the weights alone: their V tile is waited for here
+                if (r == 0 && !wait(v_full + i_k % S::VST * 8, (uint32_t)(i_k / S::VST) & 1u)) *abort_flag = 1;
+                __syncwarp();
+                mbar_arrive(p_full + t * 8);
                 // the sum is nobody's to wait for
                 uint64_t r4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -714,6 +723,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                 }
             }
+            tiles += max(un.n0, un.n1);
             const int tok = un.tok0 + t * p.P + rp, slot = un.slot;
             const int64_t orow = live ? (int64_t)tok * p.Hq + un.g * p.G + rh : -1;
             __syncwarp();
