@@ -11,9 +11,9 @@
 // one read of K and V; an item is two row tiles of one sequence and KV head. Items behind long contexts
 // are cut along the keys into units where there are too few to fill the GPU, and a second kernel joins
 // the units' (O, max, sum). The lengths live on the device, so every block of the persistent grid
-// computes the same plan (units per sequence, cut length) from them and takes every gridDim.x-th unit, a
-// sequence's longest first, the direction alternating from round to round so that descending lengths
-// even out. A captured call follows lengths that change between replays.
+// computes the same plan from them (items by falling length, cut length) and takes every gridDim.x-th
+// unit, the direction alternating from round to round so that falling lengths even out. A captured call
+// follows lengths that change between replays.
 //
 // One block per SM, 384 threads:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1: one row per thread = one tensor-memory lane
@@ -39,7 +39,8 @@
 // scores are. Their weight is 0 in P V, but 0 times a value that is no number is none either: V rows behind
 // the unit's last position are zeroed, and the V tiles in which only some rows see a key are scanned; where
 // one holds a NaN or infinity, those words are zeroed and the rows that do see them get them added to their
-// outputs (each seen value has a weight > 0) in a slow path that real data never takes.
+// outputs (each seen value has a weight > 0) in a slow path that real data never takes. The softmax threads do
+// this, between their weights and the product: they have the time.
 //
 // Roundings. S, the softmax statistics and O are fp32. P is rounded once to the model's 16-bit type, as the
 // product with V takes it (half a step per weight, averaged over the keys: of the size of the output's own
@@ -72,9 +73,10 @@ struct PromptShape {
     static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
     static constexpr int OFF_STAGE = OFF_V + VST * KV_BYTES;          // 2 KB per softmax warp
     static constexpr int OFF_PREF = OFF_STAGE + 8 * 2048;
-    static constexpr int OFF_UNITS = OFF_PREF + (PA_PACKED_MAX_SEQS + 4) * 4;
+    static constexpr int OFF_KEYS = OFF_PREF + (PA_PACKED_MAX_SEQS + 4) * 4;
+    static constexpr int OFF_UNITS = OFF_KEYS + 2 * 512 * 4;          // sort keys: 4 KB
     static constexpr int OFF_BAR = OFF_UNITS + PR_UNITS * 64;
-    static constexpr int NBAR = 2 * KST + VST + 12 + 2 * PR_UNITS + 2;
+    static constexpr int NBAR = 2 * KST + VST + 12 + 2 * PR_UNITS + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = 1024 + OFF_MISC + 32;
     static_assert(SMEM <= (int)MAX_SMEM_PER_CTA, "shared memory");
@@ -200,73 +202,115 @@ __device__ __forceinline__ void sequence(const PromptParams &p, int b, int &firs
     L = L < 0 ? 0 : (L > p.max_ctx ? p.max_ctx : L);
 }
 
-// The plan, by one warp: key tiles per unit, and the running number of units (of one KV head) per sequence.
+// The plan, computed by every block alike. Up to PR_SORT items are sorted, the ones with most key tiles first, and
+// cut into units of at most `chunk` key tiles; more items are enough to even out by themselves and stay whole, a
+// sequence's last first.
+constexpr int PR_SORT = 512;
+struct PromptPlan {
+    int *pref;                 // items of the sequences before b; then, sorted: [512] items, [513] units, [512] tiles
+    uint32_t *key, *pack;      // [PR_SORT] each, while sorting
+    int *meta;                 // items, key tiles per unit, units (of one KV head)
+    __device__ int *items() const { return pref; }                  // b << 16 | item within the sequence
+    __device__ int *units() const { return pref + PR_SORT; }        // units of the items before
+    __device__ int *tiles() const { return pref + 2 * PR_SORT + 4; }
+};
+static_assert(3 * PR_SORT + 4 <= PA_PACKED_MAX_SEQS, "the sorted plan takes the prefix's place");
+constexpr int PR_WHOLE = 1 << 24;
+
+__device__ __forceinline__ int items_of(const PromptParams &p, int n) { return (n + 2 * p.P - 1) / (2 * p.P); }
+
 // Costs are in key tiles of work: a unit costs PLAN_UNIT more than its tiles, joining PLAN_JOIN.
-__device__ int make_plan(const PromptParams &p, int *pref, int lane) {
-    constexpr int PLAN_UNIT = 3, PLAN_JOIN = 4, PLAN_MIN = 4, WHOLE = 1 << 24;
+__device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, int lane) {
+    constexpr int PLAN_UNIT = 3, PLAN_JOIN = 4, PLAN_MIN = 4;
     const int rows2 = 2 * p.P, grid = (int)gridDim.x;
-    int chunk = WHOLE;
-    if (p.max_units > 0) {
-        int items = 0, longest = 0;
-        int64_t tiles = 0;
-        for (int b = lane; b < p.num_seqs; b += 32) {
-            int first, n, L;
-            sequence(p, b, first, n, L, nullptr);
-            if (n == 0) continue;
-            const int it = (n + rows2 - 1) / rows2, nt = (L + PR_BN - 1) / PR_BN;
-            const int e0 = (L - n + (n < rows2 ? n : rows2) + PR_BN - 1) / PR_BN;
-            items += it;
-            longest = nt > longest ? nt : longest;
-            tiles += (int64_t)it * (nt + (e0 > 0 ? e0 : 0)) / 2;
-        }
+    if (tid < 32) {
+        int total = 0;
+        for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+            const int b = b0 + lane;
+            int first = 0, n = 0, L = 0;
+            if (b < p.num_seqs) sequence(p, b, first, n, L, blockIdx.x == 0 ? p.status : nullptr);
+            int x = items_of(p, n);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            items += __shfl_xor_sync(0xffffffffu, items, o);
-            tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-        }
-        // one candidate per lane: the longest context in k units
-        const int k = lane < 16 ? lane + 1 : 16 + (lane - 15) * 9;
-        int c = (longest + k - 1) / k;
-        if (c < PLAN_MIN) c = PLAN_MIN;
-        if (k == 1) c = WHOLE;
-        int64_t units = 0;
-        if ((int64_t)items * p.Hkv < 2 * grid) {
-            for (int b = 0; b < p.num_seqs; ++b) {
-                int first, n, L;
-                sequence(p, b, first, n, L, nullptr);
-                const int nt = (L + PR_BN - 1) / PR_BN;
-                units += (int64_t)((n + rows2 - 1) / rows2) * (nt > c ? (nt + c - 1) / c : 1);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
             }
-            units *= p.Hkv;
-            const int64_t unit = c < longest ? c : longest;
-            int64_t cost = units <= grid ? 2 * (unit + PLAN_UNIT)
-                                         : 2 * ((tiles * p.Hkv + units * PLAN_UNIT) / grid) + unit;
-            if (k > 1) cost += 2 * PLAN_JOIN;
-            if (k > 1 && (units > p.max_units || longest <= PLAN_MIN)) cost = (int64_t)1 << 40;
-            int64_t best = cost * 64 + lane;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-            chunk = __shfl_sync(0xffffffffu, c, (int)(best & 31));
+            if (b < p.num_seqs) pl.pref[b + 1] = total + x;
+            total += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            pl.pref[0] = 0;
+            pl.meta[0] = pl.meta[2] = total;
+            pl.meta[1] = PR_WHOLE;
         }
     }
+    __syncthreads();
+    const int items = pl.meta[0];
+    if (items > PR_SORT) return;
+    for (int k = tid; k < items; k += PR_THREADS) {
+        int lo = 0, hi = p.num_seqs;                  // pref[lo] <= k < pref[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pl.pref[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        int first, n, L;
+        sequence(p, lo, first, n, L, nullptr);
+        const int i = k - pl.pref[lo], end = L - n + min(n, (i + 1) * rows2);
+        const int e = end > PR_BN ? (end + PR_BN - 1) / PR_BN : 1;
+        pl.key[k] = (uint32_t)min(e, 1 << 22) * PR_SORT + (PR_SORT - 1 - k);        // all different
+        pl.pack[k] = (uint32_t)lo << 16 | (uint32_t)i;
+    }
+    __syncthreads();
+    for (int k = tid; k < items; k += PR_THREADS) {
+        const uint32_t mine = pl.key[k];
+        int rank = 0;
+        for (int m = 0; m < items; ++m) rank += pl.key[m] > mine;
+        pl.items()[rank] = (int)pl.pack[k];
+        pl.tiles()[rank] = (int)(mine / PR_SORT);
+    }
+    __syncthreads();
+    if (tid >= 32) return;
+    int chunk = PR_WHOLE;
+    const int *tiles = pl.tiles();
+    if (p.max_units > 0 && items > 0 && (int64_t)items * p.Hkv < 2 * grid && tiles[0] > PLAN_MIN) {
+        int64_t sum = 0;
+        for (int k = lane; k < items; k += 32) sum += tiles[k];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum *= p.Hkv;
+        // one candidate per lane, around an even share of the tiles; the last: whole items
+        const int share = (int)((sum + grid - 1) / grid);
+        int c = lane < 8 ? share * (lane + 2) / 10 : share + (lane - 8) * max(1, share / 12);
+        c = lane == 31 ? PR_WHOLE : max(c, PLAN_MIN);
+        int64_t units = 0;
+        for (int k = 0; k < items; ++k) units += tiles[k] > c ? (tiles[k] + c - 1) / c : 1;
+        units *= p.Hkv;
+        const int64_t unit = min(c, tiles[0]);
+        int64_t cost = units <= grid ? 2 * (unit + PLAN_UNIT) : 2 * ((sum + units * PLAN_UNIT) / grid) + unit;
+        if (lane < 31) cost = units > p.max_units ? (int64_t)1 << 40 : cost + 2 * PLAN_JOIN;
+        int64_t best = cost * 32 + (31 - lane);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+        chunk = __shfl_sync(0xffffffffu, c, 31 - (int)(best & 31));
+    }
     int total = 0;
-    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        int first = 0, n = 0, L = 0;
-        if (b < p.num_seqs) sequence(p, b, first, n, L, nullptr);
-        const int nt = (L + PR_BN - 1) / PR_BN;
-        int x = (n + rows2 - 1) / rows2 * (nt > chunk ? (nt + chunk - 1) / chunk : 1);
+    for (int k0 = 0; k0 < items; k0 += 32) {
+        const int k = k0 + lane;
+        int x = k < items ? (tiles[k] > chunk ? (tiles[k] + chunk - 1) / chunk : 1) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (b < p.num_seqs) pref[b + 1] = total + x;
+        if (k < items) pl.units()[k + 1] = total + x;
         total += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) pref[0] = 0;
-    return chunk;
+    if (lane == 0) {
+        pl.units()[0] = 0;
+        pl.meta[1] = chunk;
+        pl.meta[2] = total;
+    }
 }
 
 template <typename T, int D>
@@ -282,12 +326,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t v_full = k_empty + S::KST * 8, q_full = v_full + S::VST * 8, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, o_free = o_done + 16;
     const uint32_t u_full = o_free + 16, u_empty = u_full + PR_UNITS * 8;
-    const uint32_t v_raw = u_empty + PR_UNITS * 8, drain = v_raw + 8;
+    const uint32_t drain = u_empty + PR_UNITS * 8;
     PromptUnit *units = reinterpret_cast<PromptUnit *>(smem + S::OFF_UNITS);
-    int *pref = reinterpret_cast<int *>(smem + S::OFF_PREF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_chunk = reinterpret_cast<int *>(tmem_slot + 2);
+    const PromptPlan plan = {reinterpret_cast<int *>(smem + S::OFF_PREF), reinterpret_cast<uint32_t *>(smem + S::OFF_KEYS),
+                             reinterpret_cast<uint32_t *>(smem + S::OFF_KEYS) + PR_SORT,
+                             reinterpret_cast<int *>(tmem_slot + 2)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), PR_TMEM_COLS);
@@ -306,22 +351,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             mbar_init(u_full + s * 8, 1);
             mbar_init(u_empty + s * 8, 11);           // K, V and MMA warps, 8 softmax warps
         }
-        mbar_init(v_raw, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     pdl_wait();
     pdl_trigger();
-    if (warp == 0) {
-        const int c = make_plan(p, pref, lane);
-        if (lane == 0) *s_chunk = c;
-    }
+    make_plan(p, plan, tid, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int chunk = *s_chunk;
+    const int chunk = plan.meta[1];
 
     // A bounded wait that also ends when another role gave up.
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -344,7 +385,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         if (warp == PR_SCHED_WARP) {
             // ------------------------------------------------------------ units and their Q tiles
             if (lane == 0) {
-                const int total = pref[p.num_seqs] * p.Hkv, grid = (int)gridDim.x, rows2 = 2 * p.P;
+                const int items = plan.meta[0], total = plan.meta[2] * p.Hkv, grid = (int)gridDim.x, rows2 = 2 * p.P;
                 const uint64_t policy = l2_policy_evict_first();
                 int published = 0, qn[2] = {0, 0};
                 bool ok = true;
@@ -352,21 +393,27 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 for (int round = 0; ok; ++round) {
                     const int u = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
                     PromptUnit un = {};
-                    if (u < total && round * (int64_t)grid < total) {
+                    if ((int64_t)round * grid < total) {
+                        if (u >= total) continue;     // the last, partial round: the next one ends the list
                         const int w = u / p.Hkv;
-                        int lo = 0, hi = p.num_seqs;  // pref[lo] <= w < pref[hi]
+                        const int *pre = items > PR_SORT ? plan.pref : plan.units();
+                        int lo = 0, hi = items > PR_SORT ? p.num_seqs : items;     // pre[lo] <= w < pre[hi]
                         while (hi - lo > 1) {
                             const int mid = (lo + hi) >> 1;
-                            if (pref[mid] <= w) lo = mid;
+                            if (pre[mid] <= w) lo = mid;
                             else hi = mid;
                         }
-                        int first, n, L;
-                        sequence(p, lo, first, n, L, p.status);
-                        const int items = (n + rows2 - 1) / rows2, nt = (L + PR_BN - 1) / PR_BN;
-                        const int splits = nt > chunk ? (nt + chunk - 1) / chunk : 1;
-                        const int r = w - pref[lo], i = items - 1 - r / splits, s = r % splits;
-                        un.valid = 1;
+                        int i = w - pre[lo], s = 0;
                         un.b = lo;
+                        if (items <= PR_SORT) {
+                            s = i;
+                            i = plan.items()[lo] & 0xFFFF;
+                            un.b = plan.items()[lo] >> 16;
+                        }
+                        int first, n, L;
+                        sequence(p, un.b, first, n, L, nullptr);
+                        if (items > PR_SORT) i = items_of(p, n) - 1 - i;
+                        un.valid = 1;
                         un.g = u - w * p.Hkv;
                         un.tok0 = first + i * rows2;
                         un.npos = n - i * rows2;
@@ -384,9 +431,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                             const bool join = cut && s == 0;
                             p.ws_items[u] = PromptItem{un.tok0, un.npos, un.g, join ? s0 : 0, join ? s1 : 0};
                         }
-                        if (s > 0 && un.n0 == 0 && un.n1 == 0) continue;      // an early item of a cut sequence
-                    } else if (u < total || round * (int64_t)grid < total) {
-                        continue;                     // the last, partial round: the next one ends the list
                     }
                     const int st = published % PR_UNITS;
                     if (published >= PR_UNITS && !(ok = wait(u_empty + st * 8, (uint32_t)(published / PR_UNITS - 1) & 1u)))
@@ -420,14 +464,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             const CUtensorMap *map = is_v ? &tmv : &tmk;
             const uint64_t policy = l2_policy_evict_last();   // other row tiles read it again
             const int per_tile = PR_BN / p.bs;                // cache blocks per key tile
-            int issued = 0, raw = 0;
-            bool ok = true, to_raw = false;
+            int issued = 0;
+            bool ok = true;
             for (int c = 0; ok; ++c) {
                 const int st_u = c % PR_UNITS;
                 ok = __all_sync(0xffffffffu, wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u));
                 if (!ok) break;
                 const PromptUnit &un = units[st_u];
-                const int valid = un.valid, b = un.b, g = un.g, kt0 = un.kt0, nt = max(un.n0, un.n1), pos0 = un.pos0;
+                const int valid = un.valid, b = un.b, g = un.g, kt0 = un.kt0, nt = max(un.n0, un.n1);
                 const int seen = un.pos0 + min(un.npos, 2 * p.P);             // keys that any row of the unit sees
                 __syncwarp();
                 if (!valid) break;
@@ -450,10 +494,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     if (j + 1 < nt) id_next = lookup(j + 1);
                     const int t0 = (kt0 + j) * PR_BN, left = seen - t0;       // > 0
                     const int nblk = min(per_tile, (left + p.bs - 1) / p.bs);
-                    // some row does not see some key of this tile: V is looked over before it is released
-                    const bool look = is_v && t0 + PR_BN - 1 > pos0;
-                    const uint32_t bar = look ? v_raw : full0 + st * 8, dst = ring + st * S::KV_BYTES;
-                    to_raw = look;
+                    const uint32_t bar = full0 + st * 8, dst = ring + st * S::KV_BYTES;
                     if (lane == 0) mbar_arrive_expect_tx(bar, nblk * p.bs * D * 2);
                     __syncwarp();
                     if (lane < nblk) {
@@ -465,52 +506,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                     (id * p.Hkv + g) * (p.bs / 8), bar, policy);
                     }
                     ++issued;
-                    if (!look) continue;
-                    ok = __all_sync(0xffffffffu, wait(v_raw, (uint32_t)raw & 1u));
-                    if (!ok) break;
-                    ++raw;
-                    uint8_t *tile = smem + S::OFF_V + st * S::KV_BYTES;
-                    // rows behind the last position seen: other words of the pool, or what the stage held before.
-                    // Each 128-byte line is one key's half: [group][half][key in group]
-                    uint32_t acc = 0u;
-                    const int nline = PR_BN * S::HALVES;
-                    for (int l0 = 0; l0 < nline; l0 += 32) {                  // a line per lane and round
-                        const int l = l0 + lane;
-                        const int key = l / (8 * S::HALVES) * 8 + (l & 7);
-                        uint4 *line = reinterpret_cast<uint4 *>(tile + l * 128);
-                        if (key >= left) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) line[(i + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint4 w = line[(i + lane) & 7];
-                                acc = nonfinite_probe<T>(w.x, acc);
-                                acc = nonfinite_probe<T>(w.y, acc);
-                                acc = nonfinite_probe<T>(w.z, acc);
-                                acc = nonfinite_probe<T>(w.w, acc);
-                            }
-                        }
-                    }
-                    if (__any_sync(0xffffffffu, (acc & 0x7FFF7FFFu) != 0u)) {
-                        for (int l = lane; l < nline; l += 32) {
-                            uint16_t *w = reinterpret_cast<uint16_t *>(tile + l * 128);
-                            for (int i = 0; i < 64; ++i)
-                                if (is_nonfinite16<T>(w[i])) w[i] = 0;
-                        }
-                        if (lane == 0) units[st_u].poison = 1;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full0 + st * 8);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_empty + st_u * 8);
             }
             if (!ok) {                                // copies still in flight land before the block ends
-                for (int i = issued > nst ? issued - nst : 0; i < issued - (to_raw ? 1 : 0); ++i)
+                for (int i = issued > nst ? issued - nst : 0; i < issued; ++i)
                     mbar_wait_bounded(full0 + (i % nst) * 8, (uint32_t)(i / nst) & 1u, p.wait_ns);
-                if (to_raw) mbar_wait_bounded(v_raw, (uint32_t)raw & 1u, p.wait_ns);
             }
         } else {
             // ------------------------------------------------------------ MMA issue (lane 0)
@@ -674,7 +676,46 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 // the MMA thread asks for the weights alone: their V tile is waited for here
-                if (r == 0 && !wait(v_full + i_k % S::VST * 8, (uint32_t)(i_k / S::VST) & 1u)) *abort_flag = 1;
+                const uint32_t v_bar = v_full + i_k % S::VST * 8, v_phase = (uint32_t)(i_k / S::VST) & 1u;
+                if (t0 + PR_BN - 1 > un.pos0) {
+                    // some row does not see some key: V is looked over, a half key (128-byte line, [group][half][key
+                    // in group]) or two per thread
+                    if (!wait(v_bar, v_phase)) *abort_flag = 1;
+                    uint8_t *tile = smem + S::OFF_V + i_k % S::VST * S::KV_BYTES;
+                    const int left = un.pos0 + min(un.npos, 2 * p.P) - t0;
+                    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int q = 0; q < S::HALVES; ++q) {
+                        const int ln = q * PR_BM + r, key = ln / (8 * S::HALVES) * 8 + (ln & 7);
+                        uint4 *line = reinterpret_cast<uint4 *>(tile + ln * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (key >= left) {
+                                // behind the last position seen: other words of the pool, or what the stage held
+                                line[(i + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                const uint4 w = line[(i + lane) & 7];
+                                acc[0] = nonfinite_probe<T>(w.x, acc[0]);
+                                acc[1] = nonfinite_probe<T>(w.y, acc[1]);
+                                acc[2] = nonfinite_probe<T>(w.z, acc[2]);
+                                acc[3] = nonfinite_probe<T>(w.w, acc[3]);
+                            }
+                        }
+                    }
+                    if ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7FFF7FFFu) {
+                        // told before the words change: the other row tile may find them changed
+                        *reinterpret_cast<volatile int *>(&units[st_u].poison) = 1;
+                        __threadfence_block();
+                        for (int q = 0; q < S::HALVES; ++q) {
+                            uint16_t *w = reinterpret_cast<uint16_t *>(tile + (q * PR_BM + r) * 128);
+                            for (int i = 0; i < 64; ++i)
+                                if (is_nonfinite16<T>(w[i])) w[i] = 0;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                } else if (r == 0 && !wait(v_bar, v_phase)) {
+                    *abort_flag = 1;
+                }
                 __syncwarp();
                 mbar_arrive(p_full + t * 8);
                 // the sum is nobody's to wait for
@@ -699,7 +740,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < D; ++i) o[i] = 0.f;
             }
-            if (un.poison && live) {                  // values that are no numbers, at keys this row sees
+            if (*reinterpret_cast<volatile int *>(&units[st_u].poison) && live) {                  // values that are no numbers, at keys this row sees
                 const int end = min(lim + 1, key0 + nt * PR_BN);
                 for (int k = max(key0, un.pos0 / PR_BN * PR_BN); k < end; ++k) {
                     int id = __ldg(p.block_tables + (int64_t)un.b * p.stride + k / p.bs);
