@@ -192,7 +192,8 @@ pa_status pa_pool_create(const pa_pool_config *config, pa_pool **out) {
         return PA_ERR_OOM;
     }
     p->work = p->status + 8;
-    if (cudaStreamCreateWithFlags(&p->side, cudaStreamNonBlocking) != cudaSuccess ||
+    if ((c.kv_format == PA_KV_16BIT && setup_prompt(c.dtype, c.head_dim) != cudaSuccess) ||
+        cudaStreamCreateWithFlags(&p->side, cudaStreamNonBlocking) != cudaSuccess ||
         cudaEventCreateWithFlags(&p->ev_fork, cudaEventDisableTiming) != cudaSuccess ||
         cudaEventCreateWithFlags(&p->ev_join, cudaEventDisableTiming) != cudaSuccess) {
         cudaGetLastError();
@@ -662,7 +663,7 @@ pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, i
     PromptParams p;
     const pa_status st = packed_params(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, p);
     if (st != PA_OK) return st;
-    *bytes = 256 + (uint64_t)p.max_units * (PROMPT_ITEM_BYTES + prompt_slot_bytes(pool->cfg.head_dim));
+    *bytes = p.max_units == 0 ? 0 : 256 + (uint64_t)p.max_units * (PROMPT_ITEM_BYTES + prompt_slot_bytes(pool->cfg.head_dim));
     return PA_OK;
 }
 
@@ -678,7 +679,7 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
     if (num_tokens == 0 || num_seqs == 0) return PA_OK;
     uint64_t need = 0;
     pa_prefill_packed_workspace(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, &need);
-    if (!q || !out || !cu_q || !block_tables || !context_lens || !workspace || workspace_bytes < need)
+    if (!q || !out || !cu_q || !block_tables || !context_lens || (need > 0 && !workspace) || workspace_bytes < need)
         return PA_ERR_INVALID_ARG;
     const pa_pool_config &c = pool->cfg;
     if (!k_cache) {

@@ -169,6 +169,7 @@ cudaError_t launch_spec_verify(const float *p, const float *q, const int32_t *dr
 cudaError_t launch_rope_append(const RopeParams &p, int dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const CUtensorMap &tmq,
                           const CUtensorMap &tmk, const CUtensorMap &tmv, int sm_count, cudaStream_t stream);
+cudaError_t setup_prompt(int dtype, int head_dim);
 size_t prompt_slot_bytes(int head_dim);
 constexpr int PROMPT_ITEM_BYTES = 32;   // of the workspace per unit, beside its state
 cudaError_t launch_logits(const LogitsParams &p, bool probs, cudaStream_t stream);

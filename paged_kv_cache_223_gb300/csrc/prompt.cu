@@ -836,26 +836,47 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
         return r < p.P * p.G && pos < it.npos ? (int64_t)(it.tok0 + pos) * p.Hq + it.g * p.G + (r - rp * p.G) : -1;
     };
     const bool live = row_of(lane) >= 0;
+    if (__syncthreads_or(live) == 0) return;
     const size_t slot_bytes = (size_t)256 * (D + 2) * 4, step = (size_t)p.Hkv * slot_bytes;
     const uint8_t *ws = p.ws_slots + (size_t)u * slot_bytes;
     float M = -INFINITY, sum = 0.f;
     float4 acc[D / 32] = {};
     if (live) {
-        const float2 *ml = reinterpret_cast<const float2 *>(ws + (size_t)256 * D * 4) + r0 + lane;
-        for (int s = 0; s < splits; ++s)
-            M = fmaxf(M, reinterpret_cast<const float2 *>(reinterpret_cast<const uint8_t *>(ml) + s * step)->x);
-        for (int s = 0; s < splits; ++s) {
-            const float2 x = *reinterpret_cast<const float2 *>(reinterpret_cast<const uint8_t *>(ml) + s * step);
-            const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - M);
-            sum += w * x.y;
-            const float4 *o = reinterpret_cast<const float4 *>(ws + s * step) + r0 + lane;
+        // the running maximum again, over units, four of them in flight
+        constexpr int U = 4;
+        for (int s0 = 0; s0 < splits; s0 += U) {
+            float2 ml[U];
+            float4 o[U][D / 32];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const float4 y = o[(warp * (D / 32) + i) * 256];
-                acc[i].x += w * y.x;
-                acc[i].y += w * y.y;
-                acc[i].z += w * y.z;
-                acc[i].w += w * y.w;
+            for (int k = 0; k < U; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (s0 + k >= splits) continue;
+                const uint8_t *at = ws + (s0 + k) * step;
+                ml[k] = reinterpret_cast<const float2 *>(at + (size_t)256 * D * 4)[r0 + lane];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    o[k][i] = reinterpret_cast<const float4 *>(at)[(warp * (D / 32) + i) * 256 + r0 + lane];
+            }
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < U; ++k) m = fmaxf(m, ml[k].x);
+            const float w0 = M == -INFINITY ? 0.f : ex2_approx(M - m);
+            M = m;
+            sum *= w0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i].x *= w0, acc[i].y *= w0, acc[i].z *= w0, acc[i].w *= w0;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (s0 + k >= splits) continue;
+                const float w = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
+                sum += w * ml[k].y;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    acc[i].x += w * o[k][i].x;
+                    acc[i].y += w * o[k][i].y;
+                    acc[i].z += w * o[k][i].z;
+                    acc[i].w += w * o[k][i].w;
+                }
             }
         }
     }
@@ -876,14 +897,22 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
 template <typename T, int D>
 static cudaError_t launch_prompt_t(const PromptParams &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
                                    const CUtensorMap &tmv, int sm_count, cudaStream_t stream) {
-    // set on every call: the attribute belongs to the current device, and callers may use several
-    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PromptShape<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(prompt_kernel<T, D>, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream,
+    const cudaError_t e = launch_pdl(prompt_kernel<T, D>, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream,
                    tmq, tmk, tmv, p);
     if (e != cudaSuccess || p.max_units == 0) return e;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3((unsigned)p.max_units, 8u), dim3(256), 0, stream, p);
+    // 32 rows of an item per block; a call of few tokens has no more rows than they make
+    const int64_t rows = (int64_t)p.num_tokens * p.G;
+    const unsigned blocks = p.num_tokens <= p.P ? (unsigned)((rows + 31) / 32) : 8u;
+    return launch_pdl(prompt_join_kernel<T, D>, dim3((unsigned)p.max_units, blocks), dim3(256), 0, stream, p);
+}
+
+// The kernel's shared memory on the current device: once per pool, not per call.
+cudaError_t setup_prompt(int dtype, int head_dim) {
+    const void *k = dtype == PA_FP16 ? (head_dim == 64 ? (const void *)prompt_kernel<__half, 64> : (const void *)prompt_kernel<__half, 128>)
+                                     : (head_dim == 64 ? (const void *)prompt_kernel<__nv_bfloat16, 64>
+                                                       : (const void *)prompt_kernel<__nv_bfloat16, 128>);
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                head_dim == 64 ? PromptShape<64>::SMEM : PromptShape<128>::SMEM);
 }
 
 cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const CUtensorMap &tmq,

@@ -420,22 +420,25 @@ class Pool:
             _need(out, "out", dt, index, q.shape)
         if k_cache is not None or v_cache is not None:
             self._check_caches(k_cache, v_cache)
-        if workspace is None:
-            workspace = _new((self.packed_workspace(T, B, Hq, stride),), torch.uint8, self.device, stream)
+        size = 0
+        if workspace is not None:
+            size = workspace.numel()
+            _need(workspace, "workspace", torch.uint8, index, (size,))
         else:
-            _need(workspace, "workspace", torch.uint8, index, (workspace.numel(),))
+            size = self.packed_workspace(T, B, Hq, stride)
+            if size:
+                workspace = _new((size,), torch.uint8, self.device, stream)
         _check(_serving_lib().pa_prefill_packed(
             self.handle, q.data_ptr(), _ptr(k_cache), _ptr(v_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
-            context_lens.data_ptr(), T, B, Hq, float(scale), workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+            context_lens.data_ptr(), T, B, Hq, float(scale), _ptr(workspace), size, out.data_ptr(),
             _stream_on(stream, self.device)), "pa_prefill_packed")
         return out
 
     def packed_workspace(self, num_tokens: int, num_seqs: int, num_q_heads: int, block_table_stride: int) -> int:
-        """Workspace bytes of prefill_packed for these sizes (pa_prefill_packed_workspace)."""
+        """Workspace bytes of prefill_packed for these sizes (pa_prefill_packed_workspace; 0: none is needed)."""
         n = C.c_uint64()
         _check(_serving_lib().pa_prefill_packed_workspace(self.handle, num_tokens, num_seqs, num_q_heads,
-                                                          block_table_stride, C.byref(n)),
-               "pa_prefill_packed_workspace")
+                                                          block_table_stride, n), "pa_prefill_packed_workspace")
         return n.value
 
     def launches(self, block_table_stride: int, num_seqs: int, num_q_heads: int, q_len: int) -> int:

@@ -206,11 +206,14 @@ def test_refusals_on_the_host():
                 lambda: pool.prefill_packed(q[:, ::2], cu, tables, lens, scale)):
         with pytest.raises(ValueError):
             bad()
+    wide = torch.zeros(1, 200, dtype=torch.int32, device=DEV)      # tables that may hold contexts worth cutting
+    need = pool.packed_workspace(40, 1, 8, 200)
+    assert need > 0 and pool.packed_workspace(40, 1, 8, tables.shape[1]) == 0
     for bad in (lambda: pool.prefill_packed(q[:, :5].contiguous(), cu, tables, lens, scale),
                 lambda: pool.prefill_packed(q, cu, tables, lens, 0.0),
                 lambda: pool.prefill_packed(q, cu, tables, lens, math.nan),
-                lambda: pool.prefill_packed(q, cu, tables, lens, scale,
-                                            workspace=torch.empty(0, dtype=torch.uint8, device=DEV)),
+                lambda: pool.prefill_packed(q, cu, wide, lens, scale,
+                                            workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV)),
                 lambda: pool.packed_workspace(10, 5000, 8, 10)):
         with pytest.raises(pa.PagedAttnError):
             bad()
