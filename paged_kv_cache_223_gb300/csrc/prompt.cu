@@ -46,6 +46,7 @@
 // product with V takes it (half a step per weight, averaged over the keys: of the size of the output's own
 // rounding); the sum is of the unrounded weights. Keeping P in two 16-bit parts, as pa_prefill does for
 // bf16, costs half of the P V rate.
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -96,11 +97,13 @@ struct alignas(16) PromptUnit {
 };
 static_assert(sizeof(PromptUnit) == 64, "unit ring");
 
-// Header of the workspace, written by the main kernel for the joining one.
+// An item as the joining kernel needs it, written by the main kernel in the plan's order.
 struct PromptItem {
-    int tok0, npos, g;
+    int tok0, npos;
+    int first;                 // its first unit (of KV head 0)
     int splits0, splits1;      // units of row tile 0 and 1 (0: nothing to join)
 };
+static_assert(sizeof(PromptItem) <= PROMPT_ITEM_BYTES, "workspace items");
 
 size_t prompt_slot_bytes(int head_dim) { return (size_t)256 * (head_dim + 2) * 4; }
 
@@ -218,6 +221,16 @@ static_assert(3 * PR_SORT + 4 <= PA_PACKED_MAX_SEQS, "the sorted plan takes the 
 constexpr int PR_WHOLE = 1 << 24;
 
 __device__ __forceinline__ int items_of(const PromptParams &p, int n) { return (n + 2 * p.P - 1) / (2 * p.P); }
+
+// Key tiles of an item's row tiles, up to their last positions, and the units they are cut into.
+__device__ __forceinline__ void cuts(const PromptParams &p, int pos0, int npos, int chunk, int &s0, int &s1,
+                                     int *tiles0 = nullptr, int *tiles1 = nullptr) {
+    const int end0 = pos0 + min(npos, p.P), end1 = npos > p.P ? pos0 + min(npos, 2 * p.P) : 0;
+    const int e0 = end0 > 0 ? (end0 + PR_BN - 1) / PR_BN : 0, e1 = end1 > 0 ? (end1 + PR_BN - 1) / PR_BN : 0;
+    s0 = max(1, (e0 + chunk - 1) / chunk);
+    s1 = (e1 + chunk - 1) / chunk;
+    if (tiles0) *tiles0 = e0, *tiles1 = e1;
+}
 
 // Costs are in key tiles of work: a unit costs PLAN_UNIT more than its tiles, joining PLAN_JOIN.
 __device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, int lane) {
@@ -363,6 +376,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int chunk = plan.meta[1];
+    if (p.max_units > 0 && blockIdx.x == gridDim.x - 1) {             // a block that has no unit if any has none
+        const int n_items = chunk == PR_WHOLE ? 0 : plan.meta[0], rows2 = 2 * p.P;
+        if (tid == 0) *p.ws_total = n_items;
+        for (int k = tid; k < n_items; k += PR_THREADS) {
+            const int b = plan.items()[k] >> 16, i = plan.items()[k] & 0xFFFF;
+            int first, n, L;
+            sequence(p, b, first, n, L, nullptr);
+            const int npos = n - i * rows2, pos0 = L - n + i * rows2;
+            int s0, s1;
+            cuts(p, pos0, npos, chunk, s0, s1);
+            if (max(s0, s1) <= 1) s0 = s1 = 0;
+            p.ws_items[k] = PromptItem{first + i * rows2, npos, plan.units()[k], s0, s1};
+        }
+    }
 
     // A bounded wait that also ends when another role gave up.
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -389,7 +416,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 const uint64_t policy = l2_policy_evict_first();
                 int published = 0, qn[2] = {0, 0};
                 bool ok = true;
-                if (p.max_units > 0 && blockIdx.x == 0) *p.ws_total = total;
                 for (int round = 0; ok; ++round) {
                     const int u = round * grid + ((round & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
                     PromptUnit un = {};
@@ -418,19 +444,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         un.tok0 = first + i * rows2;
                         un.npos = n - i * rows2;
                         un.pos0 = L - n + i * rows2;
-                        // key tiles of each row tile: up to its last position
-                        const int end0 = un.pos0 + min(un.npos, p.P), end1 = un.npos > p.P ? un.pos0 + min(un.npos, rows2) : 0;
-                        const int e0 = end0 > 0 ? (end0 + PR_BN - 1) / PR_BN : 0, e1 = end1 > 0 ? (end1 + PR_BN - 1) / PR_BN : 0;
-                        const int s0 = max(1, (e0 + chunk - 1) / chunk), s1 = (e1 + chunk - 1) / chunk;
+                        int s0, s1, e0, e1;
+                        cuts(p, un.pos0, un.npos, chunk, s0, s1, &e0, &e1);
                         un.kt0 = s * chunk;
                         un.n0 = max(0, min(e0 - un.kt0, chunk));
                         un.n1 = max(0, min(e1 - un.kt0, chunk));
                         const bool cut = max(s0, s1) > 1;
                         un.slot = cut ? u : -1;
-                        if (u < p.max_units) {        // every unit's, where something may be cut
-                            const bool join = cut && s == 0;
-                            p.ws_items[u] = PromptItem{un.tok0, un.npos, un.g, join ? s0 : 0, join ? s1 : 0};
-                        }
                     }
                     const int st = published % PR_UNITS;
                     if (published >= PR_UNITS && !(ok = wait(u_empty + st * 8, (uint32_t)(published / PR_UNITS - 1) & 1u)))
@@ -825,15 +845,16 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
     __shared__ __align__(16) T rows[32][D + 8];
     pdl_wait();
-    const int u = blockIdx.x;
-    if (u >= *p.ws_total) return;
-    const PromptItem it = p.ws_items[u];
-    if (it.splits0 == 0) return;
+    const int k = blockIdx.x / p.Hkv, g = blockIdx.x - k * p.Hkv;
+    const int total = *p.ws_total;
+    const PromptItem it = p.ws_items[k];              // (behind the last: whatever the workspace holds)
+    if (k >= total || it.splits0 == 0) return;
+    const int u = it.first * p.Hkv + g;
     const int r0 = blockIdx.y * 32, t = r0 / PR_BM, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int splits = t ? it.splits1 : it.splits0;
     auto row_of = [&](int i) -> int64_t {             // output row of row i of this block, or -1
         const int r = (r0 & (PR_BM - 1)) + i, rp = r / p.G, pos = t * p.P + rp;
-        return r < p.P * p.G && pos < it.npos ? (int64_t)(it.tok0 + pos) * p.Hq + it.g * p.G + (r - rp * p.G) : -1;
+        return r < p.P * p.G && pos < it.npos ? (int64_t)(it.tok0 + pos) * p.Hq + g * p.G + (r - rp * p.G) : -1;
     };
     const bool live = row_of(lane) >= 0;
     if (__syncthreads_or(live) == 0) return;
@@ -900,10 +921,12 @@ static cudaError_t launch_prompt_t(const PromptParams &p, const CUtensorMap &tmq
     const cudaError_t e = launch_pdl(prompt_kernel<T, D>, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream,
                    tmq, tmk, tmv, p);
     if (e != cudaSuccess || p.max_units == 0) return e;
-    // 32 rows of an item per block; a call of few tokens has no more rows than they make
+    // 32 rows of an item and KV head per block; what is cut has fewer than max_units items, and a call of few tokens
+    // no more items and rows than they make
+    const int64_t items = ((int64_t)p.num_tokens / (2 * p.P) + std::min(p.num_tokens, p.num_seqs)) * p.Hkv;
     const int64_t rows = (int64_t)p.num_tokens * p.G;
-    const unsigned blocks = p.num_tokens <= p.P ? (unsigned)((rows + 31) / 32) : 8u;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3((unsigned)p.max_units, blocks), dim3(256), 0, stream, p);
+    const dim3 blocks((unsigned)std::min(items, (int64_t)p.max_units), p.num_tokens <= p.P ? (unsigned)((rows + 31) / 32) : 8u);
+    return launch_pdl(prompt_join_kernel<T, D>, blocks, dim3(256), 0, stream, p);
 }
 
 // The kernel's shared memory on the current device: once per pool, not per call.
