@@ -20,7 +20,7 @@
 //   warp 8, 11       K and V loads: one TMA copy per cache block, [8-key groups][64-dimension halves]
 //                    [8 keys][128 bytes] in shared memory, so that a whole block of tokens is one copy and
 //                    8-key groups stay a constant stride apart in the matrix descriptors
-//   warp 9           one thread issues every MMA: per key tile and row tile O += P V (P from tensor
+//   warp 9           issues every MMA: per key tile and row tile O += P V (P from tensor
 //                    memory, V MN-major), then S = Q K^T into the columns P came from, the row tiles in turn
 //                    so that one's products run while the other's softmax does
 //   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
@@ -152,27 +152,43 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// tcgen05.mma with descriptors as a constant upper word (128-byte swizzle, version, stride between 8-row groups)
-// and a lower word (address / 16, leading offset / 16 << 16).
+// The MMA warp runs as a whole, so that its control flow stays uniform; one lane (`lead`) issues. Descriptors are a
+// constant upper word (128-byte swizzle, version, stride between 8-row groups) and a lower word (address / 16,
+// leading offset / 16 << 16).
 __host__ __device__ constexpr uint32_t desc_hi(int group_stride) { return (uint32_t)(group_stride >> 4) | 1u << 14 | 2u << 29; }
 
-template <uint32_t HA, uint32_t HB>
-__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HA), "n"(HB));
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
 }
-
+template <uint32_t HA, uint32_t HB>
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HA), "n"(HB), "r"(lead));
+}
 // A in tensor memory.
 template <uint32_t HB>
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
         "mov.b64 db, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HB));
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HB), "r"(lead));
+}
+__device__ __forceinline__ void umma_commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 
 template <int RANK>
@@ -535,10 +551,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     mbar_wait_bounded(full0 + (i % nst) * 8, (uint32_t)(i / nst) & 1u, p.wait_ns);
             }
         } else {
-            // ------------------------------------------------------------ MMA issue (lane 0)
+            // ------------------------------------------------------------ MMA issue
             // One thread feeds the tensor cores, so what it does besides counts: descriptors are a constant upper
             // word and a lower one (address and leading offset) to which constants are added.
-            if (lane == 0) {
+            {
+                const uint32_t lead = elect_one();
                 constexpr uint32_t idesc_s = umma_idesc<T>(PR_BM, PR_BN, false);
                 constexpr uint32_t idesc_o = umma_idesc<T>(PR_BM, D, true);
                 constexpr uint32_t hi_q = desc_hi(1024), hi_kv = desc_hi(S::GROUP_BYTES);
@@ -561,11 +578,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t v = v_lo + last_vs * (S::KV_BYTES >> 4), pt = tmem + t * 256, ot = pt + 128;
-                    umma_ts<hi_kv>(ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
+                    umma_ts<hi_kv>(lead, ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
 #pragma unroll
                     for (int k = 1; k < PR_BN / 16; ++k)
-                        umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
-                    if (pj == pn - 1) umma_commit(o_done + t * 8);
+                        umma_ts<hi_kv>(lead, ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
+                    if (pj == pn - 1) umma_commit(lead, o_done + t * 8);
                     return true;
                 };
                 // S_t = Q_t K^T
@@ -579,10 +596,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     const uint32_t k = k_lo + ks * (S::KV_BYTES >> 4), q = q_lo + t * (S::Q_BYTES >> 4);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
-                        umma_ss<hi_q, hi_kv>(tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
+                        umma_ss<hi_q, hi_kv>(lead, tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
                                              k + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc_s, i > 0 ? 1u : 0u);
-                    umma_commit(s_full + t * 8);
-                    if (j == n - 1) umma_commit(q_empty + t * 8);
+                    umma_commit(lead, s_full + t * 8);
+                    if (j == n - 1) umma_commit(lead, q_empty + t * 8);
                     return true;
                 };
                 constexpr std::integral_constant<int, 0> T0{};
@@ -592,7 +609,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     if (!(ok = wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u))) break;
                     const int valid = units[st_u].valid, n0 = units[st_u].n0, n1 = units[st_u].n1;
                     if (!valid) break;
-                    mbar_arrive(u_empty + st_u * 8);
+                    if (lead) mbar_arrive(u_empty + st_u * 8);
                     const int nt = max(n0, n1);
                     for (int j = 0; j < nt; ++j) {
                         if (!(ok = wait(k_full + ks * 8, kph) && flush(T0, pn0))) break;
@@ -613,7 +630,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 if (ok) ok = flush(T0, pn0) && flush(T1, pn1);
                 if (!ok) {
-                    umma_commit(drain);
+                    umma_commit(lead, drain);
                     mbar_wait_bounded(drain, 0u, p.wait_ns);
                 }
             }
