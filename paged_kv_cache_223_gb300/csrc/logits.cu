@@ -20,6 +20,13 @@
 // bit 20 marks a prompt token, bits 21..31 hold 1 + the index of the last bias entry naming the token;
 // integer atomics, so the order of arrival changes nothing), and the first entry to claim a token's bit
 // replaces the token's word by the adjusted logit. The pass over the values only looks at the bits.
+//
+// Measured, 64 x 6 rows of 128256 fp32 logits: adjusting without lists 59 us (1.02 of the copy rate), with a history
+// of up to 4096 tokens, biases, drafts and masks 98 us; probabilities without lists 92 us, with them 150 us (0.40).
+// What is left is a block's chain of barriers (three for the lists, one of the cluster) with two blocks per SM to
+// overlap it: registers bound those. Not kept: penalties computed in the pass over the values (200 us), slices
+// dealt out in pieces of 128 or 2048 tokens so that the lists even out (lists 5 to 10 us less, the rest 13 to 20 us
+// more), the logits prefetched into L2 one round of blocks ahead and loaded behind the lists (150 us).
 #include "pa_device.cuh"
 
 namespace pa {

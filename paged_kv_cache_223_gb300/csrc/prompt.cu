@@ -25,13 +25,18 @@
 //                    so that one's products run while the other's softmax does
 //   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
 //                    [P positions][G heads][64 dimensions])
-// The MMA thread bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
+// The MMA warp bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
 // costs it 100 to 170, while the softmax is done 1000 cycles before its weights are asked for. So it waits for K
 // and the weights alone: one thread of each row tile's softmax waits for V before it hands the weights over, and
-// tells the loaders when a K tile (and the V tile before it) has been read. Measured, 4 x 4096 tokens, 64/8 heads
-// of 128, bf16: 780 us, 1410 TFLOP/s, against 1003 us with the waits, divisions and descriptors in that thread.
-// Not kept: an MMA thread per row tile, in turns or not (820, 940 us: their products interleave, or each turn
-// costs two waits), two softmax threads per row (936 us and more), weights handed over in halves (840 us).
+// tells the loaders when a K tile (and the V tile before it) has been read. Measured: 4 x 4096 tokens, 64 / 8
+// heads of 128, bf16: 770 us, 1430 TFLOP/s (0.75 of cuBLAS), against 1003 us with the waits, divisions and
+// descriptors in one thread of that warp. Not kept: an MMA warp per row tile, in turns or not (820, 940 us: their
+// products interleave, or each turn costs two waits), two softmax threads per row (936 us and more), weights
+// handed over in halves (840 us), barriers asked ahead of need (805 us).
+// 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 104 us (46 at the product's rate), of which the prologue and plan
+// take 5 and each of the up to 9 units per block about 3 at its end (masked tile, last product, stores). Heads of
+// 64: 60 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 68 us, 4.7 TB/s; its
+// key loop runs at 0.95 of the DRAM rate.
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
 //
@@ -643,6 +648,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const bool in_tile = r < p.P * p.G;
         const uint32_t tmem_s = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16), tmem_o = tmem_s + 128;
         uint8_t *stage = smem + S::OFF_STAGE + warp * 2048;
+        // fp16 weights are kept 2^7 times larger (at most 2^15 with the stale maximum's headroom; sum and O with them), so
+        // that small ones stay above the type's smallest number: off by 2^-32 of the largest weight at most, not 2^-25
+        constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
         int sc = 0, oc = 0, tiles = 0;                // scores and outputs taken; key tiles of the units before
         bool ok = true;
         for (int c = 0; ok; ++c) {
@@ -695,7 +703,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         tmem_st32(tmem_o + c0, a);
                     }
                 }
-                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + SHIFT;
                 const uint64_t sc2 = pair(p.scale_log2, p.scale_log2), nm2 = pair(nm, nm);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

@@ -21,7 +21,9 @@
 // load and store is a full vector and the pass-through dimensions take the same path; d / 16 threads
 // cover a head. The tile's sines and cosines are computed once per token into shared memory, in 16-byte
 // columns that the threads of a head read without bank conflicts. The first row of each thread is in
-// flight while they are computed, the next one while a row is rotated.
+// flight while they are computed, the next one while a row is rotated. Measured: 8192 tokens of 64 / 8 heads
+// of 128, slices of one projection's output, 56 us, 6.0 TB/s (0.89 of the copy rate; one element per thread,
+// heads in turn: 207 us); one token 2 us in a captured graph.
 #include <type_traits>
 
 #include "pa_device.cuh"

@@ -123,6 +123,25 @@ def test_peaked_and_flat_softmax():
         assert bool(((out.double() - ref).abs() <= tol).all())
 
 
+def test_many_small_weights_beside_a_large_one():
+    """One key takes nearly all the weight and has the value 0; the output is what 30000 keys of weight 2^-26 leave.
+    Each of them is off by at most 2^-32 of the largest weight in fp16 (a relative half step in bf16)."""
+    for dt in (FP, BF):
+        pool, q, cu, tables, lens, scale = make(61, [3], [29997], 4, 2, 128, dt, nan_slots=False)
+        bs = pool.geometry[2]
+        pool.k_cache.zero_(), pool.v_cache.fill_(1.0), q.zero_()
+        blk = int(tables[0, 0])
+        q[:, :, 0] = 4.0
+        pool.k_cache[blk, :, 5, 0] = 18.0 / (4.0 * scale)
+        pool.v_cache[blk, :, 5] = 0.0
+        out = pool.prefill_packed(q, cu, tables, lens, scale)
+        ref, mag = packed_attention(q, pool.k_cache, pool.v_cache, cu.tolist(), tables, lens.tolist(), scale)
+        assert 3e-4 < float(ref.min()) and float(ref.max()) < 6e-4
+        h = torch.finfo(dt).eps / 2
+        tol = ref * h + mag * (h * 1.01 + 2.0 ** -12) + 30000 * 2.0 ** -32
+        assert bool(((out.double() - ref).abs() <= tol).all()), float((out.double() / ref).min())
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("heads", [(8, 2), (4, 4)])
 def test_later_values_do_not_reach_earlier_rows(value, heads):
