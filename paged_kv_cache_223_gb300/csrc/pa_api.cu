@@ -480,6 +480,13 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
                                                                                                  : PA_ERR_CUDA;
 }
 
+// A launch's result as a status; an error is not left behind for the next caller that asks CUDA for the last one.
+static pa_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return PA_OK;
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+}
+
 pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
                          pa_rope **out) {
     if (!out) return PA_ERR_INVALID_ARG;
@@ -535,6 +542,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
     if (!pool || !rope || num_tokens < 0 || num_q_heads < 0 || num_q_heads > 65536) return PA_ERR_INVALID_ARG;
     const pa_pool_config &c = pool->cfg;
     if (rope->rot > c.head_dim || rope->device != c.device) return PA_ERR_INVALID_ARG;
+    if (num_q_heads + 2LL * c.num_kv_heads > 262144) return PA_ERR_UNSUPPORTED;
     if ((k_cache == nullptr) != (v_cache == nullptr)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
     if (!k || !v || !positions || !slot_mapping || (num_q_heads > 0 && (!q || !q_out))) return PA_ERR_INVALID_ARG;
@@ -577,7 +585,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
     p.fp8 = c.kv_format == PA_KV_FP8_E4M3;
     DeviceGuard g(c.device);
     if (!g.ok) return PA_ERR_CUDA;
-    return launch_rope_append(p, c.dtype, pool->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launched(launch_rope_append(p, c.dtype, pool->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 // The checks of pa_prefill_packed's sizes, shared with the workspace query.
@@ -635,9 +643,12 @@ static pa_status block_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return PA_ERR_CUDA;
-    if (pool->block_maps.size() > 4096) pool->block_maps.clear();
-    pool->block_maps.emplace(cache, m);
     *out = m;
+    try {
+        if (pool->block_maps.size() > 4096) pool->block_maps.clear();
+        pool->block_maps.emplace(cache, m);
+    } catch (const std::bad_alloc &) {                // the map is made again next time
+    }
     return PA_OK;
 }
 
@@ -709,10 +720,8 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
     if ((ms = q_map(p, c.dtype, c.head_dim, &tmq)) != PA_OK || (ms = block_map(pool, k_cache, &tmk)) != PA_OK ||
         (ms = block_map(pool, v_cache, &tmv)) != PA_OK)
         return ms;
-    return launch_prompt(p, c.dtype, c.head_dim, tmq, tmk, tmv, pool->sm_count, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    return launched(
+        launch_prompt(p, c.dtype, c.head_dim, tmq, tmk, tmv, pool->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) {
@@ -764,7 +773,7 @@ static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) 
     p.mask = a->mask;
     p.temperature = a->temperature;
     p.out = a->out;
-    return launch_logits(p, probs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launched(launch_logits(p, probs, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_adjust_logits(const pa_logits_args *args, void *stream) { return logits_call(args, false, stream); }
