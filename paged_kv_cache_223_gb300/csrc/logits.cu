@@ -28,6 +28,7 @@
 // dealt out in pieces of 128 or 2048 tokens so that the lists even out (lists 5 to 10 us less, the rest 13 to 20 us
 // more), the logits prefetched into L2 one round of blocks ahead and loaded behind the lists (150 us).
 #include "pa_device.cuh"
+#include "pa_serving.h"
 
 namespace pa {
 

@@ -55,6 +55,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_serving.h"
 
 namespace pa {
 
