@@ -20,7 +20,7 @@
 //   warp 8, 11       K and V loads: one TMA copy per cache block, [8-key groups][64-dimension halves]
 //                    [8 keys][128 bytes] in shared memory, so that a whole block of tokens is one copy and
 //                    8-key groups stay a constant stride apart in the matrix descriptors
-//   warp 9           issues every MMA: per key tile and row tile O += P V (P from tensor
+//   warp 9           one lane issues every MMA: per key tile and row tile O += P V (P from tensor
 //                    memory, V MN-major), then S = Q K^T into the columns P came from, the row tiles in turn
 //                    so that one's products run while the other's softmax does
 //   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
@@ -29,13 +29,14 @@
 // costs it 100 to 170, while the softmax is done 1000 cycles before its weights are asked for. So it waits for K
 // and the weights alone: one thread of each row tile's softmax waits for V before it hands the weights over, and
 // tells the loaders when a K tile (and the V tile before it) has been read. Measured: 4 x 4096 tokens, 64 / 8
-// heads of 128, bf16: 770 us, 1430 TFLOP/s (0.75 of cuBLAS), against 1003 us with the waits, divisions and
+// heads of 128, bf16: 778 us, 1410 TFLOP/s (0.74 of cuBLAS), against 1003 us with the waits, divisions and
 // descriptors in one thread of that warp. Not kept: an MMA warp per row tile, in turns or not (820, 940 us: their
 // products interleave, or each turn costs two waits), two softmax threads per row (936 us and more), weights
-// handed over in halves (840 us), barriers asked ahead of need (805 us).
-// 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 104 us (46 at the product's rate), of which the prologue and plan
+// handed over in halves (840 us), barriers asked ahead of need (805 us), the whole warp on its way with one lane
+// issuing (790 us with the lanes agreeing on every wait, which they must).
+// 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 108 us (46 at the product's rate), of which the prologue and plan
 // take 5 and each of the up to 9 units per block about 3 at its end (masked tile, last product, stores). Heads of
-// 64: 60 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 68 us, 4.7 TB/s; its
+// 64: 64 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 68 us, 4.7 TB/s; its
 // key loop runs at 0.95 of the DRAM rate.
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
@@ -158,43 +159,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// The MMA warp runs as a whole, so that its control flow stays uniform; one lane (`lead`) issues. Descriptors are a
-// constant upper word (128-byte swizzle, version, stride between 8-row groups) and a lower word (address / 16,
-// leading offset / 16 << 16).
+// tcgen05.mma with descriptors as a constant upper word (128-byte swizzle, version, stride between 8-row groups)
+// and a lower word (address / 16, leading offset / 16 << 16).
 __host__ __device__ constexpr uint32_t desc_hi(int group_stride) { return (uint32_t)(group_stride >> 4) | 1u << 14 | 2u << 29; }
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r;
-}
 template <uint32_t HA, uint32_t HB>
-__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HA), "n"(HB), "r"(lead));
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HA), "n"(HB));
 }
+
 // A in tensor memory.
 template <uint32_t HB>
-__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "mov.b64 db, {%2, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HB), "r"(lead));
-}
-__device__ __forceinline__ void umma_commit(uint32_t lead, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(lead)
-        : "memory");
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(HB));
 }
 
 template <int RANK>
@@ -557,11 +542,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     mbar_wait_bounded(full0 + (i % nst) * 8, (uint32_t)(i / nst) & 1u, p.wait_ns);
             }
         } else {
-            // ------------------------------------------------------------ MMA issue
+            // ------------------------------------------------------------ MMA issue (lane 0)
             // One thread feeds the tensor cores, so what it does besides counts: descriptors are a constant upper
             // word and a lower one (address and leading offset) to which constants are added.
-            {
-                const uint32_t lead = elect_one();
+            if (lane == 0) {
                 constexpr uint32_t idesc_s = umma_idesc<T>(PR_BM, PR_BN, false);
                 constexpr uint32_t idesc_o = umma_idesc<T>(PR_BM, D, true);
                 constexpr uint32_t hi_q = desc_hi(1024), hi_kv = desc_hi(S::GROUP_BYTES);
@@ -584,11 +568,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t v = v_lo + last_vs * (S::KV_BYTES >> 4), pt = tmem + t * 256, ot = pt + 128;
-                    umma_ts<hi_kv>(lead, ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
+                    umma_ts<hi_kv>(ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
 #pragma unroll
                     for (int k = 1; k < PR_BN / 16; ++k)
-                        umma_ts<hi_kv>(lead, ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
-                    if (pj == pn - 1) umma_commit(lead, o_done + t * 8);
+                        umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
+                    if (pj == pn - 1) umma_commit(o_done + t * 8);
                     return true;
                 };
                 // S_t = Q_t K^T
@@ -602,10 +586,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     const uint32_t k = k_lo + ks * (S::KV_BYTES >> 4), q = q_lo + t * (S::Q_BYTES >> 4);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
-                        umma_ss<hi_q, hi_kv>(lead, tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
+                        umma_ss<hi_q, hi_kv>(tmem + t * 256, q + (((i >> 2) * (PR_BM * 128) + (i & 3) * 32) >> 4),
                                              k + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), idesc_s, i > 0 ? 1u : 0u);
-                    umma_commit(lead, s_full + t * 8);
-                    if (j == n - 1) umma_commit(lead, q_empty + t * 8);
+                    umma_commit(s_full + t * 8);
+                    if (j == n - 1) umma_commit(q_empty + t * 8);
                     return true;
                 };
                 constexpr std::integral_constant<int, 0> T0{};
@@ -615,7 +599,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     if (!(ok = wait(u_full + st_u * 8, (uint32_t)(c / PR_UNITS) & 1u))) break;
                     const int valid = units[st_u].valid, n0 = units[st_u].n0, n1 = units[st_u].n1;
                     if (!valid) break;
-                    if (lead) mbar_arrive(u_empty + st_u * 8);
+                    mbar_arrive(u_empty + st_u * 8);
                     const int nt = max(n0, n1);
                     for (int j = 0; j < nt; ++j) {
                         if (!(ok = wait(k_full + ks * 8, kph) && flush(T0, pn0))) break;
@@ -636,7 +620,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 if (ok) ok = flush(T0, pn0) && flush(T1, pn1);
                 if (!ok) {
-                    umma_commit(lead, drain);
+                    umma_commit(drain);
                     mbar_wait_bounded(drain, 0u, p.wait_ns);
                 }
             }
