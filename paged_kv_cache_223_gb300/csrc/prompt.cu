@@ -25,18 +25,18 @@
 //                    so that one's products run while the other's softmax does
 //   warp 10          decodes units into a ring that all roles read, and loads their Q tiles (a TMA box of
 //                    [P positions][G heads][64 dimensions])
-// The MMA warp bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
+// The MMA thread bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
 // costs it 100 to 170, while the softmax is done 1000 cycles before its weights are asked for. So it waits for K
 // and the weights alone: one thread of each row tile's softmax waits for V before it hands the weights over, and
 // tells the loaders when a K tile (and the V tile before it) has been read. Measured: 4 x 4096 tokens, 64 / 8
-// heads of 128, bf16: 778 us, 1410 TFLOP/s (0.74 of cuBLAS), against 1003 us with the waits, divisions and
+// heads of 128, bf16: 780 us, 1410 TFLOP/s (0.74 of cuBLAS), against 1003 us with the waits, divisions and
 // descriptors in one thread of that warp. Not kept: an MMA warp per row tile, in turns or not (820, 940 us: their
 // products interleave, or each turn costs two waits), two softmax threads per row (936 us and more), weights
 // handed over in halves (840 us), barriers asked ahead of need (805 us), the whole warp on its way with one lane
 // issuing (790 us with the lanes agreeing on every wait, which they must).
 // 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 108 us (46 at the product's rate), of which the prologue and plan
 // take 5 and each of the up to 9 units per block about 3 at its end (masked tile, last product, stores). Heads of
-// 64: 64 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 68 us, 4.7 TB/s; its
+// 64: 65 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 70 us, 4.6 TB/s; its
 // key loop runs at 0.95 of the DRAM rate.
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
