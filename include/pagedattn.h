@@ -215,7 +215,9 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
  * The frequencies are kept as turns per position in 64-bit fixed point, so the
  * angle is exact to p * 2^-64 turns (plus the frequency's own rounding, 2^-64
  * turns per position) at any 32-bit position.
- * Synchronises the device. Errors: PA_ERR_INVALID_ARG, PA_ERR_OOM, PA_ERR_CUDA.
+ * Synchronises the device. A rope is kept for as long as calls with it, or
+ * graphs that captured them, may still run.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_OOM, PA_ERR_CUDA.
  */
 typedef struct pa_rope pa_rope;
 pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
@@ -237,7 +239,8 @@ void pa_rope_destroy(pa_rope *rope);
  *   slot_mapping  device int64 [num_tokens]
  *   num_q_heads   >= 0; 0 appends without a q (q and q_out are then ignored)
  *   q_out         device rows, q_out_stride as above; may be q itself with the same stride,
- *                 must not overlap the inputs otherwise
+ *                 must not overlap the rows of q, k and v otherwise (PA_ERR_INVALID_ARG, also where
+ *                 rows of different strides lie in between one another)
  *   k_cache/v_cache  device pools to write, or NULL for the pool's own
  * The rope's rot_dim is at most the pool's head_dim, and its device the pool's.
  */
@@ -255,7 +258,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  * (context_lens[b] = n_b), prompts with a cached prefix, chunks and single
  * tokens may be mixed. Values at positions a row does not see (later tokens,
  * unwritten slots) do not reach it, whatever their words are.
- *   q, out         device [num_tokens, num_q_heads, head_dim], not overlapping
+ *   q, out         device [num_tokens, num_q_heads, head_dim], not overlapping (PA_ERR_INVALID_ARG)
  *   cu_q           device int32 [num_seqs + 1], 0 <= cu_q[b] <= cu_q[b+1] <= num_tokens;
  *                  rows before cu_q[0] and from cu_q[num_seqs] on are left as they are in out
  *   block_tables   device int32 [num_seqs, block_table_stride]; entries at or beyond
@@ -415,7 +418,8 @@ typedef struct pa_logits_args {
     const float *temperature;  /* device [num_seqs], >= 0 (pa_token_probs; ignored by pa_adjust_logits);
                                   a negative or NaN one makes its rows NaN */
     float *out;                /* device fp32 [num_seqs, rows_per_seq, vocab]; may be logits itself (fp32,
-                                  same strides), must not overlap the inputs otherwise */
+                                  same strides), must not lie between the first and the last
+                                  logit otherwise (PA_ERR_INVALID_ARG), nor overlap the lists */
 } pa_logits_args;
 
 /* Token ids outside the vocabulary (in history, draft or bias_tokens; -1 as padding) are ignored. No pool

@@ -27,7 +27,6 @@ struct pa_pool {
     cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
     std::mutex mu;
     std::unordered_map<const void *, CUtensorMap> maps;
-    std::unordered_map<const void *, CUtensorMap> block_maps;   // packed prompts: one box per block
 };
 
 namespace pa {

@@ -24,6 +24,18 @@ static pa_status launched(cudaError_t e) {
     return PA_ERR_CUDA;
 }
 
+using wide = __int128;                                // strides are the caller's: no product of them overflows
+
+// Do n rows of a_row bytes at a, a_stride bytes apart, share a byte with such rows at b? Rows of different strides
+// count as sharing where their spans meet.
+static bool rows_meet(const void *a, wide a_row, wide a_stride, const void *b, wide b_row, wide b_stride, wide n) {
+    const wide x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    if (x + (n - 1) * a_stride + a_row <= y || y + (n - 1) * b_stride + b_row <= x) return false;
+    if (n == 1 || a_stride != b_stride) return true;
+    const wide d = ((y - x) % a_stride + a_stride) % a_stride;     // b's column, with a's at 0
+    return d < a_row || d + b_row > a_stride;
+}
+
 pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
                          pa_rope **out) {
     if (!out) return PA_ERR_INVALID_ARG;
@@ -55,7 +67,9 @@ pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interl
         delete r;
         return PA_ERR_OOM;
     }
-    if (cudaMemcpy(r->freq, f, sizeof(uint64_t) * (rot_dim / 2), cudaMemcpyHostToDevice) != cudaSuccess) {
+    // a copy from pageable memory may return before it has landed: streams that do not wait for the default one read it
+    if (cudaMemcpy(r->freq, f, sizeof(uint64_t) * (rot_dim / 2), cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(r->freq);
         delete r;
@@ -91,6 +105,12 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
     if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0) return PA_ERR_INVALID_ARG;
     if (num_q_heads > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 != 0 || q_out_stride % 8 != 0 ||
                             (q == q_out && q_stride != q_out_stride) || !aligned16(q) || !aligned16(q_out)))
+        return PA_ERR_INVALID_ARG;
+    const auto meets_out = [&](const void *x, int64_t row, int64_t stride) {
+        return rows_meet(q_out, 2 * q_row, (wide)2 * q_out_stride, x, 2 * row, (wide)2 * stride, num_tokens);
+    };
+    if (num_q_heads > 0 &&
+        ((q != q_out && meets_out(q, q_row, q_stride)) || meets_out(k, kv_row, k_stride) || meets_out(v, kv_row, v_stride)))
         return PA_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
@@ -159,34 +179,20 @@ static pa_status packed_params(const pa_pool *pool, int32_t num_tokens, int32_t 
 
 // The pool as a 4-D tensor for copies of whole blocks: [8 tokens x 64 dimensions], the dimension halves, groups of
 // eight tokens. One box is a block's rows of one KV head, 128-byte swizzled.
-static pa_status block_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
-    std::lock_guard<std::mutex> lk(pool->mu);
-    auto it = pool->block_maps.find(cache);
-    if (it != pool->block_maps.end()) {
-        *out = it->second;
-        return PA_OK;
-    }
+static pa_status block_map(const pa_pool_config &c, const void *cache, CUtensorMap *out) {
     auto fn = encode_fn();
     if (!fn) return PA_ERR_CUDA;
-    const pa_pool_config &c = pool->cfg;
     const cuuint64_t row = (cuuint64_t)c.head_dim * 2, groups = (cuuint64_t)c.num_blocks * c.num_kv_heads * c.block_size / 8;
     cuuint64_t dims[4] = {64, 8, (cuuint64_t)c.head_dim / 64, groups};
     cuuint64_t strides[3] = {row, 128, 8 * row};
     cuuint32_t box[4] = {64, 8, (cuuint32_t)c.head_dim / 64, (cuuint32_t)c.block_size / 8};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUtensorMap m;
-    if (fn(&m, c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-           const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return PA_ERR_CUDA;
-    *out = m;
-    try {
-        if (pool->block_maps.size() > 4096) pool->block_maps.clear();
-        pool->block_maps.emplace(cache, m);
-    } catch (const std::bad_alloc &) {                // the map is made again next time
-    }
-    return PA_OK;
+    return fn(out, c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 // q [num_tokens, Hq, head_dim] for boxes of P positions x G heads x 64 dimensions.
@@ -238,6 +244,9 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
         (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_q) & 3u))
         return PA_ERR_INVALID_ARG;
+    const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+    if ((qa < oa ? oa - qa : qa - oa) < (uintptr_t)num_tokens * num_q_heads * c.head_dim * 2)
+        return PA_ERR_INVALID_ARG;                    // a unit's rows would be written while another still reads them
     p.q = q;
     p.out = out;
     p.k_cache = k_cache;
@@ -254,8 +263,8 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
     if (!g.ok) return PA_ERR_CUDA;
     CUtensorMap tmq, tmk, tmv;
     pa_status ms;
-    if ((ms = q_map(p, c.dtype, c.head_dim, &tmq)) != PA_OK || (ms = block_map(pool, k_cache, &tmk)) != PA_OK ||
-        (ms = block_map(pool, v_cache, &tmv)) != PA_OK)
+    if ((ms = q_map(p, c.dtype, c.head_dim, &tmq)) != PA_OK || (ms = block_map(c, k_cache, &tmk)) != PA_OK ||
+        (ms = block_map(c, v_cache, &tmv)) != PA_OK)
         return ms;
     return launched(
         launch_prompt(p, c.dtype, c.head_dim, tmq, tmk, tmv, pool->sm_count, static_cast<cudaStream_t>(stream)));
@@ -286,6 +295,9 @@ static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) 
     const bool in_place = a->logits == static_cast<const void *>(a->out);
     if (in_place && (a->dtype != PA_LOGITS_FP32 || (R > 1 && a->row_stride != V) ||
                      (a->num_seqs > 1 && a->seq_stride != R * V)))
+        return PA_ERR_INVALID_ARG;
+    const wide span = (wide)(a->num_seqs - 1) * a->seq_stride + (wide)(R - 1) * a->row_stride + V;
+    if (!in_place && rows_meet(a->logits, span * (int)esize, 0, a->out, 4 * a->num_seqs * R * V, 0, 1))
         return PA_ERR_INVALID_ARG;
     LogitsParams p;
     p.logits = a->logits;

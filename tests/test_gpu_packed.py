@@ -225,6 +225,10 @@ def test_refusals_on_the_host():
                 lambda: pool.prefill_packed(q[:, ::2], cu, tables, lens, scale)):
         with pytest.raises(ValueError):
             bad()
+    both = torch.zeros(48, 8, 128, dtype=BF, device=DEV)
+    for o in (q, both[8:]):                                        # out over q's own words, whole or in part
+        with pytest.raises(pa.PagedAttnError):
+            pool.prefill_packed(q if o is q else both[:40], cu, tables, lens, scale, out=o)
     wide = torch.zeros(1, 200, dtype=torch.int32, device=DEV)      # tables that may hold contexts worth cutting
     need = pool.packed_workspace(40, 1, 8, 200)
     assert need > 0 and pool.packed_workspace(40, 1, 8, tables.shape[1]) == 0

@@ -193,6 +193,12 @@ def test_refusals_on_the_host():
     buf = torch.empty(9 * 4 * 64 + 1, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(pa.PagedAttnError):       # rows that do not start on 16 bytes
         pool.rope_append(buf[1:].view(9, 4, 64), k, v, pos, slots, rope)
+    rows = torch.zeros(10, 12, 64, dtype=torch.bfloat16, device=DEV)          # q | k | v | room for an output
+    q, k, v, room = rows[:9, :4], rows[:9, 4:6], rows[:9, 6:8], rows[:9, 8:]
+    for over in (rows[:9, 1:5], rows[:9, 3:7], rows[:9, 7:11], rows[1:, :4], rows.view(-1)[:9 * 4 * 64].view(9, 4, 64)):
+        with pytest.raises(pa.PagedAttnError):   # an output over other rows of q, or of k or v
+            pool.rope_append(q, k, v, pos, slots, rope, q_out=over)
+    assert pool.rope_append(q, k, v, pos, slots, rope, q_out=room) is room
     e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
     out = pool.rope_append(e, e[:, :2], e[:, :2], pos[:0], slots[:0], rope)
     assert out.shape == (0, 4, 64)

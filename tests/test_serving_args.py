@@ -55,7 +55,8 @@ def test_logits_arguments(pa):
                        dict(row_stride=-8), dict(history_stride=-1), dict(dtype=3), dict(dtype=-1), dict(logits=None),
                        dict(out=None), dict(history_lens=None), dict(bias_tokens=None), dict(bias_values=None),
                        dict(logits=1026), dict(dtype=0, logits=1025), dict(mask=1027), dict(out=4098),
-                       dict(out=1024, row_stride=104), dict(out=1024, seq_stride=208), dict(out=1024, dtype=1)):
+                       dict(out=1024, row_stride=104), dict(out=1024, seq_stride=208), dict(out=1024, dtype=1),
+                       dict(out=1424), dict(out=1020), dict(out=1024 + 1596)):     # over some of the logits: 400 floats at 1024
             assert f(C.byref(logits_args(pa, **change)), None) == pa.PA_ERR_INVALID_ARG, change
         for change in (dict(vocab=393217), dict(history_stride=1000001), dict(num_bias=2001), dict(rows_per_seq=4097),
                        dict(num_seqs=1 << 23)):
