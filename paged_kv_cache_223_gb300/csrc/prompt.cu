@@ -37,7 +37,7 @@
 // 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 108 us (46 at the product's rate), of which the prologue and plan
 // take 5 and each of the up to 9 units per block about 3 at its end (masked tile, last product, stores). Heads of
 // 64: 65 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 70 us, 4.6 TB/s; its
-// key loop runs at 0.95 of the DRAM rate.
+// key loop runs at 0.94 of the DRAM rate.
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
 //
