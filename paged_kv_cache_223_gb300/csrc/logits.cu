@@ -405,8 +405,9 @@ static cudaError_t launch_ng(const LogitsParams &p, int slice, int slices, cudaS
     const bool lists = p.history || p.draft || p.num_bias > 0;
     const size_t smem = lists ? (size_t)slice * 4 + slice / 8 + LG_KEPT * 2 : 0;
     auto kernel = logits_kernel<PROBS, VEC, NG>;
-    // set on every call: the attribute belongs to the current device, and callers may use several
-    if (smem > 48 * 1024) {
+    // from where it may pass 48 KB with the fixed part; set on every call: the attribute belongs to the current device,
+    // and callers may use several
+    if (smem > 32 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  NG * LG_GROUP * 4 + NG * LG_GROUP / 8 + LG_KEPT * 2);

@@ -80,6 +80,18 @@ def test_parity(case):
     close_probs(pa.token_probs(logits, t, **kw), probs(ref, t), mag, t)
 
 
+@pytest.mark.parametrize("V", [9100, 9500, 36800, 40000, 72960, 76032, 79400])
+def test_slices_whose_table_ends_near_48_kb(V):
+    """Tables that reach the shared memory a launch has by default only together with the kernel's fixed part."""
+    logits, kw, t = make(29, 2, 1, V, torch.float32, 100, 9, True, False, 0)
+    ref, mag = adjusted(logits, **kw)
+    close_adjusted(pa.adjust_logits(logits, **kw), ref, mag)
+    close_probs(pa.token_probs(logits, t, **kw), probs(ref, t), mag, t)
+    many = make(30, 320, 1, V, torch.bfloat16, 20, 2, False, False, 0)       # rows that fill the GPU: fewest slices
+    ref, mag = adjusted(many[0], **many[1])
+    close_adjusted(pa.adjust_logits(many[0], **many[1]), ref, mag)
+
+
 @pytest.mark.parametrize("left_out", ["history", "repetition", "presence", "frequency", "bias", "mask", "draft",
                                       "prompt_lens", "all"])
 def test_each_list_may_be_missing(left_out):
