@@ -22,7 +22,9 @@
 // replaces the token's word by the adjusted logit. The pass over the values only looks at the bits.
 //
 // Measured, 64 x 6 rows of 128256 fp32 logits: adjusting without lists 59 us (1.02 of the copy rate), with a history
-// of up to 4096 tokens, biases, drafts and masks 98 us; probabilities without lists 92 us, with them 150 us (0.40).
+// of up to 4096 tokens, biases, drafts and masks 87 us; probabilities without lists 92 us, with them 141 us (0.42), of
+// which counting takes about 22 and the adjusted logits 16 (entries kept in one list of the block, with the positions
+// from shared atomics, and eight entries held per thread, which spilled: 151 us).
 // What is left is a block's chain of barriers (three for the lists, one of the cluster) with two blocks per SM to
 // overlap it: registers bound those. Not kept: penalties computed in the pass over the values (200 us), slices
 // dealt out in pieces of 128 or 2048 tokens so that the lists even out (lists 5 to 10 us less, the rest 13 to 20 us
@@ -41,7 +43,8 @@ constexpr int LG_BIAS_SHIFT = 21;
 static_assert(PA_LOGITS_MAX_HISTORY + 4096 <= (int)LG_COUNT, "an output count fits its field");
 static_assert(PA_LOGITS_MAX_BIAS + 1 < (1 << (32 - LG_BIAS_SHIFT)), "a bias index fits its field");
 constexpr int LG_MAX_SLICES = 8;                      // blocks of a row: a portable cluster
-constexpr int LG_KEPT = 4096;                         // entries of a slice kept in shared memory
+constexpr int LG_KEPT = 384;                          // entries of a slice that a warp keeps in shared memory
+constexpr int LG_KEPT_BYTES = LG_THREADS / 32 * LG_KEPT * 2;
 static_assert(PA_LOGITS_MAX_VOCAB <= 8 * 65536, "a token within a slice fits 16 bits of an entry");
 static_assert(PA_LOGITS_MAX_VOCAB <= 8 * 24 * LG_GROUP, "a cluster holds the largest row");
 
@@ -52,27 +55,21 @@ struct RowPart {
 
 // The lists of a row, and this thread's first entries of them, loaded before the logits are (behind those, a
 // list's latency would be theirs too).
-constexpr int LG_HELD = 8;
+constexpr int LG_HELD = 6;
 struct RowLists {
-    const int32_t *bias, *hist, *draft;
-    int num_bias, cap, len, prompt, drafts;
-    int bias0, draft0, hist0[LG_HELD];
+    int len, prompt, bias0, draft0, hist0[LG_HELD];
 };
 
 __device__ __forceinline__ void load_lists(const LogitsParams &p, int b, int j, int tid, RowLists &l) {
-    l.bias = p.bias_tokens + (int64_t)b * p.num_bias;
-    l.hist = p.history + b * p.history_stride;
-    l.draft = p.draft + (int64_t)b * (p.R - 1);
-    l.num_bias = p.num_bias;
-    l.cap = p.history ? p.history_cap : 0;
-    l.drafts = p.draft ? j : 0;
-    l.len = l.cap > 0 ? __ldg(p.history_lens + b) : 0;
-    l.prompt = l.cap > 0 && p.prompt_lens ? __ldg(p.prompt_lens + b) : 0;
-    l.bias0 = tid < l.num_bias ? __ldg(l.bias + tid) : -1;
-    l.draft0 = tid < l.drafts ? __ldg(l.draft + tid) : -1;
+    const int cap = p.history ? p.history_cap : 0;
+    l.len = cap > 0 ? __ldg(p.history_lens + b) : 0;
+    l.prompt = cap > 0 && p.prompt_lens ? __ldg(p.prompt_lens + b) : 0;
+    l.bias0 = tid < p.num_bias ? __ldg(p.bias_tokens + (int64_t)b * p.num_bias + tid) : -1;
+    l.draft0 = p.draft && tid < j ? __ldg(p.draft + b * (p.R - 1) + tid) : -1;
+    const int32_t *hist = p.history + b * p.history_stride;
 #pragma unroll
     for (int k = 0; k < LG_HELD; ++k)
-        l.hist0[k] = tid + k * LG_THREADS < l.cap ? __ldg(l.hist + tid + k * LG_THREADS) : -1;
+        l.hist0[k] = tid + k * LG_THREADS < cap ? __ldg(hist + tid + k * LG_THREADS) : -1;
 }
 
 __device__ __forceinline__ float load_logit(const LogitsParams &p, int64_t i) {
@@ -83,20 +80,21 @@ __device__ __forceinline__ float load_logit(const LogitsParams &p, int64_t i) {
 
 // Adjusted logits of the listed tokens of the slice [base, base + n) (entries that name another slice's token,
 // or none, are left to others): bit t of `bits` set, the fp32 word in table[t]. `off`: the slice's first logit.
-// Tokens that entries named are kept for the last step; a slice with more than LG_KEPT such entries (a long
-// history of few different tokens) reads the lists again for it. table, bits and *s_kept come zeroed.
-__device__ __forceinline__ void adjust_listed(const LogitsParams &p, RowLists &l, int b, int base, int n, int64_t off,
-                                              uint32_t *table, uint32_t *bits, uint16_t *kept, int *s_kept, int tid) {
+// Each warp keeps the tokens that its entries named for the last step; one with more than LG_KEPT of them (a long
+// history of few different tokens) reads its entries again for it. table and bits come zeroed.
+__device__ __forceinline__ void adjust_listed(const LogitsParams &p, RowLists &l, int b, int j, int base, int n, int64_t off,
+                                              uint32_t *table, uint32_t *bits, uint16_t *kept, int tid) {
     const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
     const float freq = p.frequency ? __ldg(p.frequency + b) : 0.f, pres = p.presence ? __ldg(p.presence + b) : 0.f;
     const int lane = tid & 31, first = tid - lane;
-    const int len = l.len < 0 ? 0 : (l.len > l.cap ? l.cap : l.len);
+    const int cap = p.history ? p.history_cap : 0, len = l.len < 0 ? 0 : (l.len > cap ? cap : l.len);
+    const int drafts = p.draft ? j : 0;
     // fn(token within the slice, or a negative number; index in the list), by whole warps
     auto local = [&](int t) { return t >= base && t - base < n ? t - base : -1; };
     auto biases = [&](auto &&fn) {
-        for (int i0 = first; i0 < l.num_bias; i0 += LG_THREADS) {
+        for (int i0 = first; i0 < p.num_bias; i0 += LG_THREADS) {
             const int i = i0 + lane;
-            fn(local(i0 == first ? l.bias0 : (i < l.num_bias ? __ldg(l.bias + i) : -1)), i);
+            fn(local(i0 == first ? l.bias0 : (i < p.num_bias ? __ldg(p.bias_tokens + (int64_t)b * p.num_bias + i) : -1)), i);
         }
     };
     auto tokens = [&](auto &&fn) {
@@ -110,25 +108,25 @@ __device__ __forceinline__ void adjust_listed(const LogitsParams &p, RowLists &l
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = i0 + lane + k * LG_THREADS;
-                t[k] = i < len ? __ldg(l.hist + i) : -1;
+                t[k] = i < len ? __ldg(p.history + b * p.history_stride + i) : -1;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) fn(local(t[k]), i0 + lane + k * LG_THREADS);
         }
-        for (int i0 = first; i0 < l.drafts; i0 += LG_THREADS) {
+        for (int i0 = first; i0 < drafts; i0 += LG_THREADS) {
             const int i = i0 + lane;
-            fn(local(i0 == first ? l.draft0 : (i < l.drafts ? __ldg(l.draft + i) : -1)), 0x7fffffff);
+            fn(local(i0 == first ? l.draft0 : (i < drafts ? __ldg(p.draft + b * (p.R - 1) + i) : -1)), 0x7fffffff);
         }
     };
-    auto keep = [&](int t) {                          // one addition to the shared count per warp
+    kept += (tid >> 5) * LG_KEPT;
+    int count = 0;                                    // of this warp's entries
+    auto keep = [&](int t) {
         const uint32_t all = __ballot_sync(0xffffffffu, t >= 0);
-        if (all == 0u) return;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(s_kept, __popc(all));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1u));
+        const int at = count + __popc(all & ((1u << lane) - 1u));
         if (t >= 0 && at < LG_KEPT) kept[at] = (uint16_t)t;
+        count += __popc(all);
     };
-    if (l.num_bias > 0) {
+    if (p.num_bias > 0) {
         biases([&](int t, int i) {
             keep(t);
             if (t >= 0) atomicMax(table + t, (uint32_t)(i + 1) << LG_BIAS_SHIFT);
@@ -155,9 +153,8 @@ __device__ __forceinline__ void adjust_listed(const LogitsParams &p, RowLists &l
             x = __fadd_rn(x, __ldg(p.bias_values + (int64_t)b * p.num_bias + (w >> LG_BIAS_SHIFT) - 1));
         table[t] = __float_as_uint(x);
     };
-    const int count = *s_kept;
     if (count <= LG_KEPT) {
-        for (int i = tid; i < count; i += LG_THREADS) adjust(kept[i]);
+        for (int i = lane; i < count; i += 32) adjust(kept[i]);
     } else {
         auto each = [&](int t, int) {
             if (t >= 0) adjust(t);
@@ -192,7 +189,6 @@ __global__ void __launch_bounds__(LG_THREADS, NG <= 8 ? 2 : 1) logits_kernel(con
     extern __shared__ __align__(16) uint32_t lg_table[];
     __shared__ RowPart s_parts[LG_MAX_SLICES][LG_THREADS / 32];
     __shared__ uint32_t s_mask[NG * LG_GROUP / 32];
-    __shared__ int s_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / slices, rank = blockIdx.x - row * slices;
     const int b = row / p.R, j = row - b * p.R;
@@ -208,7 +204,6 @@ __global__ void __launch_bounds__(LG_THREADS, NG <= 8 ? 2 : 1) logits_kernel(con
         load_lists(p, b, j, tid, l);
         for (int i = tid * 4; i < slice + slice / 32; i += LG_THREADS * 4)
             *reinterpret_cast<uint4 *>(lg_table + i) = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0) s_kept = 0;
     }
     float T = 0.f;
     if constexpr (PROBS) T = __ldg(p.temperature + b);
@@ -259,8 +254,7 @@ __global__ void __launch_bounds__(LG_THREADS, NG <= 8 ? 2 : 1) logits_kernel(con
     }
     __syncthreads();
     if (lists)
-        adjust_listed(p, l, b, base, n, off, lg_table, bits, reinterpret_cast<uint16_t *>(bits + slice / 32), &s_kept,
-                      tid);
+        adjust_listed(p, l, b, j, base, n, off, lg_table, bits, reinterpret_cast<uint16_t *>(bits + slice / 32), tid);
 
     float x[NG][4];
     float m = -INFINITY;
@@ -405,14 +399,14 @@ __global__ void __launch_bounds__(LG_THREADS, NG <= 8 ? 2 : 1) logits_kernel(con
 template <bool PROBS, bool VEC, int NG>
 static cudaError_t launch_ng(const LogitsParams &p, int slice, int slices, cudaStream_t stream) {
     const bool lists = p.history || p.draft || p.num_bias > 0;
-    const size_t smem = lists ? (size_t)slice * 4 + slice / 8 + LG_KEPT * 2 : 0;
+    const size_t smem = lists ? (size_t)slice * 4 + slice / 8 + LG_KEPT_BYTES : 0;
     auto kernel = logits_kernel<PROBS, VEC, NG>;
     // from where it may pass 48 KB with the fixed part; set on every call: the attribute belongs to the current device,
     // and callers may use several
     if (smem > 32 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 NG * LG_GROUP * 4 + NG * LG_GROUP / 8 + LG_KEPT * 2);
+                                 NG * LG_GROUP * 4 + NG * LG_GROUP / 8 + LG_KEPT_BYTES);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
