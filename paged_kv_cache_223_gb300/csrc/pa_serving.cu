@@ -47,12 +47,13 @@ pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interl
     // 1 / 2 pi as the sum of two doubles: the nearest double and what is left of it
     const double inv_2pi = 0.15915494309189535, inv_2pi_lo = -9.839338337591243e-18;
     for (int i = 0; i < rot_dim / 2; ++i) {
-        const double w = inv_freq[i];
-        if (!std::isfinite(w) || std::fabs(w) > 1e6) return PA_ERR_INVALID_ARG;
-        const double hi = w * inv_2pi;
+        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1e6) return PA_ERR_INVALID_ARG;
+        // of the magnitude: hi - floor(hi) is exact from 0 on, but rounds for a small negative hi
+        const double w = std::fabs(inv_freq[i]), hi = w * inv_2pi;
         const double lo = std::fma(w, inv_2pi, -hi) + w * inv_2pi_lo;
-        const double frac = hi - std::floor(hi);                      // [0, 1), exact
-        f[i] = (frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+        const double units = std::ldexp(hi - std::floor(hi), 64), whole = std::floor(units);   // below 2^64
+        f[i] = (uint64_t)whole + (uint64_t)(int64_t)std::llrint((units - whole) + std::ldexp(lo, 64));
+        if (inv_freq[i] < 0) f[i] = 0 - f[i];
     }
     DeviceGuard g(device);
     if (!g.ok) return PA_ERR_CUDA;
