@@ -231,7 +231,8 @@ void pa_rope_destroy(pa_rope *rope);
  * skipped, q is still rotated; slots beyond the pool are skipped and flagged,
  * PA_ERR_DEVICE_BOUNDS; two tokens with one slot: which one lands is
  * unspecified). Rotation is fp32, rounded once to the model type; an FP8 pool's
- * k codes are quantised from the fp32 values.
+ * k codes are quantised from the fp32 values (scale 1 also where amax / 448 is
+ * below the smallest fp32 number).
  *   q, k, v       device rows [heads, head_dim] of the pool's dtype, 16-byte aligned; token i's
  *                 starts i * stride elements behind the first (strides: multiples of 8, at least
  *                 heads * head_dim), so the three may be slices of one projection's output

@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
             const unsigned group = ((1u << TPH) - 1u) << ((tid & 31) / TPH * TPH);
 #pragma unroll
             for (int o = TPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, o));
-            const float scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+            const float unit = __fdiv_rn(m, 448.f);                    // 0 for rows below 448 of the smallest number, too
+            const float scale = unit > 0.f ? unit : 1.f;
             uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + srow * D);
             dst[v0] = e4m3x8(x, scale);
             dst[v1] = e4m3x8(y, scale);
