@@ -272,7 +272,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  *                  call alone while it runs
  * Violations in cu_q, block_tables or context_lens are clamped and flagged
  * (PA_ERR_DEVICE_BOUNDS at pa_pool_check); the sequence's outputs are then
- * unspecified. 16-bit pools, head_dim 64 or 128 (PA_ERR_UNSUPPORTED
+ * unspecified, where cu_q decreases every sequence's. 16-bit pools, head_dim 64 or 128 (PA_ERR_UNSUPPORTED
  * otherwise), at most PA_PACKED_MAX_SEQS sequences. Nothing of the pool is written, so
  * calls with workspaces of their own may run at the same time. Results are
  * deterministic run to run.

@@ -245,6 +245,9 @@ __device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, 
     const int rows2 = 2 * p.P, grid = (int)gridDim.x;
     if (tid < 32) {
         int total = 0;
+        // No more than non-decreasing cu_q can make: what else it holds (flagged) neither overflows the prefix nor makes
+        // the sequences' work many times over.
+        const int most = min(p.num_tokens, p.num_tokens / (2 * p.P) + min(p.num_tokens, p.num_seqs));
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
             const int b = b0 + lane;
             int first = 0, n = 0, L = 0;
@@ -255,8 +258,8 @@ __device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, 
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            if (b < p.num_seqs) pl.pref[b + 1] = total + x;
-            total += __shfl_sync(0xffffffffu, x, 31);
+            if (b < p.num_seqs) pl.pref[b + 1] = min(total + x, most);
+            total = min(total + __shfl_sync(0xffffffffu, x, 31), most);
         }
         if (lane == 0) {
             pl.pref[0] = 0;

@@ -1,0 +1,46 @@
+"""prefill_packed at the ends of what its plan can hold."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_cache_223_gb300 import pagedattn as pa
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def test_a_decreasing_cu_q_is_flagged_and_bounded():
+    """2048 sequences, every other one naming all rows: flagged, and not 1024 times a call's work."""
+    T, n, hq, hkv, d, bs = 4096, 2048, 64, 8, 128, 16
+    g = torch.Generator(device=DEV).manual_seed(71)
+    pool = pa.Pool(T // bs, bs, hkv, d, torch.bfloat16, max_seqs=1, max_context_len=512)
+    pool.k_cache.normal_(generator=g), pool.v_cache.normal_(generator=g)
+    q = torch.randn(T + 3, hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    tables = torch.arange(T // bs, dtype=torch.int32, device=DEV).repeat(n, 1)
+    lens, whole, wrong = i32([T] * n), i32([0, T]), i32([0, T] * (n // 2) + [0])
+    out = torch.full_like(q, 7.0)
+
+    def timed(cu):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        pool.prefill_packed(q, cu, tables, lens, 1 / math.sqrt(d), out=out)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    timed(whole)
+    one = min(timed(whole) for _ in range(3))
+    assert pool.check() == pa.PA_OK
+    ref = out.clone()
+    out.fill_(7.0)
+    many = timed(wrong)
+    assert pool.check() == pa.PA_ERR_DEVICE_BOUNDS
+    assert many < 100 * one, (many, one)
+    assert bool((out[T:] == 7.0).all())               # rows of no sequence
+    timed(whole)
+    assert pool.check() == pa.PA_OK and torch.equal(out, ref)
