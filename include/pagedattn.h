@@ -264,7 +264,8 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  *                  rows before cu_q[0] and from cu_q[num_seqs] on are left as they are in out
  *   block_tables   device int32 [num_seqs, block_table_stride]; entries at or beyond
  *                  ceil(context_lens[b] / bs) are never read
- *   context_lens   device int32 [num_seqs]; n_b <= context_lens[b] <= stride * bs
+ *   context_lens   device int32 [num_seqs]; n_b <= context_lens[b] <= stride * bs, and at most
+ *                  PA_PACKED_MAX_CONTEXT
  *   num_q_heads    a multiple of num_kv_heads, at most 128 per KV head
  *   scale          softmax scale, finite and > 0
  *   workspace      device, 16-byte aligned, at least pa_prefill_packed_workspace() bytes (0 where
@@ -278,6 +279,7 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  * deterministic run to run.
  */
 #define PA_PACKED_MAX_SEQS 2048
+#define PA_PACKED_MAX_CONTEXT (1 << 29)
 pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                                       int32_t block_table_stride, uint64_t *bytes);
 pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, const void *v_cache,

@@ -157,7 +157,7 @@ static pa_status packed_params(const pa_pool *pool, int32_t num_tokens, int32_t 
     if (G > 128 || num_seqs > PA_PACKED_MAX_SEQS || (int64_t)num_tokens * num_q_heads >= (int64_t)1 << 31)
         return PA_ERR_UNSUPPORTED;
     int64_t max_ctx = (int64_t)stride * c.block_size;
-    if (max_ctx > 0x7fffff00) max_ctx = 0x7fffff00;
+    if (max_ctx > PA_PACKED_MAX_CONTEXT) max_ctx = PA_PACKED_MAX_CONTEXT;
     p.stride = stride;
     p.num_tokens = num_tokens;
     p.num_seqs = num_seqs;

@@ -226,6 +226,8 @@ struct PromptPlan {
 };
 static_assert(3 * PR_SORT + 4 <= PA_PACKED_MAX_SEQS, "the sorted plan takes the prefix's place");
 constexpr int PR_WHOLE = 1 << 24;
+static_assert(PA_PACKED_MAX_CONTEXT / PR_BN < PR_WHOLE && (PA_PACKED_MAX_CONTEXT / PR_BN + 1ull) * PR_SORT <= 1ull << 32,
+              "an item's key tiles fit a sort key");
 
 __device__ __forceinline__ int items_of(const PromptParams &p, int n) { return (n + 2 * p.P - 1) / (2 * p.P); }
 
@@ -281,7 +283,7 @@ __device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, 
         sequence(p, lo, first, n, L, nullptr);
         const int i = k - pl.pref[lo], end = L - n + min(n, (i + 1) * rows2);
         const int e = end > PR_BN ? (end + PR_BN - 1) / PR_BN : 1;
-        pl.key[k] = (uint32_t)min(e, 1 << 22) * PR_SORT + (PR_SORT - 1 - k);        // all different
+        pl.key[k] = (uint32_t)e * PR_SORT + (PR_SORT - 1 - k);                      // all different
         pl.pack[k] = (uint32_t)lo << 16 | (uint32_t)i;
     }
     __syncthreads();

@@ -5,6 +5,8 @@ import pytest
 import torch
 
 from paged_kv_cache_223_gb300 import pagedattn as pa
+from serving_reference import packed_attention
+from test_gpu_packed import close
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -44,3 +46,25 @@ def test_a_decreasing_cu_q_is_flagged_and_bounded():
     assert bool((out[T:] == 7.0).all())               # rows of no sequence
     timed(whole)
     assert pool.check() == pa.PA_OK and torch.equal(out, ref)
+
+
+def test_the_longest_context():
+    """PA_PACKED_MAX_CONTEXT tokens, of blocks whose keys are 0 and values 1: weights of 1 and sums of whole numbers,
+    so the output is 1. One block more is flagged, and the sequence beside it keeps its result."""
+    most, hq, d, bs, shared = 1 << 29, 2, 64, 32, 8192
+    pool = pa.Pool(shared + 2, bs, 1, d, torch.float16, max_seqs=1, max_q_heads=hq, max_context_len=512)
+    g = torch.Generator(device=DEV).manual_seed(72)
+    pool.k_cache.normal_(generator=g), pool.v_cache.normal_(generator=g)
+    pool.k_cache[:shared] = 0.0
+    pool.v_cache[:shared] = 1.0
+    tables = (torch.arange(most // bs + 1, dtype=torch.int32, device=DEV) % shared).repeat(2, 1)
+    tables[1, 0], tables[1, 1] = shared + 1, shared
+    q = torch.randn(1 + 40, hq, d, generator=g, device=DEV).half()
+    cu = i32([0, 1, 41])
+    out = pool.prefill_packed(q, cu, tables, i32([most, 50]), 0.125)
+    assert pool.check() == pa.PA_OK
+    assert bool((out[0] == 1.0).all())
+    ref, mag = packed_attention(q[1:], pool.k_cache, pool.v_cache, [0, 40], tables[1:], [50], 0.125)
+    close(out[1:], ref, mag)
+    long = pool.prefill_packed(q, cu, tables, i32([most + bs, 50]), 0.125)
+    assert pool.check() == pa.PA_ERR_DEVICE_BOUNDS and torch.equal(long[1:], out[1:])
