@@ -165,7 +165,9 @@ class Rope:
 
     @classmethod
     def from_base(cls, rot_dim: int, base: float = 10000.0, **kw) -> "Rope":
-        """Frequencies base ** (-2i / rot_dim)."""
+        """Frequencies base ** (-2i / rot_dim), i < rot_dim / 2."""
+        if rot_dim % 2:
+            raise ValueError(f"rot_dim must be even, got {rot_dim}")
         return cls([base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], **kw)
 
     @property

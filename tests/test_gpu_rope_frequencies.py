@@ -79,3 +79,13 @@ def test_angles_near_whole_turns(sign):
         got = float(out[i, 0, len(freqs) + i])
         tol = abs(s) * (2.0 ** -11 + 2.0 ** -21) + scale * p * 2.0 ** -64 * 2 * math.pi + 2.0 ** -25
         assert abs(got - s) <= tol, (freqs[i], p, got, s, tol)
+
+
+def test_frequencies_of_a_base():
+    pool = pa.Pool(1, 16, 1, 128, torch.float16, max_seqs=1, max_context_len=512)
+    q = rows(100, 2, 2)
+    pos = torch.arange(100, dtype=torch.int32, device=DEV) * 77
+    for rot, base in ((128, 10000.0), (64, 500000.0)):
+        a = append(pool, q, pos, pa.Rope.from_base(rot, base, interleaved=True, scale=0.5))
+        b = append(pool, q, pos, pa.Rope([base ** (-2.0 * i / rot) for i in range(rot // 2)], True, 0.5))
+        assert torch.equal(a, b)
