@@ -207,7 +207,8 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
 /*
  * Rotary frequencies of a model, laid out on the device once: pa_rope_append
  * turns dimension pair i of a row at position p by the angle p * inv_freq[i].
- *   inv_freq      host, rot_dim / 2 finite frequencies in radians per position
+ *   inv_freq      host, rot_dim / 2 frequencies in radians per position, of either sign, magnitude
+ *                 at most PA_ROPE_MAX_FREQ
  *   rot_dim       rotated dimensions of a head, a multiple of 16 (16 .. 128); dimensions
  *                 from rot_dim on pass through
  *   interleaved   0: pair i is dimensions (i, i + rot_dim / 2); 1: (2i, 2i + 1)
@@ -219,6 +220,7 @@ pa_status pa_prefill(pa_pool *pool, const void *q, const void *k_cache, const vo
  * graphs that captured them, may still run.
  * Errors: PA_ERR_INVALID_ARG, PA_ERR_OOM, PA_ERR_CUDA.
  */
+#define PA_ROPE_MAX_FREQ 1000000
 typedef struct pa_rope pa_rope;
 pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interleaved, float scale, int32_t device,
                          pa_rope **out);
@@ -238,7 +240,8 @@ void pa_rope_destroy(pa_rope *rope);
  *                 heads * head_dim), so the three may be slices of one projection's output
  *   positions     device int32 [num_tokens], any sign
  *   slot_mapping  device int64 [num_tokens]
- *   num_q_heads   >= 0; 0 appends without a q (q and q_out are then ignored)
+ *   num_q_heads   0 .. 65536; 0 appends without a q (q and q_out are then ignored);
+ *                 num_q_heads + 2 num_kv_heads at most 262144 (PA_ERR_UNSUPPORTED)
  *   q_out         device rows, q_out_stride as above; may be q itself with the same stride,
  *                 must not overlap the rows of q, k and v otherwise (PA_ERR_INVALID_ARG, also where
  *                 rows of different strides lie in between one another)
@@ -273,9 +276,10 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  *                  call alone while it runs
  * Violations in cu_q, block_tables or context_lens are clamped and flagged
  * (PA_ERR_DEVICE_BOUNDS at pa_pool_check); the sequence's outputs are then
- * unspecified, where cu_q decreases every sequence's. 16-bit pools, head_dim 64 or 128 (PA_ERR_UNSUPPORTED
- * otherwise), at most PA_PACKED_MAX_SEQS sequences. Nothing of the pool is written, so
- * calls with workspaces of their own may run at the same time. Results are
+ * unspecified, where cu_q decreases every sequence's. 16-bit pools, head_dim 64
+ * or 128, at most PA_PACKED_MAX_SEQS sequences, num_tokens * num_q_heads below
+ * 2^31 (PA_ERR_UNSUPPORTED otherwise). Nothing of the pool is written, so calls
+ * with workspaces of their own may run at the same time. Results are
  * deterministic run to run.
  */
 #define PA_PACKED_MAX_SEQS 2048
@@ -402,7 +406,7 @@ typedef struct pa_logits_args {
     const void *logits;        /* device; row (b, j) starts at b * seq_stride + j * row_stride elements */
     int32_t dtype;             /* pa_logits_dtype */
     int32_t num_seqs;          /* >= 0 */
-    int32_t rows_per_seq;      /* >= 1 (num_draft + 1 for a verify); num_seqs * rows_per_seq < 2^24 */
+    int32_t rows_per_seq;      /* 1 .. PA_LOGITS_MAX_ROWS (num_draft + 1 for a verify); num_seqs * rows_per_seq < 2^24 */
     int32_t num_bias;          /* entries of a bias row, 0 .. PA_LOGITS_MAX_BIAS */
     int64_t vocab;             /* 1 .. PA_LOGITS_MAX_VOCAB */
     int64_t seq_stride, row_stride;   /* elements, >= 0; rows need not be aligned beyond an element */
@@ -431,6 +435,7 @@ typedef struct pa_logits_args {
 #define PA_LOGITS_MAX_VOCAB 393216
 #define PA_LOGITS_MAX_HISTORY 1000000
 #define PA_LOGITS_MAX_BIAS 2000
+#define PA_LOGITS_MAX_ROWS 4096
 pa_status pa_adjust_logits(const pa_logits_args *args, void *stream);
 pa_status pa_token_probs(const pa_logits_args *args, void *stream);
 

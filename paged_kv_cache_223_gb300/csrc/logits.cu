@@ -40,7 +40,7 @@ constexpr int LG_THREADS = 512;
 constexpr int LG_GROUP = 4 * LG_THREADS;              // values of a block per group of four per thread
 constexpr uint32_t LG_PROMPT = 1u << 20, LG_COUNT = LG_PROMPT - 1u;
 constexpr int LG_BIAS_SHIFT = 21;
-static_assert(PA_LOGITS_MAX_HISTORY + 4096 <= (int)LG_COUNT, "an output count fits its field");
+static_assert(PA_LOGITS_MAX_HISTORY + PA_LOGITS_MAX_ROWS <= (int)LG_COUNT, "an output count fits its field");
 static_assert(PA_LOGITS_MAX_BIAS + 1 < (1 << (32 - LG_BIAS_SHIFT)), "a bias index fits its field");
 constexpr int LG_MAX_SLICES = 8;                      // blocks of a row: a portable cluster
 constexpr int LG_KEPT = 384;                          // entries of a slice that a warp keeps in shared memory

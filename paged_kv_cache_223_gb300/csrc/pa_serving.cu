@@ -47,7 +47,7 @@ pa_status pa_rope_create(const double *inv_freq, int32_t rot_dim, int32_t interl
     // 1 / 2 pi as the sum of two doubles: the nearest double and what is left of it
     const double inv_2pi = 0.15915494309189535, inv_2pi_lo = -9.839338337591243e-18;
     for (int i = 0; i < rot_dim / 2; ++i) {
-        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1e6) return PA_ERR_INVALID_ARG;
+        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > PA_ROPE_MAX_FREQ) return PA_ERR_INVALID_ARG;
         // of the magnitude: hi - floor(hi) is exact from 0 on, but rounds for a small negative hi
         const double w = std::fabs(inv_freq[i]), hi = w * inv_2pi;
         const double lo = std::fma(w, inv_2pi, -hi) + w * inv_2pi_lo;
@@ -278,7 +278,7 @@ static pa_status logits_call(const pa_logits_args *a, bool probs, void *stream) 
     if (a->dtype != PA_LOGITS_FP16 && a->dtype != PA_LOGITS_BF16 && a->dtype != PA_LOGITS_FP32)
         return PA_ERR_INVALID_ARG;
     if (a->vocab > PA_LOGITS_MAX_VOCAB || a->history_stride > PA_LOGITS_MAX_HISTORY ||
-        a->num_bias > PA_LOGITS_MAX_BIAS || a->rows_per_seq > 4096 ||
+        a->num_bias > PA_LOGITS_MAX_BIAS || a->rows_per_seq > PA_LOGITS_MAX_ROWS ||
         (int64_t)a->num_seqs * a->rows_per_seq >= (int64_t)1 << 24)
         return PA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return PA_OK;
