@@ -1,6 +1,7 @@
 // pa_serving.cu -- the serving operators' part of the C ABI declared in include/pagedattn.h: rotary
 // frequencies, argument validation, TMA descriptor encoding and kernel launches. The kernels are those of
 // rope_append.cu, prompt.cu and logits.cu.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -174,7 +175,9 @@ static pa_status packed_params(const pa_pool *pool, int32_t num_tokens, int32_t 
     const int64_t least_items = ((int64_t)num_tokens + 2 * p.P - 1) / (2 * p.P) * c.num_kv_heads;
     p.max_units = least_items < 2 * pool->sm_count && max_ctx > 4 * 128 ? 2 * pool->sm_count : 0;
     p.status = pool->status;
-    p.wait_ns = pool->wait_ns;
+    // The kernel's longest waits last as long as a unit's work (the next unit's Q takes the place of its Q): 1.5 to 2 us
+    // per key tile of what may be a whole context. Four times that, where it is above the pool's limit.
+    p.wait_ns = std::max(pool->wait_ns, (uint64_t)(max_ctx / 128) * 8000);
     return PA_OK;
 }
 

@@ -68,3 +68,16 @@ def test_the_longest_context():
     close(out[1:], ref, mag)
     long = pool.prefill_packed(q, cu, tables, i32([most + bs, 50]), 0.125)
     assert pool.check() == pa.PA_ERR_DEVICE_BOUNDS and torch.equal(long[1:], out[1:])
+
+
+def test_a_long_context_that_is_not_cut():
+    """2^28 tokens of one row beside rows that fill the GPU: one block works through them for about three seconds while
+    its next unit waits."""
+    long, rest, hq, d, bs, shared = 1 << 28, 640, 128, 64, 32, 8192
+    pool = pa.Pool(shared, bs, 1, d, torch.float16, max_seqs=1, max_q_heads=hq, max_context_len=512)
+    pool.k_cache.zero_(), pool.v_cache.fill_(1.0)
+    tables = (torch.arange(long // bs, dtype=torch.int32, device=DEV) % shared).repeat(2, 1)
+    q = torch.ones(1 + rest, hq, d, dtype=torch.float16, device=DEV)
+    out = pool.prefill_packed(q, i32([0, 1, 1 + rest]), tables, i32([long, rest]), 0.125)
+    assert pool.check() == pa.PA_OK
+    assert bool((out[1:] == 1.0).all())
