@@ -271,9 +271,9 @@ pa_status pa_rope_append(pa_pool *pool, const pa_rope *rope, const void *q, int6
  *                  PA_PACKED_MAX_CONTEXT
  *   num_q_heads    a multiple of num_kv_heads, at most 128 per KV head
  *   scale          softmax scale, finite and > 0
- *   workspace      device, 16-byte aligned, at least pa_prefill_packed_workspace() bytes (0 where
- *                  num_tokens or the tables leave nothing to cut: NULL will do), written by this
- *                  call alone while it runs
+ *   workspace      device, 16-byte aligned, at least pa_prefill_packed_workspace() bytes (0 where the
+ *                  tables hold short contexts only: NULL will do), written by this call alone while
+ *                  it runs
  * Violations in cu_q, block_tables or context_lens are clamped and flagged
  * (PA_ERR_DEVICE_BOUNDS at pa_pool_check); the sequence's outputs are then
  * unspecified, where cu_q decreases every sequence's. 16-bit pools, head_dim 64

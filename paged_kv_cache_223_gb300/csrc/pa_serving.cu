@@ -221,7 +221,9 @@ pa_status pa_prefill_packed_workspace(const pa_pool *pool, int32_t num_tokens, i
     PromptParams p;
     const pa_status st = packed_params(pool, num_tokens, num_seqs, num_q_heads, block_table_stride, p);
     if (st != PA_OK) return st;
-    *bytes = p.max_units == 0 ? 0 : 256 + (uint64_t)p.max_units * (PROMPT_ITEM_BYTES + prompt_slot_bytes(pool->cfg.head_dim));
+    // a state for each unit of a call that may be cut, for each block of one that is not but whose sums may be long
+    const uint64_t slots = p.max_units > 0 ? p.max_units : p.max_ctx > 128 * PROMPT_FOLD_TILES ? pool->sm_count : 0;
+    *bytes = slots == 0 ? 0 : 256 + (uint64_t)p.max_units * PROMPT_ITEM_BYTES + slots * prompt_slot_bytes(pool->cfg.head_dim);
     return PA_OK;
 }
 

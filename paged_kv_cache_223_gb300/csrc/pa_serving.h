@@ -71,6 +71,7 @@ cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const 
 cudaError_t setup_prompt(int dtype, int head_dim);
 size_t prompt_slot_bytes(int head_dim);
 constexpr int PROMPT_ITEM_BYTES = 32;   // of the workspace per unit, beside its state
+constexpr int PROMPT_FOLD_TILES = 128;  // key tiles (of 128 keys) that a unit sums up without a state in the workspace
 cudaError_t launch_logits(const LogitsParams &p, bool probs, cudaStream_t stream);
 
 }  // namespace pa

@@ -100,7 +100,8 @@ struct alignas(16) PromptUnit {
     int n0, n1;                // key tiles of row tile 0 and 1
     int slot;                  // where the unit's state goes; -1: the output itself
     int poison;                // V tiles of the unit held values that are no numbers
-    int pad[5];
+    int fold;                  // state slot that long sums are kept in meanwhile
+    int pad[4];
 };
 static_assert(sizeof(PromptUnit) == 64, "unit ring");
 
@@ -113,6 +114,30 @@ struct PromptItem {
 static_assert(sizeof(PromptItem) <= PROMPT_ITEM_BYTES, "workspace items");
 
 size_t prompt_slot_bytes(int head_dim) { return (size_t)256 * (head_dim + 2) * 4; }
+
+// Sums over long contexts. An MMA aligns each product to the accumulator it is added to and drops what is below about
+// 2^-26 of that, so a sum of N like terms comes out up to N 2^-26 too small (measured: N 2^-27, 2.6% at 2^22 keys). So
+// where contexts may be longer, O leaves the accumulator every PROMPT_FOLD_TILES key tiles (2^14 keys: 2^-12 at most)
+// for a state of the row in the workspace (as a unit's: [D / 4][256 rows] float4, then [256 rows] (max, sum)), is summed
+// there in fp32 and starts anew; the row's sum of weights goes the same way. One thread per row does both, so
+// nothing has to be waited for. A prompt of 32768 tokens, 32 / 8 heads of 128: 5.76 -> 5.90 ms (every 64 tiles 6.03).
+constexpr int PR_FOLD = PROMPT_FOLD_TILES;
+static_assert((PR_FOLD & (PR_FOLD - 1)) == 0, "a power of two");
+
+template <int D>
+struct RowState {
+    float4 *o;                 // [D / 4], 256 apart
+    float2 *ml;
+    __device__ RowState(uint8_t *slot, int row)
+        : o(reinterpret_cast<float4 *>(slot) + row), ml(reinterpret_cast<float2 *>(slot + (size_t)256 * D * 4) + row) {}
+    // The weight of what is kept, relative to the maximum m; its sum is added to l.
+    __device__ float weigh(float m, float &l) const {
+        const float2 old = *ml;
+        const float w = old.x == -INFINITY ? 0.f : ex2_approx(old.x - m);
+        l += old.y * w;
+        return w;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite_probe(uint32_t x, uint32_t acc) {
@@ -338,7 +363,8 @@ __device__ void make_plan(const PromptParams &p, const PromptPlan &pl, int tid, 
     }
 }
 
-template <typename T, int D>
+// LONG: contexts of more than PR_FOLD key tiles may come (elsewhere the code for them would cost 2 to 3%).
+template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(PR_THREADS, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const PromptParams p) {
@@ -463,6 +489,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         un.n1 = max(0, min(e1 - un.kt0, chunk));
                         const bool cut = max(s0, s1) > 1;
                         un.slot = cut ? u : -1;
+                        un.fold = chunk == PR_WHOLE ? (int)blockIdx.x : u;
                     }
                     const int st = published % PR_UNITS;
                     if (published >= PR_UNITS && !(ok = wait(u_empty + st * 8, (uint32_t)(published / PR_UNITS - 1) & 1u)))
@@ -573,7 +600,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t v = v_lo + last_vs * (S::KV_BYTES >> 4), pt = tmem + t * 256, ot = pt + 128;
-                    umma_ts<hi_kv>(ot, pt, v, idesc_o, pj > 0 ? 1u : 0u);
+                    umma_ts<hi_kv>(ot, pt, v, idesc_o, (LONG ? pj & (PR_FOLD - 1) : pj) > 0 ? 1u : 0u);
 #pragma unroll
                     for (int k = 1; k < PR_BN / 16; ++k)
                         umma_ts<hi_kv>(ot, pt + k * 8, v + ((k * 2 * S::GROUP_BYTES) >> 4), idesc_o, 1u);
@@ -661,6 +688,29 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 // that work on it release it
                 if (r == 0) mbar_arrive_count(k_empty + i_k % S::KST * 8, j < min(un.n0, un.n1) ? 1u : 2u);
                 tc_fence_after();
+                if (LONG && j > 0 && (j & (PR_FOLD - 1)) == 0) {
+                    // P(j-1) V was issued before S(j), so the commit of S(j) covers it; P(j) V overwrites O
+                    const RowState<D> kept(p.ws_slots + (size_t)un.fold * 256 * (D + 2) * 4, t * PR_BM + r);
+                    const bool more = j > PR_FOLD;
+                    const float w = more ? kept.weigh(m_ref, l) : 0.f;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float a[32];
+                        tmem_ld32(tmem_o + c0, a);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float4 x = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+                            float4 *at = kept.o + (c0 / 4 + i) * 256;
+                            if (more) {
+                                const float4 y = *at;
+                                x.x += y.x * w, x.y += y.y * w, x.z += y.z * w, x.w += y.w * w;
+                            }
+                            *at = x;
+                        }
+                    }
+                    *kept.ml = make_float2(m_ref, l);
+                    l = 0.f;
+                }
                 float sv[PR_BN];
                 tmem_ld_cols(tmem_s, sv);
                 const int t0 = key0 + j * PR_BN;
@@ -771,6 +821,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 tmem_ld_cols(tmem_o, o);
                 tc_fence_before();
                 mbar_arrive(o_free + t * 8);
+                if (LONG && nt > PR_FOLD) {
+                    const RowState<D> kept(p.ws_slots + (size_t)un.fold * 256 * (D + 2) * 4, t * PR_BM + r);
+                    const float w = kept.weigh(m_ref, l);
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i) {
+                        const float4 y = kept.o[i * 256];
+                        o[4 * i] += y.x * w, o[4 * i + 1] += y.y * w, o[4 * i + 2] += y.z * w, o[4 * i + 3] += y.w * w;
+                    }
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < D; ++i) o[i] = 0.f;
@@ -933,8 +992,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
 template <typename T, int D>
 static cudaError_t launch_prompt_t(const PromptParams &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
                                    const CUtensorMap &tmv, int sm_count, cudaStream_t stream) {
-    const cudaError_t e = launch_pdl(prompt_kernel<T, D>, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream,
-                   tmq, tmk, tmv, p);
+    const auto kernel = p.max_ctx > PR_FOLD * PR_BN ? prompt_kernel<T, D, true> : prompt_kernel<T, D, false>;
+    const cudaError_t e =
+        launch_pdl(kernel, dim3((unsigned)sm_count), dim3(PR_THREADS), (size_t)PromptShape<D>::SMEM, stream, tmq, tmk, tmv, p);
     if (e != cudaSuccess || p.max_units == 0) return e;
     // 32 rows of an item and KV head per block; what is cut has fewer than max_units items, and a call of few tokens
     // no more items and rows than they make
@@ -944,13 +1004,19 @@ static cudaError_t launch_prompt_t(const PromptParams &p, const CUtensorMap &tmq
     return launch_pdl(prompt_join_kernel<T, D>, blocks, dim3(256), 0, stream, p);
 }
 
-// The kernel's shared memory on the current device: once per pool, not per call.
+// The kernels' shared memory on the current device: once per pool, not per call.
+template <typename T, int D>
+static cudaError_t setup_prompt_t() {
+    const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               PromptShape<D>::SMEM);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(prompt_kernel<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   PromptShape<D>::SMEM);
+}
+
 cudaError_t setup_prompt(int dtype, int head_dim) {
-    const void *k = dtype == PA_FP16 ? (head_dim == 64 ? (const void *)prompt_kernel<__half, 64> : (const void *)prompt_kernel<__half, 128>)
-                                     : (head_dim == 64 ? (const void *)prompt_kernel<__nv_bfloat16, 64>
-                                                       : (const void *)prompt_kernel<__nv_bfloat16, 128>);
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                head_dim == 64 ? PromptShape<64>::SMEM : PromptShape<128>::SMEM);
+    if (dtype == PA_FP16) return head_dim == 64 ? setup_prompt_t<__half, 64>() : setup_prompt_t<__half, 128>();
+    return head_dim == 64 ? setup_prompt_t<__nv_bfloat16, 64>() : setup_prompt_t<__nv_bfloat16, 128>();
 }
 
 cudaError_t launch_prompt(const PromptParams &p, int dtype, int head_dim, const CUtensorMap &tmq,

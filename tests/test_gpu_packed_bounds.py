@@ -81,3 +81,36 @@ def test_a_long_context_that_is_not_cut():
     out = pool.prefill_packed(q, i32([0, 1, 1 + rest]), tables, i32([long, rest]), 0.125)
     assert pool.check() == pa.PA_OK
     assert bool((out[1:] == 1.0).all())
+
+
+@pytest.mark.parametrize("scores", ["flat", "random", "rising", "falling"])
+@pytest.mark.parametrize("log2,d,dt", [(15, 64, torch.float16), (18, 128, torch.bfloat16), (20, 64, torch.float16),
+                                       (20, 128, torch.float16)])
+def test_sums_over_long_contexts_that_are_not_cut(log2, d, dt, scores):
+    """One row behind 2^log2 tokens beside rows that fill the GPU, values between 1 and 2. The tolerance of the packed
+    prompts' tests, and what an accumulator drops of the products added to it: 2^-26 of the sum each, for the 128
+    tiles of 128 keys that it takes, 2^-12 in all."""
+    long, rest, hq, bs = 1 << log2, 9800, 8, 32
+    g = torch.Generator(device=DEV).manual_seed(73)
+    nb = long // bs
+    pool = pa.Pool(nb, bs, 1, d, dt, max_seqs=1, max_q_heads=hq, max_context_len=512)
+    pool.k_cache.normal_(generator=g), pool.v_cache.uniform_(1.0, 2.0, generator=g)
+    q = torch.randn(1 + rest, hq, d, generator=g, device=DEV).to(dt)
+    scale = 1 / math.sqrt(d)
+    if scores == "flat":
+        q.zero_()
+    elif scores != "random":                          # from 0 to 24 along the context, or back
+        q[0] = 0.0
+        q[0, :, 0] = 4.0
+        ramp = torch.linspace(0.0, 6.0 / scale, long, device=DEV)
+        pool.k_cache.view(long, d)[:, 0] = (ramp if scores == "rising" else ramp.flip(0)).to(dt)
+    tables = torch.arange(nb, dtype=torch.int32, device=DEV).repeat(2, 1)
+    out = pool.prefill_packed(q, i32([0, 1, 1 + rest]), tables, i32([long, rest]), scale)
+    assert pool.check() == pa.PA_OK
+    K, V = pool.k_cache.view(long, d), pool.v_cache.view(long, d)
+    s = torch.cat([q[0].double() @ k.double().T for k in K.split(1 << 18)], 1) * scale
+    w = torch.softmax(s, 1)
+    ref = sum(x @ v.double() for x, v in zip(w.split(1 << 18, 1), V.split(1 << 18)))      # all values > 0: sum p|v| too
+    h = torch.finfo(dt).eps / 2
+    err = (out[0].double() - ref).abs()
+    assert bool((err <= ref * (2.01 * h + 2.0 ** -12 + 2.0 ** -12)).all()), float((err / ref).max())
