@@ -21,16 +21,18 @@
 // integer atomics, so the order of arrival changes nothing), and the first entry to claim a token's bit
 // replaces the token's word by the adjusted logit. The pass over the values only looks at the bits.
 //
-// Measured, 64 x 6 rows of 128256 fp32 logits: adjusting without lists 59 us (1.02 of the copy rate), with a history
-// of up to 4096 tokens, biases, drafts and masks 87 us; probabilities without lists 92 us, with them 141 us (0.42), of
+// Measured, 64 x 6 rows of 128256 fp32 logits: adjusting without lists 59 us (0.99 of the copy rate), with a history
+// of up to 4096 tokens, biases, drafts and masks 87 us; probabilities without lists 91 us, with them 141 us (0.42), of
 // which counting takes about 22 and the adjusted logits 16 (entries kept in one list of the block, with the positions
 // from shared atomics, and eight entries held per thread, which spilled: 151 us).
 // What is left is a block's chain of barriers (three for the lists, one of the cluster) with two blocks per SM to
-// overlap it: registers bound those. Not kept: penalties computed in the pass over the values (200 us), slices
-// dealt out in pieces of 128 or 2048 tokens so that the lists even out (lists 5 to 10 us less, the rest 13 to 20 us
-// more), the logits prefetched into L2 one round of blocks ahead and loaded behind the lists (150 us), the lists read
-// once for six rows that a cluster takes in turn (161 us), asynchronous copies of the listed logits and of the biases
-// into shared memory (160 us).
+// overlap it: registers bound those (64 a thread with 8 groups, 8 to 16 bytes spilled). Rows above 131072 tokens
+// take the kernel of 24 groups, one block per SM and up to 284 bytes spilled: 64 x 6 rows with lists of 151936 fp32
+// logits 329 us (0.21), of 262144 409 us (0.30). Not kept: penalties computed in the pass over the values (200 us),
+// slices dealt out in pieces of 128 or 2048 tokens so that the lists even out (lists 5 to 10 us less, the rest 13
+// to 20 us more), the logits prefetched into L2 one round of blocks ahead and loaded behind the lists (150 us), the
+// lists read once for six rows that a cluster takes in turn (161 us), asynchronous copies of the listed logits and
+// of the biases into shared memory (160 us).
 #include "pa_device.cuh"
 #include "pa_serving.h"
 

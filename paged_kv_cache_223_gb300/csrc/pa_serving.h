@@ -26,7 +26,7 @@ struct RopeParams {
 struct PromptParams {
     const void *q;              // [num_tokens, Hq, D]
     void *out;
-    const void *k_cache, *v_cache;
+    const void *v_cache;        // for the values that are no numbers; K and V come through the tensor maps
     const int32_t *block_tables;
     const int32_t *cu_q;        // [num_seqs + 1]
     const int32_t *context_lens;
@@ -37,8 +37,8 @@ struct PromptParams {
     int bs, num_blocks;
     int max_ctx;                // longest context the tables hold
     int P;                      // positions of a row tile: 128 / G
-    int max_units;              // units that the workspace holds states for; 0: nothing is cut
-    int *ws_total;              // workspace: units of the call, their items, their states
+    int max_units;              // units that a call may be cut into; 0: nothing is cut
+    int *ws_total;              // workspace: number of items to join, the items, the states of units or blocks
     struct PromptItem *ws_items;
     uint8_t *ws_slots;
     float scale_log2;

@@ -8,12 +8,12 @@
 //
 // Work. A query "row" is one (position, query head of the KV group) pair. A row tile holds the rows of
 // P = 128 / G positions (G query heads per KV head), position-major, so that all heads of a group share
-// one read of K and V; an item is two row tiles of one sequence and KV head. Items behind long contexts
-// are cut along the keys into units where there are too few to fill the GPU, and a second kernel joins
-// the units' (O, max, sum). The lengths live on the device, so every block of the persistent grid
-// computes the same plan from them (items by falling length, cut length) and takes every gridDim.x-th
-// unit, the direction alternating from round to round so that falling lengths even out. A captured call
-// follows lengths that change between replays.
+// one read of K and V; an item is two row tiles of one sequence and KV head. Items behind long contexts are cut
+// along the keys into units where all items together are too few to fill the GPU (elsewhere a long context is not
+// cut, however short the others are), and a second kernel joins the units' (O, max, sum). The lengths live on the
+// device, so every block of the persistent grid computes the same plan from them (items by falling length, cut
+// length) and takes every gridDim.x-th unit, the direction alternating from round to round so that falling lengths
+// even out. A captured call follows lengths that change between replays.
 //
 // One block per SM, 384 threads:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1: one row per thread = one tensor-memory lane
@@ -28,16 +28,18 @@
 // The MMA thread bounds a step: of about 3200 cycles (2048 of products), every wait and every commit it issues
 // costs it 100 to 170, while the softmax is done 1000 cycles before its weights are asked for. So it waits for K
 // and the weights alone: one thread of each row tile's softmax waits for V before it hands the weights over, and
-// tells the loaders when a K tile (and the V tile before it) has been read. Measured: 4 x 4096 tokens, 64 / 8
-// heads of 128, bf16: 780 us, 1410 TFLOP/s (0.74 of cuBLAS), against 1003 us with the waits, divisions and
-// descriptors in one thread of that warp. Not kept: an MMA warp per row tile, in turns or not (820, 940 us: their
-// products interleave, or each turn costs two waits), two softmax threads per row (936 us and more), weights
-// handed over in halves (840 us), barriers asked ahead of need (805 us), the whole warp on its way with one lane
-// issuing (790 us with the lanes agreeing on every wait, which they must).
+// tells the loaders when a K tile (and the V tile before it) has been read. Measured: 4 x 4096 tokens, 64 / 8 heads
+// of 128, bf16: 780 us, 1410 TFLOP/s (0.74 of cuBLAS; calls on end, at the power limit, 830 us, 1325 TFLOP/s, 0.77
+// of what cuBLAS sustains), against 1003 us with the waits, divisions and descriptors in one thread of that warp.
+// Not kept: an MMA warp per row tile, in turns or not (820, 940 us: their products interleave, or each turn costs
+// two waits), two softmax threads per row (936 us and more), weights handed over in halves (840 us), barriers asked
+// ahead of need (805 us), the whole warp on its way with one lane issuing (790 us with the lanes agreeing on every
+// wait, which they must).
 // 32 prompts of 1 to 2000 tokens, 32 / 8 heads: 108 us (46 at the product's rate), of which the prologue and plan
 // take 5 and each of the up to 9 units per block about 3 at its end (masked tile, last product, stores). Heads of
-// 64: 65 us, paced by the softmax (2800 cycles a step). 30 rows behind 78000 cached tokens: 70 us, 4.6 TB/s; its
-// key loop runs at 0.94 of the DRAM rate.
+// 64: 65 us; a step takes 2800 cycles with nothing at its limit (tensor pipe 18%, exponentials 22%, issue 34%): S,
+// the softmax and P are a chain, as each row tile has one buffer for S and P. 30 rows behind 78000 cached tokens:
+// 70 us, 4.6 TB/s; its key loop runs at 0.94 of the DRAM rate.
 // The roles run across unit borders: the next unit's Q, K and V are on their way, and its first S may be
 // issued, while the last softmax and the output of this one are still at work.
 //
@@ -238,8 +240,8 @@ __device__ __forceinline__ void sequence(const PromptParams &p, int b, int &firs
 }
 
 // The plan, computed by every block alike. Up to PR_SORT items are sorted, the ones with most key tiles first, and
-// cut into units of at most `chunk` key tiles; more items are enough to even out by themselves and stay whole, a
-// sequence's last first.
+// cut into units of at most `chunk` key tiles. More items stay whole and in the caller's order of sequences, a sequence's
+// last first: items of like lengths even out, but a long context that comes late in the batch ends late.
 constexpr int PR_SORT = 512;
 struct PromptPlan {
     int *pref;                 // items of the sequences before b; then, sorted: [512] items, [513] units, [512] tiles
