@@ -294,8 +294,142 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
                             float scale, void *workspace, uint64_t workspace_bytes, void *out, void *stream);
 
 /*
+ * The tables of a serving step, made on the device from the requests' lengths:
+ * what pa_allocator_append does on the host for one sequence, for all of them
+ * by one launch that a captured graph can repeat. In this order:
+ *   every sequence b is cut back to kept = min(context_lens[b], keep_lens[b])
+ *   tokens (0: its request has ended; rejected drafts; NULL: nothing is cut), the
+ *   blocks that it no longer needs go back on the free stack;
+ *   it is given new_lens[b] tokens and takes the blocks that they need:
+ *   context_lens[b] = kept + new_lens[b];
+ *   the new tokens, sequence after sequence, get rows cu_q[b] .. cu_q[b+1] of
+ *   positions and slot_mapping (as pa_rope_append and pa_cache_write take them;
+ *   cu_q as pa_prefill_packed does); the rows behind them position 0, slot -1.
+ * free_blocks[0 .. *num_free) is the free stack, its top last. Blocks are taken
+ * in the order of sequences and their blocks; returned ones are put back so that
+ * the first of them ends on top: cutting back a step's tokens and taking as many
+ * again gives the same blocks. Entries of a table row at or beyond the
+ * sequence's blocks, and of the stack at or beyond *num_free, are left over.
+ * Every block has one owner: blocks that several tables share are the host
+ * allocator's (pa_allocator_*).
+ * A negative length, a sequence longer than its table row (or 2^29 tokens),
+ * more new tokens than num_tokens, or *num_free outside what the pool's blocks
+ * allow is flagged (PA_ERR_DEVICE_BOUNDS at pa_pool_check), more blocks than are
+ * free is flagged as PA_ERR_OOM: tables, lengths and stack are then left as they
+ * are, and the step has no tokens (cu_q all 0, positions 0, slots -1). A block id
+ * outside the pool is flagged, its tokens' slots are -1.
+ */
+#define PA_TABLES_MAX_SEQS 8192
+typedef struct pa_tables_args {
+    int32_t num_seqs;            /* 0 .. PA_TABLES_MAX_SEQS */
+    int32_t num_tokens;          /* rows of positions and slot_mapping, >= 0 */
+    int32_t block_table_stride;  /* entries of a table row, >= 1 */
+    const int32_t *new_lens;     /* device [num_seqs], >= 0 */
+    const int32_t *keep_lens;    /* device [num_seqs], >= 0, or NULL */
+    int32_t *context_lens;       /* device [num_seqs], in and out; may be new_lens or keep_lens as well */
+    int32_t *block_tables;       /* device [num_seqs, block_table_stride], in and out */
+    int32_t *free_blocks;        /* device [num_blocks], in and out */
+    int32_t *num_free;           /* device [1], in and out */
+    int32_t *cu_q;               /* device [num_seqs + 1], out */
+    int32_t *positions;          /* device [num_tokens], out */
+    int64_t *slot_mapping;       /* device [num_tokens], out */
+} pa_tables_args;                /* arrays that are written overlap no other one but as stated (PA_ERR_INVALID_ARG) */
+pa_status pa_step_tables(pa_pool *pool, const pa_tables_args *args, void *stream);
+
+/*
+ * Sparse decoding: attention over the blocks that a cheap score selects for each
+ * query, instead of the whole context. Three calls beside the cache:
+ * pa_key_bounds keeps, for each block and KV head, bounds of its keys;
+ * pa_select_blocks scores a sequence's blocks by them and lists the best;
+ * pa_decode_selected attends to the listed blocks.
+ *
+ * The bounds of a block and KV head: codes hi[d], lo[d] (int8) and a step, with
+ * hi * step and lo * step the largest and smallest key in each dimension,
+ * rounded to the nearest multiple (even of two); step is the smallest power of
+ * two with |hi|, |lo| <= 127 (0 for keys of zeros). Keys are the pool's values
+ * in fp32 (FP8 pools: code * scale). A NaN or infinite key makes the step +inf:
+ * its block is always wanted. One buffer: codes int8
+ * [num_blocks, Hkv, 2, head_dim] (hi, then lo), then steps float32
+ * [num_blocks, Hkv]; pa_key_bounds_size() bytes, owned by the caller, one for
+ * each cache.
+ */
+pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
+
+/*
+ * Bounds of the blocks that hold the newest tokens: sequence b's newest
+ * cu_q[b+1] - cu_q[b] tokens end at context_lens[b] (as for pa_prefill_packed;
+ * their K is in the pool already); the bounds of every block that holds one of
+ * them are made anew from all its tokens before context_lens[b]. Other blocks'
+ * bounds are left as they are. 16-bit and FP8 pools.
+ *   k_cache        device pool, or NULL for the pool's own
+ *   cu_q           device int32 [num_seqs + 1], 0 <= cu_q[b] <= cu_q[b+1] <= num_tokens
+ *   block_tables   device int32 [num_seqs, block_table_stride]
+ *   context_lens   device int32 [num_seqs], at most stride * bs and 2^29
+ *   num_seqs       0 .. PA_TABLES_MAX_SEQS
+ *   bounds         device, 16-byte aligned, pa_key_bounds_size() bytes
+ * Lengths and block ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at
+ * pa_pool_check), the sequence or block is skipped. Two sequences that name one
+ * block with different fillings: whose bounds land is unspecified.
+ */
+pa_status pa_key_bounds(pa_pool *pool, const void *k_cache, const int32_t *cu_q, const int32_t *block_tables,
+                        int32_t block_table_stride, const int32_t *context_lens, int32_t num_tokens, int32_t num_seqs,
+                        void *bounds, void *stream);
+
+/*
+ * Selection: for each sequence and KV head, the `budget` blocks with the largest
+ * scores, ascending, -1 behind them where the context has fewer; the first
+ * num_first and the last num_last blocks of the context are always among them.
+ * The score of a block is the largest, over the query rows that read the KV head
+ * (q_len rows of num_q_heads / num_kv_heads heads), of
+ *   s * step * sum_d max(c[d] * hi[d], c[d] * lo[d])
+ * with the row as whole numbers c and a step s, made from q as the bounds' codes
+ * are from the keys. Sums are of whole numbers and steps are powers of two, so
+ * scores are exact (in fp32's range); of equal scores the lowest block comes
+ * first. A row of q with a NaN or an infinity does not count.
+ *   q              device [num_seqs, q_len, num_q_heads, head_dim] of the pool's dtype
+ *   bounds         of a cache (pa_key_bounds)
+ *   block_tables   device int32 [num_seqs, block_table_stride], at most PA_SELECT_MAX_BLOCKS entries a row
+ *   context_lens   device int32 [num_seqs], counting the q_len newest tokens; 0: a row of padding
+ *   num_q_heads    a multiple of num_kv_heads; (num_q_heads / num_kv_heads) * q_len <= 32
+ *   budget         1 .. PA_SELECT_MAX_BUDGET, at least num_first + num_last
+ *   num_last       at least the blocks that q_len tokens may lie in, ceil((q_len - 1) / bs) + 1
+ *   selected       device int32 [num_seqs, num_kv_heads, budget], no part of the inputs
+ * Lengths and block ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at
+ * pa_pool_check); such a block scores lowest, such a length is clamped. No
+ * workspace: concurrent calls on one pool are allowed, as for pa_decode_selected.
+ */
+#define PA_SELECT_MAX_BUDGET 4096
+#define PA_SELECT_MAX_BLOCKS 262144
+pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, const int32_t *block_tables,
+                           int32_t block_table_stride, const int32_t *context_lens, int32_t num_seqs,
+                           int32_t num_q_heads, int32_t q_len, int32_t budget, int32_t num_first, int32_t num_last,
+                           int32_t *selected, void *stream);
+
+/*
+ * pa_decode over listed blocks only: row (b, qi) sits at position
+ * context_lens[b] - q_len + qi and attends to the tokens at or before it in the
+ * blocks selected[b][h / (num_q_heads / num_kv_heads)][0 .. budget). The list is
+ * pa_select_blocks's or any other, in any order; negative entries are skipped, a
+ * block listed twice counts twice. A row that sees no listed token gives zeros
+ * (so does a context of 0). Values at positions a row does not see do not reach
+ * it, whatever their words are. Softmax and sums are fp32; deterministic run to
+ * run. 16-bit pools with heads of 64 or 128 and FP8 pools.
+ *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping
+ *   selected       device int32 [num_seqs, num_kv_heads, budget]; budget 1 .. PA_SELECT_MAX_BUDGET
+ *   scale          softmax scale, finite
+ * the others as pa_select_blocks. Entries beyond the context, lengths and block
+ * ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at pa_pool_check); such
+ * an entry is skipped, such a length is clamped.
+ */
+pa_status pa_decode_selected(pa_pool *pool, const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *selected, int32_t budget, const int32_t *block_tables,
+                             int32_t block_table_stride, const int32_t *context_lens, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t q_len, float scale, void *out, void *stream);
+
+/*
  * Synchronise the device, read and clear the pool's status word.
- * Returns PA_OK, PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT or PA_ERR_CUDA.
+ * Returns PA_OK, PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT, PA_ERR_OOM (pa_step_tables:
+ * a step needed more blocks than were free) or PA_ERR_CUDA.
  */
 pa_status pa_pool_check(pa_pool *pool, void *stream);
 

@@ -6,6 +6,7 @@
 
 #include "pa_pool.h"
 #include "pa_serving.h"
+#include "pa_sparse.h"
 
 using namespace pa;
 
@@ -23,11 +24,9 @@ PFN_cuTensorMapEncodeTiled_v12000 pa::encode_fn() {
     return fn;
 }
 
-namespace {
-
 // The pool seen as a 2-D tensor: rows = num_blocks * Hkv * block_size key rows of head_dim
 // elements. Boxes are 16 rows x 64 elements (128 bytes), swizzled 128B in shared memory.
-pa_status tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
+pa_status pa::tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
     std::lock_guard<std::mutex> lk(pool->mu);
     auto it = pool->maps.find(cache);
     if (it != pool->maps.end()) {
@@ -54,6 +53,8 @@ pa_status tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
     *out = m;
     return PA_OK;
 }
+
+namespace {
 
 void free_pool(pa_pool *p) {
     if (!p) return;
@@ -505,6 +506,7 @@ pa_status pa_pool_check(pa_pool *pool, void *stream) {
         return PA_ERR_CUDA;
     if (h & STATUS_TIMEOUT) return PA_ERR_TIMEOUT;
     if (h & STATUS_BOUNDS) return PA_ERR_DEVICE_BOUNDS;
+    if (h & STATUS_NO_BLOCKS) return PA_ERR_OOM;
     return PA_OK;
 }
 

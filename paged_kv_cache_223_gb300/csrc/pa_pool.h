@@ -49,4 +49,7 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 // cuTensorMapEncodeTiled, looked up once (nullptr: the driver has none).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
+// The map of one of the pool's caches for copies of 16 token rows, kept per cache address.
+pa_status tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out);
+
 }  // namespace pa

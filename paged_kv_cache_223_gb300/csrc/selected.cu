@@ -1,0 +1,567 @@
+// selected.cu -- attention of new query rows over a list of blocks for each (sequence, KV head).
+//
+// out = sum_t softmax_t(scale q . K_t) V_t over the tokens t of the listed blocks that are at or before the row's
+// position, by one pass with the running maximum and sum; rows that see none of them give zeros.
+//
+// What bounds it: the K and V rows of the listed blocks, read once. A unit (sequence, KV head; all its query rows together)
+// is one cluster of CTAs. Its tiles of 16 tokens are dealt out to the warps of the whole cluster in turn, so a list that is
+// short of its budget still spreads over all of them. Every warp looks its tiles up (list, then block table) before its
+// first copy, keeps those that hold tokens, and runs a pipeline of its own over them: TMA tile loads, scores S^T = K Q^T
+// and O^T += V^T P^T as warp-level products with the query rows as columns, softmax in fp32 between them. The states of a
+// CTA's warps are joined in its shared memory, those of the cluster's CTAs through each other's, each CTA writing a share
+// of the outputs: one launch, no workspace, a fixed order.
+#include <type_traits>
+
+#include "pa_cluster.cuh"
+#include "pa_device.cuh"
+#include "pa_sparse.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int ATT_WARPS = 4;
+constexpr int ATT_THREADS = ATT_WARPS * 32;
+constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
+
+__host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
+__host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : !kv8 && nt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int att_tile_bytes(int D, bool kv8) { return TILE_TOKENS * (kv8 ? 128 : 2 * D); }
+__host__ __device__ constexpr int att_scale_bytes(bool kv8, int nt) {
+    return kv8 ? (ATT_WARPS * att_stages(kv8, nt) * 2 * TILE_TOKENS * 4 + 1023) / 1024 * 1024 : 0;
+}
+__host__ __device__ constexpr int att_ring_bytes(int D, bool kv8, int nt) {
+    return ATT_WARPS * att_stages(kv8, nt) * 2 * att_tile_bytes(D, kv8) + att_scale_bytes(kv8, nt);
+}
+// states of the warps [W][RP][D + 4] and (max, sum) [W][RP], the CTA's own [RP][D + 4] and (max, sum) [RP], factors [RP][W]
+__host__ __device__ constexpr int att_join_bytes(int D, int nt) {
+    return 4 * nt * 8 * ((ATT_WARPS + 1) * (D + 4) + (ATT_WARPS + 1) * 2 + ATT_WARPS);
+}
+__host__ __device__ constexpr int att_body_bytes(int D, bool kv8, int nt) {
+    return (att_ring_bytes(D, kv8, nt) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8, nt) : att_join_bytes(D, nt)) + 15 & ~15;
+}
+
+__device__ __forceinline__ float value16(uint16_t w, __half) { return __half2float(__ushort_as_half(w)); }
+__device__ __forceinline__ float value16(uint16_t w, __nv_bfloat16) { return __bfloat162float(__ushort_as_bfloat16(w)); }
+
+}  // namespace
+
+template <typename T, int D, int NT, bool KV8>
+__global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
+    selected_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                    const SelectedParams p) {
+    static_assert(!KV8 || D == 128, "FP8 pools are built for head_dim 128");
+    using M = typename std::conditional<KV8, __half, T>::type;   // E4M3 codes are exact in fp16
+    constexpr int W = ATT_WARPS, STAGES = att_stages(KV8, NT);
+    constexpr int TILE = att_tile_bytes(D, KV8), STAGE = 2 * TILE, SPAN = TILE_TOKENS * 128;   // 128-byte swizzle spans
+    constexpr int KS = D / 16, MT = D / 16, RP = NT * 8, OS = D + 4;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base_u32 - smem_u32(smem_raw));
+    constexpr int BODY = att_body_bytes(D, KV8, NT);
+    const uint32_t bars_u32 = base_u32 + BODY;
+    int *failed = reinterpret_cast<int *>(smem + BODY + W * STAGES * 8);
+    int2 *lists = reinterpret_cast<int2 *>(smem + BODY + W * STAGES * 8 + 16);     // [W][warp_tiles]: pool row, position
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    const int unit = (int)(blockIdx.x / ranks), g = unit % p.Hkv, b = unit / p.Hkv;
+    pdl_trigger();
+    pdl_wait();
+
+    int L = __ldg(p.context_lens + b);
+    if (L < 0 || L > p.max_len || (L > 0 && L < p.q_len)) {
+        if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
+        L = L < 0 ? 0 : min(L, p.max_len);
+    }
+
+    // ---- this warp's tiles: those of the listed blocks that hold tokens
+    int2 *list = lists + warp * p.warp_tiles;
+    int tiles = 0;
+    {
+        const int all = p.budget * (p.bs / TILE_TOKENS), step = ranks * W, blocks = (L + p.bs - 1) / p.bs;
+        for (int i0 = rank * W + warp; i0 < all; i0 += 32 * step) {
+            const int i = i0 + lane * step;
+            int row = 0, pos = -1;
+            if (i < all) {
+                const int tok = i * TILE_TOKENS, off = tok % p.bs;
+                const int j = __ldg(p.selected + (int64_t)unit * p.budget + tok / p.bs);
+                if (j >= blocks) set_status(p.status, STATUS_BOUNDS);
+                else if (j >= 0 && j * p.bs + off < L) {
+                    const int id = __ldg(p.block_tables + b * p.stride + j);
+                    if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
+                    else row = (id * p.Hkv + g) * p.bs + off, pos = j * p.bs + off;
+                }
+            }
+            const uint32_t have = __ballot_sync(0xffffffffu, pos >= 0);
+            if (pos >= 0) list[tiles + __popc(have & ((1u << lane) - 1u))] = make_int2(row, pos);
+            tiles += __popc(have);
+        }
+    }
+    if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(bars_u32 + (warp * STAGES + s) * 8, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+
+    const uint32_t ring_u32 = base_u32 + warp * STAGES * STAGE;
+    const uint32_t scales_u32 = base_u32 + W * STAGES * STAGE + warp * STAGES * 2 * TILE_TOKENS * 4;   // FP8 only
+    const uint64_t policy = l2_policy_evict_first();
+    auto issue = [&](int it) {
+        const int s = it % STAGES, row = list[it].x;
+        const uint32_t bar = bars_u32 + (warp * STAGES + s) * 8, dst = ring_u32 + s * STAGE;
+        fence_proxy_async_smem();
+        if constexpr (KV8) {
+            const uint32_t sdst = scales_u32 + s * 2 * TILE_TOKENS * 4;
+            mbar_arrive_expect_tx(bar, STAGE + 2 * TILE_TOKENS * 4);
+            tma_load_2d(dst, &tmk, 0, row, bar, policy);
+            tma_load_2d(dst + TILE, &tmv, 0, row, bar, policy);
+            bulk_load(sdst, p.k_scales + row, TILE_TOKENS * 4, bar, policy);
+            bulk_load(sdst + TILE_TOKENS * 4, p.v_scales + row, TILE_TOKENS * 4, bar, policy);
+        } else {
+            mbar_arrive_expect_tx(bar, STAGE);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                tma_load_2d(dst + h * SPAN, &tmk, h * 64, row, bar, policy);
+                tma_load_2d(dst + TILE + h * SPAN, &tmv, h * 64, row, bar, policy);
+            }
+        }
+    };
+    int issued = min(tiles, STAGES);
+    if (lane == 0)
+        for (int it = 0; it < issued; ++it) issue(it);
+
+    // ---- query rows as the B operand. FP8 pools: a lane's four codes are consecutive dimensions, the contraction's order
+    // is theirs, and a bf16 row is taken into fp16's range by a power of two that its scores get back.
+    uint32_t qf[NT][KS][2];
+    float qscale[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + gq;
+        qscale[nt][0] = qscale[nt][1] = p.scale_log2;
+        if (r < p.rows) {
+            const int qi = r / p.G, hh = r - qi * p.G;
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(
+                static_cast<const T *>(p.q) + (((int64_t)b * p.q_len + qi) * p.Hq + g * p.G + hh) * D);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                qf[nt][ks][0] = __ldg(q + ks * 8 + (KV8 ? 2 * tq : tq));
+                qf[nt][ks][1] = __ldg(q + ks * 8 + (KV8 ? 2 * tq + 1 : 4 + tq));
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) qf[nt][ks][0] = qf[nt][ks][1] = 0u;
+        }
+        if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value) {
+            uint32_t top = 0;                          // bf16 without its sign, as an integer: the exponent on top
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t x = qf[nt][ks][e];
+                    top = max(top, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^-(e - 127 - 14): the largest magnitude below 2^15; rows of at most 2^15 stay as they are
+            const int e = (int)(top >> 7);
+            const bool large = e > 141 && e < 255;
+            const float down = large ? __uint_as_float((uint32_t)(127 + 141 - e) << 23) : 1.f;
+            const float up = large ? __uint_as_float((uint32_t)(127 + e - 141) << 23) : 1.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qf[nt][ks][k]));
+                    qf[nt][ks][k] = pack2<__half>(f.x * down, f.y * down);
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) qscale[nt][j] *= __shfl_sync(0xffffffffu, up, (2 * tq + j) * 4);
+        }
+    }
+
+    int last[NT][2];                                   // positions of the columns' rows: the newest token that they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) last[nt][j] = L - p.q_len + min((nt * 8 + 2 * tq + j) / p.G, p.q_len - 1);
+    const int seen_by_all = L - p.q_len + 1;           // tokens before this one
+
+    float m[NT][2], l[NT][2], o[MT][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int md = 0; md < MT; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
+    }
+
+    int vexp = 0;                                      // FP8: O is in units of 2^vexp
+    bool vset = false;
+    bool ok = true;
+    int it = 0;
+    for (; it < tiles; ++it) {
+        const int s = it % STAGES;
+        if (!mbar_wait_bounded(bars_u32 + (warp * STAGES + s) * 8, (uint32_t)(it / STAGES) & 1u, p.wait_ns)) {
+            ok = false;
+            break;
+        }
+        const int pos = list[it].y;
+        const uint32_t kb = ring_u32 + s * STAGE, vb = kb + TILE;
+        const float *scale_k = reinterpret_cast<const float *>(smem + (scales_u32 - base_u32) + s * 2 * TILE_TOKENS * 4);
+        const float *scale_v = scale_k + TILE_TOKENS;
+
+        // S^T = K Q^T: 16 keys, 8 NT query rows
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
+        if constexpr (KV8) {
+#pragma unroll
+            for (int kp = 0; kp < KS / 2; ++kp) {
+                const int chunk = kp * 2 + (lane >> 4);
+                uint32_t r0, r1, r2, r3;
+                ldsm_x4(kb + krow * 128 + ((chunk ^ (krow & 7)) << 4), r0, r1, r2, r3);
+                const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)r0), a2 = e4m3x2_to_f16x2((uint16_t)(r0 >> 16));
+                const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)r1), a3 = e4m3x2_to_f16x2((uint16_t)(r1 >> 16));
+                const uint32_t c0 = e4m3x2_to_f16x2((uint16_t)r2), c2 = e4m3x2_to_f16x2((uint16_t)(r2 >> 16));
+                const uint32_t c1 = e4m3x2_to_f16x2((uint16_t)r3), c3 = e4m3x2_to_f16x2((uint16_t)(r3 >> 16));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_16816<M>(sc[nt], a0, a1, a2, a3, qf[nt][2 * kp][0], qf[nt][2 * kp][1]);
+                    mma_16816<M>(sc[nt], c0, c1, c2, c3, qf[nt][2 * kp + 1][0], qf[nt][2 * kp + 1][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const int chunk = ks * 2 + (lane >> 4);
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(kb + (chunk >> 3) * SPAN + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_16816<M>(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+            }
+        }
+
+        // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8
+        const int t0 = pos + gq, t1 = t0 + 8;
+        float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
+        float alpha[NT][2];
+        bool moved = false;
+        if constexpr (KV8) {
+            ks0 = scale_k[gq], ks1 = scale_k[gq + 8], vs0 = scale_v[gq], vs1 = scale_v[gq + 8];
+            // weights times V scales go into the product as fp16: below 2^8 times 2^5 of the largest scale's power of two,
+            // of the tokens that every row sees (the others are added apart)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(t0 < seen_by_all ? __float_as_uint(vs0) & 0x7FFFFFFFu : 0u,
+                                                                    t1 < seen_by_all ? __float_as_uint(vs1) & 0x7FFFFFFFu : 0u));
+            const int e = min(max((int)(top >> 23) - 127, -60), 100);
+            if (top != 0 && (!vset || e > vexp + 4)) {
+                const float f = ldexpf(1.f, vexp - e);
+#pragma unroll
+                for (int md = 0; md < MT; ++md)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[md][nt][k] *= f;
+                vexp = e;
+                vset = true;
+            }
+            const float unit_v = __uint_as_float((uint32_t)(127 - vexp) << 23);   // 2^-vexp
+            vs0 *= unit_v, vs1 *= unit_v;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // what a masked place holds (a score, a scale) is selected away, not multiplied
+                const float s0 = t0 <= last[nt][j] ? sc[nt][j] * (ks0 * qscale[nt][j]) : -INFINITY;
+                const float s1 = t1 <= last[nt][j] ? sc[nt][2 + j] * (ks1 * qscale[nt][j]) : -INFINITY;
+                float mx = fmaxf(s0, s1);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                alpha[nt][j] = 1.f;
+                if (mx > m[nt][j] + ATT_RESCALE_LOG2) {
+                    alpha[nt][j] = ex2_approx(m[nt][j] - mx);
+                    m[nt][j] = mx;
+                    moved = true;
+                }
+                const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+                const float p0 = ex2_approx(s0 - ref), p1 = ex2_approx(s1 - ref);
+                l[nt][j] = l[nt][j] * alpha[nt][j] + p0 + p1;
+                sc[nt][j] = p0 * vs0;
+                sc[nt][2 + j] = p1 * vs1;
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int md = 0; md < MT; ++md) {
+                        o[md][nt][j] *= alpha[nt][j];
+                        o[md][nt][2 + j] *= alpha[nt][j];
+                    }
+        }
+
+        // Values that not every row sees may be anything to the others, and what lies behind the context anything at all.
+        // The tiles at the end of the context: such values are added row by row in fp32, then their weights and words are 0.
+        const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
+        if (whole < TILE_TOKENS) {
+            const int w0 = whole < 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos);
+            for (int kk = w0; kk < w1; ++kk) {
+                const int src = (kk & 7) * 4 + tq;     // the lane that holds this token's weights of the same columns
+                float pv[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float x = __shfl_sync(0xffffffffu, sc[nt][j], src), y = __shfl_sync(0xffffffffu, sc[nt][2 + j], src);
+                        pv[nt][j] = kk < 8 ? x : y;
+                    }
+#pragma unroll
+                for (int md = 0; md < MT; ++md)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v;
+                        if constexpr (KV8) {
+                            const int dim = md * 16 + 2 * gq + e;
+                            const uint8_t code = smem[(vb - base_u32) + kk * 128 + (((dim >> 4) ^ (kk & 7)) << 4) + (dim & 15)];
+                            const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)code);
+                            v = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
+                        } else {
+                            const int dim = md * 16 + gq + 8 * e, c = dim >> 3;
+                            v = value16(*reinterpret_cast<const uint16_t *>(smem + (vb - base_u32) + (c >> 3) * SPAN + kk * 128 +
+                                                                            (((c & 7) ^ (kk & 7)) << 4) + (dim & 7) * 2), T());
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (pos + kk <= last[nt][j]) o[md][nt][2 * e + j] += pv[nt][j] * v;
+                    }
+            }
+            __syncwarp();
+            const int zero = TILE_TOKENS - w0;
+            for (int c = lane; c < zero * 8 * (TILE / SPAN); c += 32) {
+                const int h = c / (zero * 8), rc = c - h * zero * 8;
+                *reinterpret_cast<uint4 *>(smem + (vb - base_u32) + h * SPAN + (w0 + rc / 8) * 128 + (rc % 8) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (gq >= w0) sc[nt][j] = 0.f;
+                    if (gq + 8 >= w0) sc[nt][2 + j] = 0.f;
+                }
+        }
+
+        // P^T as the B operand, in V's type; bf16 has too few bits for one part, so it is carried as two (the nearest bf16
+        // and what is left of it), fp16's eleven do alone
+        constexpr bool TWO = std::is_same<M, __nv_bfloat16>::value;
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float x = sc[nt][2 * k], y = sc[nt][2 * k + 1];
+                const uint32_t hi = pack2<M>(x, y);
+                ph[nt][k] = movmatrix_trans(hi);
+                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u)))
+                                : 0u;
+            }
+
+        // O^T += V^T P^T
+        if constexpr (KV8) {
+            // a lane gets two keys of two neighbouring dimensions: the even ones are rows 0-7 of the fragment, the odd 8-15
+            const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+            for (int mp = 0; mp < MT / 2; ++mp) {
+                const int chunk = mp * 2 + (lane >> 4);
+                uint32_t r[4];
+                ldsm_x4_trans(vb + vrow * 128 + ((chunk ^ (vrow & 7)) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t lo = r[2 * h], hi = r[2 * h + 1];
+                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4420));
+                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4431));
+                    const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4420));
+                    const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4431));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                }
+            }
+        } else {
+            const int vrow = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+            for (int md = 0; md < MT; ++md) {
+                const int chunk = md * 2 + ((lane >> 3) & 1);
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4_trans(vb + (chunk >> 3) * SPAN + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_16816<M>(o[md][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                    if constexpr (TWO) mma_16816<M>(o[md][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (it + STAGES < tiles) {
+            if (lane == 0) issue(it + STAGES);
+            ++issued;
+        }
+    }
+    if (!ok && lane == 0)                              // no copy lands behind the end of the pipeline
+        for (int k = it; k < issued; ++k)
+            mbar_wait_bounded(bars_u32 + (warp * STAGES + (k % STAGES)) * 8, (uint32_t)(k / STAGES) & 1u, p.wait_ns);
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+        }
+    const int lost = __syncthreads_or(!ok);            // the ring is free now
+    if (tid == 0) {
+        *failed = lost;
+        if (lost) set_status(p.status, STATUS_TIMEOUT);
+    }
+
+    // ---- the warps' states
+    const float unit_o = __uint_as_float((uint32_t)(127 + vexp) << 23);   // 2^vexp
+    float *ow = reinterpret_cast<float *>(smem);       // [W][RP][OS]
+    float *oc = ow + W * RP * OS;                      // [RP][OS]
+    float2 *mw = reinterpret_cast<float2 *>(oc + RP * OS);   // [W][RP] (maximum, sum)
+    float2 *mc = mw + W * RP;                          // [RP]
+    float *fw = reinterpret_cast<float *>(mc + RP);    // [RP][W] factors
+#pragma unroll
+    for (int md = 0; md < MT; ++md)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dim = md * 16 + (KV8 ? 2 * gq + (e >> 1) : gq + (e >> 1) * 8);
+                ow[(warp * RP + nt * 8 + 2 * tq + (e & 1)) * OS + dim] = KV8 ? o[md][nt][e] * unit_o : o[md][nt][e];
+            }
+    if (gq == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mw[warp * RP + nt * 8 + 2 * tq + j] = make_float2(m[nt][j], l[nt][j]);
+    }
+    __syncthreads();
+    for (int r = tid; r < p.rows; r += ATT_THREADS) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) top = fmaxf(top, mw[w * RP + r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = exp2f(mw[w * RP + r].x - ref);
+            fw[r * W + w] = f;
+            sum += f * mw[w * RP + r].y;
+        }
+        mc[r] = make_float2(top, sum);
+    }
+    __syncthreads();
+    constexpr int D8 = D / 8;
+    const auto store = [&](int r, int d0, const float (&a)[8], float sum) {
+        const int qi = r / p.G, h = g * p.G + (r - qi * p.G);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing: zeros
+        uint4 v;
+        v.x = pack2<T>(a[0] * inv, a[1] * inv);
+        v.y = pack2<T>(a[2] * inv, a[3] * inv);
+        v.z = pack2<T>(a[4] * inv, a[5] * inv);
+        v.w = pack2<T>(a[6] * inv, a[7] * inv);
+        *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (((int64_t)b * p.q_len + qi) * p.Hq + h) * D + d0) = v;
+    };
+    for (int idx = tid; idx < p.rows * D8; idx += ATT_THREADS) {
+        const int r = idx / D8, d0 = (idx - r * D8) * 8;
+        float a[8] = {};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = fw[r * W + w];
+            const float4 x = *reinterpret_cast<const float4 *>(ow + (w * RP + r) * OS + d0);
+            const float4 y = *reinterpret_cast<const float4 *>(ow + (w * RP + r) * OS + d0 + 4);
+            a[0] += f * x.x, a[1] += f * x.y, a[2] += f * x.z, a[3] += f * x.w;
+            a[4] += f * y.x, a[5] += f * y.y, a[6] += f * y.z, a[7] += f * y.w;
+        }
+        if (ranks == 1) {
+            if (!lost) store(r, d0, a, mc[r].y);
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(oc + r * OS + d0);
+            dst[0] = make_float4(a[0], a[1], a[2], a[3]);
+            dst[1] = make_float4(a[4], a[5], a[6], a[7]);
+        }
+    }
+    if (ranks == 1) return;
+
+    // ---- the CTAs' states, each CTA a share of the outputs
+    cluster_sync();
+    int any_failed = 0;
+    for (int c = 0; c < ranks; ++c) any_failed |= ld_cluster_int(map_rank(smem_u32(failed), c));
+    if (!any_failed) {
+        for (int idx = rank * ATT_THREADS + tid; idx < p.rows * D8; idx += ranks * ATT_THREADS) {
+            const int r = idx / D8, d0 = (idx - r * D8) * 8;
+            float top = -INFINITY, sum = 0.f, a[8] = {};
+            for (int c = 0; c < ranks; ++c) top = fmaxf(top, ld_cluster_float2(map_rank(smem_u32(mc + r), c)).x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            for (int c = 0; c < ranks; ++c) {
+                const float2 ms = ld_cluster_float2(map_rank(smem_u32(mc + r), c));
+                const uint32_t src = map_rank(smem_u32(oc + r * OS + d0), c);
+                const float4 x = ld_cluster_float4(src), y = ld_cluster_float4(src + 16);
+                const float f = exp2f(ms.x - ref);
+                sum += f * ms.y;
+                a[0] += f * x.x, a[1] += f * x.y, a[2] += f * x.z, a[3] += f * x.w;
+                a[4] += f * y.x, a[5] += f * y.y, a[6] += f * y.z, a[7] += f * y.w;
+            }
+            store(r, d0, a, sum);
+        }
+    }
+    cluster_sync();                                    // nobody reads this CTA's memory any more
+}
+
+template <typename T, int D, bool KV8>
+static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, const CUtensorMap &tmv, int sm_count,
+                                     cudaStream_t stream) {
+    const int64_t units = (int64_t)p.num_seqs * p.Hkv;
+    const int tiles = p.budget * (p.bs / TILE_TOKENS), nt = (p.rows + 7) / 8;
+    // CTAs of a cluster: enough for four rounds of resident CTAs, each with four tiles for every warp at least
+    int ranks = 1;
+    while (ranks < 8 && units * ranks < 4LL * att_ctas(KV8, nt) * sm_count && tiles >= 2 * ranks * ATT_WARPS * 4) ranks *= 2;
+    p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
+    const auto launch = [&](auto kernel, int n) {
+        const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8, n) * 8 + 16 +
+                            (size_t)ATT_WARPS * p.warp_tiles * 8;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        return e != cudaSuccess
+                   ? e
+                   : launch_clusters(kernel, (unsigned)(units * ranks), ATT_THREADS, smem, ranks, stream, tmk, tmv, p);
+    };
+    switch (nt) {
+        case 1: return launch(selected_kernel<T, D, 1, KV8>, 1);
+        case 2: return launch(selected_kernel<T, D, 2, KV8>, 2);
+        case 3: return launch(selected_kernel<T, D, 3, KV8>, 3);
+        default: return launch(selected_kernel<T, D, 4, KV8>, 4);
+    }
+}
+
+cudaError_t launch_selected(SelectedParams p, int dtype, int head_dim, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                            int sm_count, cudaStream_t stream) {
+    if (p.k_scales)
+        return dtype == PA_FP16 ? launch_selected_t<__half, 128, true>(p, tmk, tmv, sm_count, stream)
+                                : launch_selected_t<__nv_bfloat16, 128, true>(p, tmk, tmv, sm_count, stream);
+    if (dtype == PA_FP16)
+        return head_dim == 128 ? launch_selected_t<__half, 128, false>(p, tmk, tmv, sm_count, stream)
+                               : launch_selected_t<__half, 64, false>(p, tmk, tmv, sm_count, stream);
+    return head_dim == 128 ? launch_selected_t<__nv_bfloat16, 128, false>(p, tmk, tmv, sm_count, stream)
+                           : launch_selected_t<__nv_bfloat16, 64, false>(p, tmk, tmv, sm_count, stream);
+}
+
+}  // namespace pa

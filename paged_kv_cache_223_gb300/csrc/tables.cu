@@ -1,0 +1,173 @@
+// tables.cu -- the tables of a serving step on the device: sequences are cut back, given new tokens and the blocks
+// that those need; positions and slots of the new tokens.
+//
+// With kept = min(length, keep), have = ceil(kept / bs), old = ceil(length / bs), want = max(have, ceil((kept + new) / bs)):
+// blocks [have, old) of every sequence go back on the free stack, then every sequence takes want - have from its top, both
+// in the order of (sequence, block), the returned ones so that the first of them ends on top. Exclusive sums B and T of
+// old - have and want - have over the sequences place every move by itself: with n blocks free and F returned, returned
+// block i lies at n + F - 1 - i, taken block i comes from n + F - 1 - i. Cutting back what a step took and taking it
+// again therefore gives the same blocks.
+//
+// One cluster does all of it: every CTA makes the sums of all sequences for itself (they are few words), checks them and
+// comes to the same verdict, the CTAs share the returned blocks, meet at the cluster's barrier, and share the taken blocks,
+// the tokens and the new lengths. So the lengths, tables and the stack are changed in place by one launch without a
+// workspace, and a call that is refused changes nothing of them.
+#include "pa_cluster.cuh"
+#include "pa_device.cuh"
+#include "pa_sparse.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int TAB_THREADS = 512;
+
+struct Sums {
+    long long tokens, back, taken;
+};
+
+__device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) {
+    return {a.tokens + b.tokens, a.back + b.back, a.taken + b.taken};
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums &v, int d) {
+    return {__shfl_up_sync(0xffffffffu, v.tokens, d), __shfl_up_sync(0xffffffffu, v.back, d),
+            __shfl_up_sync(0xffffffffu, v.taken, d)};
+}
+
+// The last index b < n with start[b] <= i, for i below start[n].
+__device__ __forceinline__ int owner(const int *start, int n, int i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams p) {
+    extern __shared__ int tsm[];
+    const int B = p.num_seqs;
+    int *cu = tsm, *back = cu + B + 1, *taken = back + B + 1, *kept = taken + B + 1;   // sums of B + 1, then [B]
+    __shared__ Sums wsum[TAB_THREADS / 32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    const int all = threads * ranks, gid = rank * threads + tid;
+    pdl_trigger();
+    pdl_wait();
+
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    const int bs = 1 << p.bs_shift;
+    const int n_free = __ldcg(p.num_free);
+    Sums carry = {0, 0, 0};
+    for (int b0 = 0; b0 < B; b0 += threads) {
+        const int b = b0 + tid;
+        Sums v = {0, 0, 0};
+        if (b < B) {
+            const int len = __ldcg(p.context_lens + b), add = __ldcg(p.new_lens + b);
+            const int keep = p.keep_lens ? __ldcg(p.keep_lens + b) : len;
+            const int k = keep < len ? keep : len;
+            if (len < 0 || len > p.max_len || add < 0 || keep < 0 || (long long)k + add > p.max_len) {
+                bad = 1;                               // every writer writes the same
+            } else {
+                const int have = (int)(((long long)k + bs - 1) >> p.bs_shift);
+                const int old = (int)(((long long)len + bs - 1) >> p.bs_shift);
+                const int want = (int)(((long long)k + add + bs - 1) >> p.bs_shift);
+                v = {add, old - have, want > have ? want - have : 0};
+                kept[b] = k;
+            }
+        }
+        Sums s = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sums u = shfl_up(s, d);
+            if (lane >= d) s = s + u;
+        }
+        if (lane == 31) wsum[warp] = s;
+        __syncthreads();
+        Sums before = carry;
+        for (int w = 0; w < threads / 32; ++w) {
+            if (w < warp) before = before + wsum[w];
+            carry = carry + wsum[w];
+        }
+        if (b < B) {
+            cu[b] = (int)(before.tokens + s.tokens - v.tokens);
+            back[b] = (int)(before.back + s.back - v.back);
+            taken[b] = (int)(before.taken + s.taken - v.taken);
+        }
+        __syncthreads();
+    }
+    const bool wrong = bad || n_free < 0 || n_free > p.num_blocks || n_free + carry.back > p.num_blocks ||
+                       carry.tokens > p.num_tokens;
+    const bool none_left = !wrong && carry.taken > n_free + carry.back;
+    if (wrong || none_left) {                          // the same in every CTA: no table, length or block is touched
+        if (gid == 0) set_status(p.status, wrong ? STATUS_BOUNDS : STATUS_NO_BLOCKS);
+        for (int b = gid; b <= B; b += all) p.cu_q[b] = 0;
+        for (int i = gid; i < p.num_tokens; i += all) {
+            p.positions[i] = 0;
+            p.slots[i] = -1;
+        }
+        return;
+    }
+    const int tokens = (int)carry.tokens, F = (int)carry.back, T = (int)carry.taken, top = n_free + F - 1;
+    if (tid == 0) {
+        cu[B] = tokens;
+        back[B] = F;
+        taken[B] = T;
+    }
+    __syncthreads();
+
+    // returned blocks onto the stack
+    for (int i = gid; i < F; i += all) {
+        const int b = owner(back, B, i);
+        const int j = ((kept[b] + bs - 1) >> p.bs_shift) + i - back[b];
+        const int id = __ldcg(p.block_tables + b * p.stride + j);
+        if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
+        __stcg(p.free_blocks + top - i, id);
+    }
+    cluster_sync();                                    // every CTA has read the lengths; the stack is whole
+
+    for (int i = gid; i < T; i += all) {
+        const int b = owner(taken, B, i);
+        const int j = ((kept[b] + bs - 1) >> p.bs_shift) + i - taken[b];
+        const int id = __ldcg(p.free_blocks + top - i);
+        if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
+        p.block_tables[b * p.stride + j] = id;
+    }
+    for (int i = gid; i < p.num_tokens; i += all) {
+        int pos = 0;
+        int64_t slot = -1;
+        if (i < tokens) {
+            const int b = owner(cu, B, i);
+            pos = kept[b] + i - cu[b];
+            const int have = (kept[b] + bs - 1) >> p.bs_shift, j = pos >> p.bs_shift;
+            // a block that this call takes is read where it comes from, not from the table that it is written to
+            const int id = j < have ? __ldcg(p.block_tables + b * p.stride + j)
+                                    : __ldcg(p.free_blocks + top - (taken[b] + j - have));
+            if (id >= 0 && id < p.num_blocks) slot = ((int64_t)id << p.bs_shift) + (pos & (bs - 1));
+            else set_status(p.status, STATUS_BOUNDS);
+        }
+        p.positions[i] = pos;
+        p.slots[i] = slot;
+    }
+    for (int b = gid; b <= B; b += all) {
+        p.cu_q[b] = cu[b];
+        if (b < B) p.context_lens[b] = kept[b] + cu[b + 1] - cu[b];
+    }
+    if (gid == 0) *p.num_free = n_free + F - T;
+}
+
+cudaError_t launch_tables(const TablesParams &p, int sm_count, cudaStream_t stream) {
+    const size_t smem = (size_t)(4 * p.num_seqs + 3) * sizeof(int);
+    const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int cluster = 1;
+    return launch_clusters(tables_kernel, cluster, TAB_THREADS, smem, cluster, stream, p);
+}
+
+}  // namespace pa

@@ -222,6 +222,34 @@ def _serving_lib() -> C.CDLL:
     return L
 
 
+_sparse_ready = False
+
+
+class PaTablesArgs(C.Structure):
+    _fields_ = [("num_seqs", C.c_int32), ("num_tokens", C.c_int32), ("block_table_stride", C.c_int32),
+                ("new_lens", C.c_void_p), ("keep_lens", C.c_void_p), ("context_lens", C.c_void_p),
+                ("block_tables", C.c_void_p), ("free_blocks", C.c_void_p), ("num_free", C.c_void_p), ("cu_q", C.c_void_p),
+                ("positions", C.c_void_p), ("slot_mapping", C.c_void_p)]
+
+
+def _sparse_lib() -> C.CDLL:
+    global _sparse_ready
+    if _sparse_ready:
+        return _lib
+    L = lib()
+    if not _sparse_ready:
+        P, I32 = C.c_void_p, C.c_int32
+        L.pa_step_tables.argtypes = [P, C.POINTER(PaTablesArgs), P]
+        L.pa_key_bounds_size.argtypes = [P, C.POINTER(C.c_uint64)]
+        L.pa_key_bounds.argtypes = [P, P, P, P, I32, P, I32, I32, P, P]
+        L.pa_select_blocks.argtypes = [P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, P]
+        L.pa_decode_selected.argtypes = [P, P, P, P, P, I32, P, I32, P, I32, I32, I32, C.c_float, P, P]
+        for f in ("pa_step_tables", "pa_key_bounds_size", "pa_key_bounds", "pa_select_blocks", "pa_decode_selected"):
+            getattr(L, f).restype = C.c_int
+        _sparse_ready = True
+    return L
+
+
 class Pool:
     """One paged KV pool (pa_pool_create) with its caches.
 
@@ -442,6 +470,140 @@ class Pool:
         _check(_serving_lib().pa_prefill_packed_workspace(self.handle, num_tokens, num_seqs, num_q_heads,
                                                           block_table_stride, n), "pa_prefill_packed_workspace")
         return n.value
+
+    def step_tables(self, new_lens: torch.Tensor, context_lens: torch.Tensor, block_tables: torch.Tensor,
+                    free_blocks: torch.Tensor, num_free: torch.Tensor, num_tokens: int,
+                    keep_lens: Optional[torch.Tensor] = None, cu_q: Optional[torch.Tensor] = None,
+                    positions: Optional[torch.Tensor] = None, slot_mapping: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """The tables of a step on the device (pa_step_tables): sequences are cut back to keep_lens, given new_lens
+        tokens and the blocks that these need. context_lens [B], block_tables [B, stride], free_blocks
+        [num_blocks] (a stack of num_free[0] ids) and num_free [1] are changed in place (all int32). Returns
+        cu_q int32 [B + 1], positions int32 and slot_mapping int64 [num_tokens]: 0 and -1 behind the last token."""
+        index, i32, num_tokens = self.device.index, torch.int32, int(num_tokens)
+        if new_lens.dim() != 1 or block_tables.dim() != 2:
+            raise ValueError(f"new_lens must be [B], block_tables [B, stride]: got {tuple(new_lens.shape)}, "
+                             f"{tuple(block_tables.shape)}")
+        B, stride = new_lens.shape[0], block_tables.shape[1]
+        _need(new_lens, "new_lens", i32, index, (B,))
+        _need(context_lens, "context_lens", i32, index, (B,))
+        _need(block_tables, "block_tables", i32, index, (B, stride))
+        _need(free_blocks, "free_blocks", i32, index, (self.geometry[0],))
+        _need(num_free, "num_free", i32, index, (1,))
+        if keep_lens is not None:
+            _need(keep_lens, "keep_lens", i32, index, (B,))
+        if num_tokens < 0:
+            raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
+        for name, t, dt, n in (("cu_q", cu_q, i32, B + 1), ("positions", positions, i32, num_tokens),
+                               ("slot_mapping", slot_mapping, torch.int64, num_tokens)):
+            if t is not None:
+                _need(t, name, dt, index, (n,))
+        cu_q = _new((B + 1,), i32, self.device, stream) if cu_q is None else cu_q
+        positions = _new((num_tokens,), i32, self.device, stream) if positions is None else positions
+        slot_mapping = _new((num_tokens,), torch.int64, self.device, stream) if slot_mapping is None else slot_mapping
+        a = PaTablesArgs(B, num_tokens, stride, new_lens.data_ptr(), _ptr(keep_lens), context_lens.data_ptr(),
+                         block_tables.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), cu_q.data_ptr(),
+                         positions.data_ptr(), slot_mapping.data_ptr())
+        _check(_sparse_lib().pa_step_tables(self.handle, a, _stream_on(stream, self.device)), "pa_step_tables")
+        return cu_q, positions, slot_mapping
+
+    def bounds_size(self) -> int:
+        """Bytes of the bounds of one cache of this pool's geometry (pa_key_bounds_size)."""
+        n = C.c_uint64()
+        _check(_sparse_lib().pa_key_bounds_size(self.handle, n), "pa_key_bounds_size")
+        return n.value
+
+    def new_bounds(self) -> torch.Tensor:
+        """A bounds buffer for one cache (uint8, zeros: every block scores 0 until key_bounds has seen it)."""
+        return torch.zeros(self.bounds_size(), dtype=torch.uint8, device=self.device)
+
+    def _bounds(self, bounds: torch.Tensor) -> torch.Tensor:
+        nb, hkv, _, d = self.geometry
+        _need(bounds, "bounds", torch.uint8, self.device.index, (nb * hkv * (2 * d + 4),))
+        return bounds
+
+    def key_bounds(self, bounds: torch.Tensor, cu_q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                   num_tokens: int, k_cache: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Bounds of the keys of every block that holds one of the newest tokens (pa_key_bounds): sequence b's are
+        the cu_q[b + 1] - cu_q[b] tokens up to context_lens[b], num_tokens at most in all. Changes and returns bounds."""
+        index = self.device.index
+        if cu_q.dim() != 1 or cu_q.shape[0] < 1 or block_tables.dim() != 2 or context_lens.dim() != 1:
+            raise ValueError(f"cu_q must be [B + 1], block_tables [>= B, stride], context_lens [>= B]: got "
+                             f"{tuple(cu_q.shape)}, {tuple(block_tables.shape)}, {tuple(context_lens.shape)}")
+        B, (rows, stride), lens = cu_q.shape[0] - 1, block_tables.shape, context_lens.shape[0]
+        if rows < B or lens < B:
+            raise ValueError(f"block_tables and context_lens must hold {B} sequences, got {rows} and {lens}")
+        self._bounds(bounds)
+        _need(cu_q, "cu_q", torch.int32, index, (B + 1,))
+        _need(block_tables, "block_tables", torch.int32, index, (rows, stride))
+        _need(context_lens, "context_lens", torch.int32, index, (lens,))
+        if k_cache is not None:
+            _need(k_cache, "k_cache", self.k_cache.dtype, index, self.k_cache.shape)
+        _check(_sparse_lib().pa_key_bounds(self.handle, _ptr(k_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
+                                           context_lens.data_ptr(), int(num_tokens), B, bounds.data_ptr(),
+                                           _stream_on(stream, self.device)), "pa_key_bounds")
+        return bounds
+
+    def _rows(self, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor) -> int:
+        """Checks q [B, q_len, Hq, d] and what goes with it; returns the tables' stride."""
+        index, d = self.device.index, self.geometry[3]
+        if q.dim() != 4 or block_tables.dim() != 2 or context_lens.dim() != 1:
+            raise ValueError(f"q must be [B, q_len, Hq, {d}], block_tables [>= B, stride], context_lens [>= B]: got "
+                             f"{tuple(q.shape)}, {tuple(block_tables.shape)}, {tuple(context_lens.shape)}")
+        B, (rows, stride), lens = q.shape[0], block_tables.shape, context_lens.shape[0]
+        if rows < B or lens < B:
+            raise ValueError(f"block_tables and context_lens must hold {B} sequences, got {rows} and {lens}")
+        _need(q, "q", self.dtype, index, (B, q.shape[1], q.shape[2], d))
+        _need(block_tables, "block_tables", torch.int32, index, (rows, stride))
+        _need(context_lens, "context_lens", torch.int32, index, (lens,))
+        return stride
+
+    def select_blocks(self, q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      budget: int, num_first: int = 1, num_last: int = 2, out: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """The budget best blocks for each sequence and KV head of q [B, q_len, Hq, d] by the bounds' scores
+        (pa_select_blocks), the first num_first and the last num_last always among them: int32 [B, Hkv, budget],
+        ascending, -1 behind the last."""
+        stride, budget = self._rows(q, block_tables, context_lens), int(budget)
+        self._bounds(bounds)
+        B, q_len, Hq, _ = q.shape
+        shape = (B, self.geometry[1], budget)
+        if out is None:
+            out = _new((B, shape[1], max(budget, 0)), torch.int32, self.device, stream)
+        else:
+            _need(out, "out", torch.int32, self.device.index, shape)
+        _check(_sparse_lib().pa_select_blocks(
+            self.handle, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), stride, context_lens.data_ptr(), B, Hq,
+            q_len, budget, int(num_first), int(num_last), out.data_ptr(), _stream_on(stream, self.device)), "pa_select_blocks")
+        return out
+
+    def decode_selected(self, q: torch.Tensor, selected: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                        k_cache: Optional[torch.Tensor] = None, v_cache: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """decode over the listed blocks only (pa_decode_selected): selected int32 [B, Hkv, budget] names blocks of
+        each sequence by their place in its table, negative entries are skipped."""
+        stride = self._rows(q, block_tables, context_lens)
+        if selected.dim() != 3:
+            raise ValueError(f"selected must be [B, Hkv, budget], got {tuple(selected.shape)}")
+        B, q_len, Hq, _ = q.shape
+        budget = selected.shape[2]
+        _need(selected, "selected", torch.int32, self.device.index, (B, self.geometry[1], budget))
+        if out is None:
+            out = _new(q.shape, self.dtype, self.device, stream)
+        else:
+            _need(out, "out", self.dtype, self.device.index, q.shape)
+        if (k_cache is None) != (v_cache is None):
+            raise ValueError("pass both k_cache and v_cache, or neither")
+        if k_cache is not None:
+            _need(k_cache, "k_cache", self.k_cache.dtype, self.device.index, self.k_cache.shape)
+            _need(v_cache, "v_cache", self.v_cache.dtype, self.device.index, self.v_cache.shape)
+        _check(_sparse_lib().pa_decode_selected(
+            self.handle, q.data_ptr(), _ptr(k_cache), _ptr(v_cache), selected.data_ptr(), budget, block_tables.data_ptr(),
+            stride, context_lens.data_ptr(), B, Hq, q_len, float(scale), out.data_ptr(), _stream_on(stream, self.device)),
+            "pa_decode_selected")
+        return out
 
     def launches(self, block_table_stride: int, num_seqs: int, num_q_heads: int, q_len: int) -> int:
         return lib().pa_decode_launches(self.handle, block_table_stride, num_seqs, num_q_heads, q_len)
