@@ -243,10 +243,13 @@ cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, in
 
 constexpr int SEL_WARPS = 8;
 constexpr int SEL_THREADS = SEL_WARPS * 32;
+constexpr int SEL_BINS = 256;
+static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
+constexpr int SEL_MAX_RANKS = 16;
 
 __host__ __device__ constexpr int sel_q_stride(int D) { return 4 * D + 8; }   // bytes of a row [c+, c-] in fp16, and a pad
 __host__ __device__ constexpr size_t sel_smem(int D, int NT, int chunk) {
-    return (size_t)NT * 8 * (sel_q_stride(D) + 8) + (4 * 256 + 2 + SEL_WARPS * 2) * 4 + (size_t)chunk * 4;
+    return (size_t)NT * 8 * (sel_q_stride(D) + 8) + (4 * SEL_BINS + 4 + SEL_WARPS * 4) * 4 + (size_t)chunk * 4;
 }
 
 // Whole numbers of four bytes as two pairs of fp16: the byte plus 128, under the exponent of 1024, less 1152.
@@ -269,8 +272,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // Scores: 16 blocks per warp and step, the rows of an m16n8k16 product whose columns are 8 query rows; the codes go from
 // global memory to the fragments without shared memory, 16 bytes per lane: a lane's 4 bytes are its four values of one
 // 16-deep step, so the contraction's order is the bytes' own, and the query rows are laid out to match.
-// Then the budget-th largest key, by its four bytes from the top (histograms in shared memory, summed over the cluster),
-// and the indices of the keys above it and of the first ones equal to it, in order.
+//
+// Then the threshold, the least key that is taken beside the blocks that always are: digits of 8 bits, from the highest
+// bit in which the keys differ, by histograms that every CTA sums over the cluster for itself; it ends where a bin is
+// taken whole, after two digits as a rule, after all of them only among equal scores. What the CTAs before this one hold
+// above and at the threshold comes out of the same histograms, so the indices are written in order without another round.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams p) {
     constexpr int RP = NT * 8, LOADS = D / 32;         // 64-byte pieces of [hi, lo]
@@ -279,9 +285,10 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
     uint8_t *qsm = ssm;                                // [RP][QS]
     float *qmul = reinterpret_cast<float *>(qsm + RP * QS), *qadd = qmul + RP;   // a row's step; 0, or -inf: does not count
     int *hist = reinterpret_cast<int *>(qadd + RP);    // [4][256]
-    int *counts = hist + 4 * 256;                      // keys above and equal to the threshold
-    int *wcount = counts + 2;                          // [warps][2]
-    uint32_t *keys = reinterpret_cast<uint32_t *>(wcount + SEL_WARPS * 2);
+    uint32_t *ends = reinterpret_cast<uint32_t *>(hist + 4 * SEL_BINS);   // least and largest key, of the CTA
+    int *digit = reinterpret_cast<int *>(ends + 2);    // the digit, what is needed of its bin
+    int *wtot = digit + 2;                             // [warps] sums; [warps][3] counts
+    uint32_t *keys = reinterpret_cast<uint32_t *>(wtot + SEL_WARPS * 4);   // the block ids, then the keys in their place
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int unit = (int)(blockIdx.x / ranks), g = unit % p.Hkv, b = unit / p.Hkv;
@@ -299,6 +306,12 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
         for (int i = rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) out[i] = i < n ? i : -1;
         return;
     }
+    // blocks of this CTA, shared out evenly in tiles of 16; those of [lo, hi) are chosen by score, the others always
+    const int per = ((n + 15) / 16 + ranks - 1) / ranks * 16;
+    const int i0 = rank * per, mine = max(0, min(per, n - i0));
+    const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
+    const int32_t *trow = p.block_tables + b * p.stride + i0;
+    for (int i = tid; i < mine; i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i);
 
     // ---- query rows
     for (int r = warp; r < RP; r += SEL_WARPS) {
@@ -327,13 +340,13 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
         }
         if (lane == 0) qmul[r] = step, qadd[r] = counts_row ? 0.f : -INFINITY;
     }
-    for (int i = tid; i < 4 * 256; i += SEL_THREADS) hist[i] = 0;
+    for (int i = tid; i < 4 * SEL_BINS; i += SEL_THREADS) hist[i] = 0;
+    if (tid == 0) ends[0] = 0xFFFFFFFFu, ends[1] = 0u;
     __syncthreads();
 
     // ---- scores
-    const int i0 = rank * p.chunk, mine = max(0, min(p.chunk, n - i0));
     const int gq = lane >> 2, tq = lane & 3;
-    const int32_t *trow = p.block_tables + b * p.stride;
+    uint32_t least = 0xFFFFFFFFu, most = 0u;
     float mul[NT][2], add[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -345,7 +358,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = t + gq + 8 * e;
-            id[e] = i < mine ? __ldg(trow + i0 + i) : 0;
+            id[e] = i < mine ? (int)keys[i] : 0;
             ok[e] = id[e] >= 0 && id[e] < p.num_blocks;
             if (!ok[e]) {
                 set_status(p.status, STATUS_BOUNDS);
@@ -393,95 +406,121 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
         for (int e = 0; e < 2; ++e) {
             best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 1));
             best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 2));
-            const int i = t + gq + 8 * e, at = i0 + i;
+            const int i = t + gq + 8 * e;
             // a zero's sign must not order blocks; a step that is no number wants its block
             const float score = step[e] == INFINITY ? INFINITY : step[e] == 0.f ? 0.f : __fadd_rn(__fmul_rn(best[e], step[e]), 0.f);
-            if (tq == e && i < mine)
-                keys[i] = at < p.num_first || at >= n - p.num_last ? 0xFFFFFFFFu : ok[e] ? ordered(score) : 0u;
+            if (tq == e && i >= lo && i < hi) {
+                const uint32_t key = ok[e] ? ordered(score) : 0u;
+                keys[i] = key;
+                least = min(least, key), most = max(most, key);
+            }
         }
     }
-    __syncthreads();
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMin(ends, least), atomicMax(ends + 1, most);
 
-    // ---- the budget-th largest key
-    uint32_t prefix = 0, mask = 0;
-    int need = p.budget;
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        int *h = hist + pass * 256;
-        for (int i = tid; i < mine; i += SEL_THREADS)
-            if ((keys[i] & mask) == prefix) atomicAdd(h + ((keys[i] >> shift) & 255), 1);
-        cluster_sync();
-        // warp 0: lane l sums bins 8 (31 - l) .. + 7, from the top
-        if (warp == 0) {
-            int bin[8], sum = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) bin[k] = 0;
+    // ---- the threshold: a key is taken if its digits so far are above `prefix`, or equal and among the first `need` of those
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    least = ends[0], most = ends[1];
+    if (ranks > 1) {
+        const uint32_t a = smem_u32(ends);
+        for (int r = 0; r < ranks; ++r) {
+            least = min(least, (uint32_t)ld_cluster_int(map_rank(a, r)));
+            most = max(most, (uint32_t)ld_cluster_int(map_rank(a + 4, r)));
+        }
+    }
+    int need = p.budget - (p.num_first + p.num_last);
+    // what the CTAs before this one hold: above the threshold (the first blocks and, as the last CTA may, the last ones),
+    // and at it
+    int gt_before = min(i0, p.num_first) + max(0, min(i0, n) - (n - p.num_last)), eq_before = 0;
+    int bits = 32 - __clz(least ^ most);               // bits in which the keys differ
+    uint32_t mask = bits == 32 ? 0u : 0xFFFFFFFFu << bits, prefix = most & mask;
+    if (need == 0) mask = prefix = 0xFFFFFFFFu, bits = 0;   // above every key
+    else if (bits == 0) eq_before = max(0, min(i0, n - p.num_last) - p.num_first);   // equal keys
+    for (int pass = 0; bits > 0; ++pass) {
+        const int shift = max(0, bits - 8);
+        const uint32_t digits = (1u << (bits - shift)) - 1u;
+        int *h = hist + pass * SEL_BINS;
+        for (int i = lo + tid; i < hi; i += SEL_THREADS) {
+            const uint32_t key = keys[i];
+            if ((key & mask) == prefix) atomicAdd(h + ((key >> shift) & digits), 1);
+        }
+        const int bin = SEL_BINS - 1 - tid;            // this thread's, from the top
+        int sum = 0, before = 0;
+        if (ranks > 1) {
+            cluster_sync();
+            const uint32_t src = smem_u32(h + bin);
+#pragma unroll 4
             for (int r = 0; r < ranks; ++r) {
-                const uint32_t src = map_rank(smem_u32(h + 8 * (31 - lane)), r);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) bin[k] += ld_cluster_int(src + 4 * k);
+                const int v = ld_cluster_int(map_rank(src, r));
+                sum += v;
+                before += r < rank ? v : 0;
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += bin[k];
-            int above = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, above, d);
-                if (lane >= d) above += u;
-            }
-            above -= sum;
-            if (above < need && above + sum >= need) {
-                int k = 7;
-                while (above + bin[k] < need) above += bin[k--];
-                wcount[0] = 8 * (31 - lane) + k;
-                wcount[1] = need - above;
-            }
+        } else {
+            __syncthreads();
+            sum = h[bin];
         }
+        int above = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, above, d);
+            if (lane >= d) above += u;
+        }
+        if (lane == 31) wtot[warp] = above;
+        above -= sum;
         __syncthreads();
-        prefix |= (uint32_t)wcount[0] << shift;
-        mask |= 0xFFu << shift;
-        need = wcount[1];
+        for (int w = 0; w < warp; ++w) above += wtot[w];
+        if (above < need && above + sum >= need) digit[0] = bin, digit[1] = need - above;
         __syncthreads();
+        const int d = digit[0];
+        // the bin's size, and what lies before this CTA in the bins above and in this one
+        int *cnt = wtot + SEL_WARPS;                   // [warps][3]
+        const int up = __reduce_add_sync(0xffffffffu, bin > d ? before : 0);
+        const int at = __reduce_add_sync(0xffffffffu, bin == d ? before : 0);
+        const int size = __reduce_add_sync(0xffffffffu, bin == d ? sum : 0);
+        if (lane == 0) cnt[3 * warp] = up, cnt[3 * warp + 1] = at, cnt[3 * warp + 2] = size;
+        need = digit[1];
+        __syncthreads();
+        int bin_size = 0;
+        eq_before = 0;
+#pragma unroll
+        for (int w = 0; w < SEL_WARPS; ++w) gt_before += cnt[3 * w], eq_before += cnt[3 * w + 1], bin_size += cnt[3 * w + 2];
+        prefix |= (uint32_t)d << shift;
+        mask = shift == 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << shift;
+        bits = bin_size == need ? 0 : shift;           // a bin that is taken whole ends it
     }
+    if (ranks > 1) cluster_arrive();                   // this CTA reads no other one's memory any more
 
-    // ---- the keys above the threshold, and the first `need` equal to it
-    if (tid == 0) counts[0] = counts[1] = 0;
-    __syncthreads();
+    // ---- the indices, in order: a stretch of blocks per warp, counted and then written
+    const int stretch = (mine + SEL_THREADS - 1) / SEL_THREADS * 32, s0 = min(mine, warp * stretch), s1 = min(mine, s0 + stretch);
+    const auto taken = [&](int i, bool &is_gt, bool &is_eq) {
+        const uint32_t key = i < s1 ? keys[i] & mask : 0u;
+        const bool scored = i >= lo && i < hi;
+        is_gt = i < s1 && (!scored || key > prefix);
+        is_eq = i < s1 && scored && key == prefix;
+    };
+    __syncthreads();                                   // the sums' words are free
     int gt = 0, eq = 0;
-    for (int i = tid; i < mine; i += SEL_THREADS) gt += keys[i] > prefix, eq += keys[i] == prefix;
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        if (gt) atomicAdd(counts, gt);
-        if (eq) atomicAdd(counts + 1, eq);
+    for (int i = s0 + lane; i < s0 + stretch; i += 32) {
+        bool a, e;
+        taken(i, a, e);
+        gt += __popc(__ballot_sync(0xffffffffu, a)), eq += __popc(__ballot_sync(0xffffffffu, e));
     }
-    cluster_sync();
-    int gts = 0, eqs = 0;                              // before this CTA's blocks, then before this round's
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t src = map_rank(smem_u32(counts), r);
-        gts += ld_cluster_int(src);
-        eqs += ld_cluster_int(src + 4);
+    if (lane == 0) wtot[2 * warp] = gt, wtot[2 * warp + 1] = eq;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) gt_before += wtot[2 * w], eq_before += wtot[2 * w + 1];
+    for (int i = s0 + lane; i < s0 + stretch; i += 32) {
+        bool a, e;
+        taken(i, a, e);
+        const uint32_t ma = __ballot_sync(0xffffffffu, a), me = __ballot_sync(0xffffffffu, e), below = (1u << lane) - 1u;
+        const int ga = gt_before + __popc(ma & below), ee = eq_before + __popc(me & below);
+        if (a || (e && ee < need)) out[ga + min(ee, need)] = i0 + i;
+        gt_before += __popc(ma);
+        eq_before += __popc(me);
     }
-    cluster_arrive();                                  // this CTA reads no other one's memory any more
-    for (int base = 0; base < mine; base += SEL_THREADS) {
-        const int i = base + tid;
-        const uint32_t key = i < mine ? keys[i] : 0u;
-        const bool is_gt = i < mine && key > prefix, is_eq = i < mine && key == prefix;
-        const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
-        if (lane == 0) wcount[2 * warp] = __popc(mg), wcount[2 * warp + 1] = __popc(me);
-        __syncthreads();
-        int g0 = gts, e0 = eqs;
-        for (int w = 0; w < SEL_WARPS; ++w) {
-            if (w < warp) g0 += wcount[2 * w], e0 += wcount[2 * w + 1];
-            gts += wcount[2 * w], eqs += wcount[2 * w + 1];
-        }
-        const uint32_t below = (1u << lane) - 1u;
-        g0 += __popc(mg & below);
-        e0 += __popc(me & below);
-        if (is_gt || (is_eq && e0 < need)) out[g0 + min(e0, need)] = i0 + i;
-        __syncthreads();
-    }
-    cluster_wait();
+    if (ranks > 1) cluster_wait();
 }
 
 template <typename T, int D>
@@ -490,11 +529,12 @@ static cudaError_t launch_select_t(SelectParams p, int sm_count, cudaStream_t st
     const int64_t units = (int64_t)p.num_seqs * p.Hkv;
     // CTAs of a cluster: enough for two on each SM, each with a tile for every warp
     int ranks = 1;
-    while (ranks < 8 && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * 2048)) ranks *= 2;
+    while (ranks < SEL_MAX_RANKS && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * 1024)) ranks *= 2;
     p.chunk = (tiles + ranks - 1) / ranks * 16;
     const auto launch = [&](auto kernel, int nt) {
         const size_t smem = sel_smem(D, nt, p.chunk);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return e != cudaSuccess ? e : launch_clusters(kernel, (unsigned)(units * ranks), SEL_THREADS, smem, ranks, stream, p);
     };
     switch ((p.rows + 7) / 8) {

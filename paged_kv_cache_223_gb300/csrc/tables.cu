@@ -139,21 +139,42 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
         if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
         p.block_tables[b * p.stride + j] = id;
     }
-    for (int i = gid; i < p.num_tokens; i += all) {
-        int pos = 0;
-        int64_t slot = -1;
-        if (i < tokens) {
-            const int b = owner(cu, B, i);
-            pos = kept[b] + i - cu[b];
-            const int have = (kept[b] + bs - 1) >> p.bs_shift, j = pos >> p.bs_shift;
-            // a block that this call takes is read where it comes from, not from the table that it is written to
-            const int id = j < have ? __ldcg(p.block_tables + b * p.stride + j)
-                                    : __ldcg(p.free_blocks + top - (taken[b] + j - have));
-            if (id >= 0 && id < p.num_blocks) slot = ((int64_t)id << p.bs_shift) + (pos & (bs - 1));
-            else set_status(p.status, STATUS_BOUNDS);
+    // four tokens at a time: they share the search and, as a rule, the block
+    for (int i4 = gid; i4 < (p.num_tokens + 3) / 4; i4 += all) {
+        int pos[4];
+        long long slot[4];
+        int b = 4 * i4 < tokens ? owner(cu, B, 4 * i4) : B, was = -1, id = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 4 * i4 + e;
+            pos[e] = 0;
+            slot[e] = -1;
+            if (i >= tokens) continue;
+            while (cu[b + 1] <= i) ++b, was = -1;
+            pos[e] = kept[b] + i - cu[b];
+            const int j = pos[e] >> p.bs_shift;
+            if (j != was) {
+                // a block that this call takes is read where it comes from, not from the table that it is written to
+                const int have = (kept[b] + bs - 1) >> p.bs_shift;
+                id = j < have ? __ldcg(p.block_tables + b * p.stride + j)
+                              : __ldcg(p.free_blocks + top - (taken[b] + j - have));
+                was = j;
+                if (id < 0 || id >= p.num_blocks) {
+                    set_status(p.status, STATUS_BOUNDS);
+                    id = -1;
+                }
+            }
+            if (id >= 0) slot[e] = ((long long)id << p.bs_shift) + (pos[e] & (bs - 1));
         }
-        p.positions[i] = pos;
-        p.slots[i] = slot;
+        if (p.vectors && 4 * i4 + 4 <= p.num_tokens) {
+            reinterpret_cast<int4 *>(p.positions)[i4] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            reinterpret_cast<longlong2 *>(p.slots)[2 * i4] = make_longlong2(slot[0], slot[1]);
+            reinterpret_cast<longlong2 *>(p.slots)[2 * i4 + 1] = make_longlong2(slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * i4 + e < p.num_tokens) p.positions[4 * i4 + e] = pos[e], p.slots[4 * i4 + e] = slot[e];
+        }
     }
     for (int b = gid; b <= B; b += all) {
         p.cu_q[b] = cu[b];
@@ -162,12 +183,16 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     if (gid == 0) *p.num_free = n_free + F - T;
 }
 
-cudaError_t launch_tables(const TablesParams &p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_tables(TablesParams p, cudaStream_t stream) {
     const size_t smem = (size_t)(4 * p.num_seqs + 3) * sizeof(int);
-    const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    const int cluster = 1;
-    return launch_clusters(tables_kernel, cluster, TAB_THREADS, smem, cluster, stream, p);
+    p.vectors = (reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
+    // CTAs of the cluster: one for each two rounds of four tokens per thread
+    int ranks = 1;
+    while (ranks < 16 && p.num_tokens > ranks * TAB_THREADS * 8) ranks *= 2;
+    return launch_clusters(tables_kernel, ranks, TAB_THREADS, smem, ranks, stream, p);
 }
 
 }  // namespace pa
