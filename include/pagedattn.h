@@ -366,7 +366,7 @@ pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
  *   block_tables   device int32 [num_seqs, block_table_stride]
  *   context_lens   device int32 [num_seqs], at most stride * bs and 2^29
  *   num_seqs       0 .. PA_TABLES_MAX_SEQS
- *   bounds         device, 16-byte aligned, pa_key_bounds_size() bytes
+ *   bounds         device, 32-byte aligned, pa_key_bounds_size() bytes
  * Lengths and block ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at
  * pa_pool_check), the sequence or block is skipped. Two sequences that name one
  * block with different fillings: whose bounds land is unspecified.

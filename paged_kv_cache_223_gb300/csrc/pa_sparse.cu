@@ -110,7 +110,7 @@ pa_status pa_key_bounds(pa_pool *pool, const void *k_cache, const int32_t *cu_q,
     if (num_tokens == 0 || num_seqs == 0) return PA_OK;
     const pa_pool_config &c = pool->cfg;
     if (!k_cache) k_cache = pool->k_cache;
-    if (!cu_q || !block_tables || !context_lens || !bounds || !aligned16(k_cache) || !aligned16(bounds) ||
+    if (!cu_q || !block_tables || !context_lens || !bounds || !aligned16(k_cache) || !aligned(bounds, 32) ||
         !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PA_ERR_INVALID_ARG;
     const Span out = {bounds, bounds_bytes(c)};
@@ -153,7 +153,7 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
     if (num_last < (q_len - 2 + c.block_size) / c.block_size + 1 || (int64_t)num_first + num_last > budget)
         return PA_ERR_INVALID_ARG;
     if (num_seqs == 0) return PA_OK;
-    if (!q || !bounds || !block_tables || !context_lens || !selected || !aligned16(q) || !aligned16(bounds) ||
+    if (!q || !bounds || !block_tables || !context_lens || !selected || !aligned16(q) || !aligned(bounds, 32) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(selected, 4))
         return PA_ERR_INVALID_ARG;
     const uint64_t n = num_seqs;

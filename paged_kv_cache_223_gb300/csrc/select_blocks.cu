@@ -243,13 +243,23 @@ cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, in
 
 constexpr int SEL_WARPS = 8;
 constexpr int SEL_THREADS = SEL_WARPS * 32;
+constexpr int SEL_CTAS = 4;                           // per SM
 constexpr int SEL_BINS = 256;
 static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
 constexpr int SEL_MAX_RANKS = 16;
 
-__host__ __device__ constexpr int sel_q_stride(int D) { return 4 * D + 8; }   // bytes of a row [c+, c-] in fp16, and a pad
+__host__ __device__ constexpr int sel_q_stride(int D) { return 4 * D + 32; }   // bytes of a row [c+, c-] in fp16, and a pad
+// Where value i of a row lies: the four values of each of a quad's lanes in one step side by side.
+__device__ __forceinline__ int sel_q_at(int i) { return (((i >> 7) * 8 + ((i & 31) >> 2)) * 4 + ((i >> 5) & 3)) * 4 + (i & 3); }
 __host__ __device__ constexpr size_t sel_smem(int D, int NT, int chunk) {
     return (size_t)NT * 8 * (sel_q_stride(D) + 8) + (4 * SEL_BINS + 4 + SEL_WARPS * 4) * 4 + (size_t)chunk * 4;
+}
+
+// 32 bytes that no other CTA of this call reads (the bounds of a step are larger than what L2 could keep for the next).
+__device__ __forceinline__ void ldg256(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.nc.L1::evict_first.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
 }
 
 // Whole numbers of four bytes as two pairs of fp16: the byte plus 128, under the exponent of 1024, less 1152.
@@ -270,7 +280,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 
 // One cluster per (sequence, KV head); its CTAs hold the keys (ordered scores) of `chunk` blocks each in shared memory.
 // Scores: 16 blocks per warp and step, the rows of an m16n8k16 product whose columns are 8 query rows; the codes go from
-// global memory to the fragments without shared memory, 16 bytes per lane: a lane's 4 bytes are its four values of one
+// global memory to the fragments without shared memory, 32 bytes per lane: a lane's 4 bytes are its four values of one
 // 16-deep step, so the contraction's order is the bytes' own, and the query rows are laid out to match.
 //
 // Then the threshold, the least key that is taken beside the blocks that always are: digits of 8 bits, from the highest
@@ -278,8 +288,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // taken whole, after two digits as a rule, after all of them only among equal scores. What the CTAs before this one hold
 // above and at the threshold comes out of the same histograms, so the indices are written in order without another round.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams p) {
-    constexpr int RP = NT * 8, LOADS = D / 32;         // 64-byte pieces of [hi, lo]
+__global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const SelectParams p) {
+    constexpr int RP = NT * 8, LOADS = D / 64;         // 128-byte pieces of [hi, lo]
     constexpr int QS = sel_q_stride(D);
     extern __shared__ __align__(16) uint8_t ssm[];
     uint8_t *qsm = ssm;                                // [RP][QS]
@@ -296,22 +306,10 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
     pdl_wait();
 
     int len = __ldg(p.context_lens + b);
-    if (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)) {
-        if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
-        len = len < 0 ? 0 : min(len, p.max_len);
-    }
-    const int n = (len + p.bs - 1) / p.bs;
-    int32_t *out = p.selected + (int64_t)unit * p.budget;
-    if (n <= p.budget) {                               // all of them (the same in every CTA of the cluster)
-        for (int i = rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) out[i] = i < n ? i : -1;
-        return;
-    }
-    // blocks of this CTA, shared out evenly in tiles of 16; those of [lo, hi) are chosen by score, the others always
-    const int per = ((n + 15) / 16 + ranks - 1) / ranks * 16;
-    const int i0 = rank * per, mine = max(0, min(per, n - i0));
-    const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
-    const int32_t *trow = p.block_tables + b * p.stride + i0;
-    for (int i = tid; i < mine; i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i);
+    // one CTA to a unit holds its blocks whatever the length is: their ids are on their way before it is known
+    const int32_t *trow = p.block_tables + b * p.stride;
+    if (ranks == 1)
+        for (int i = tid; i < min(p.chunk, (int)p.stride); i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i);
 
     // ---- query rows
     for (int r = warp; r < RP; r += SEL_WARPS) {
@@ -335,11 +333,27 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
 #pragma unroll
         for (int e = 0; e < PL; ++e) {
             const int c = counts_row ? code_of(x[e], step, inv) : 0;
-            row[lane * PL + e] = __int2half_rn(max(c, 0));
-            row[D + lane * PL + e] = __int2half_rn(min(c, 0));
+            row[sel_q_at(lane * PL + e)] = __int2half_rn(max(c, 0));
+            row[sel_q_at(D + lane * PL + e)] = __int2half_rn(min(c, 0));
         }
         if (lane == 0) qmul[r] = step, qadd[r] = counts_row ? 0.f : -INFINITY;
     }
+    if (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)) {
+        if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
+        len = len < 0 ? 0 : min(len, p.max_len);
+    }
+    const int n = (len + p.bs - 1) / p.bs;
+    int32_t *out = p.selected + (int64_t)unit * p.budget;
+    if (n <= p.budget) {                               // all of them (the same in every CTA of the cluster)
+        for (int i = rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) out[i] = i < n ? i : -1;
+        return;
+    }
+    // blocks of this CTA, shared out evenly in tiles of 16; those of [lo, hi) are chosen by score, the others always
+    const int per = ((n + 15) / 16 + ranks - 1) / ranks * 16;
+    const int i0 = rank * per, mine = max(0, min(per, n - i0));
+    const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
+    if (ranks > 1)
+        for (int i = tid; i < mine; i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i0 + i);
     for (int i = tid; i < 4 * SEL_BINS; i += SEL_THREADS) hist[i] = 0;
     if (tid == 0) ends[0] = 0xFFFFFFFFu, ends[1] = 0u;
     __syncthreads();
@@ -365,14 +379,14 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
                 id[e] = 0;
             }
         }
-        uint4 w[2][LOADS];
+        uint32_t w[2][LOADS][8];
         float step[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t u = (int64_t)id[e] * p.Hkv + g;
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + u * 2 * D) + tq;
+            const int8_t *src = p.codes + u * 2 * D + 32 * tq;
 #pragma unroll
-            for (int l = 0; l < LOADS; ++l) w[e][l] = __ldg(src + 4 * l);
+            for (int l = 0; l < LOADS; ++l) ldg256(src + 128 * l, w[e][l]);
             step[e] = __ldg(p.steps + u);
         }
         float acc[NT][4];
@@ -380,16 +394,14 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
         for (int l = 0; l < LOADS; ++l) {
-            const uint32_t x[4] = {w[0][l].x, w[0][l].y, w[0][l].z, w[0][l].w};
-            const uint32_t y[4] = {w[1][l].x, w[1][l].y, w[1][l].z, w[1][l].w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 uint32_t a0, a1, a2, a3;
-                bytes_to_f16(x[c], a0, a2);
-                bytes_to_f16(y[c], a1, a3);
+                bytes_to_f16(w[0][l][c], a0, a2);
+                bytes_to_f16(w[1][l][c], a1, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(qsm + (nt * 8 + gq) * QS + (64 * l + 16 * tq + 4 * c) * 2);
+                    const uint2 q = *reinterpret_cast<const uint2 *>(qsm + (nt * 8 + gq) * QS + (8 * l + c) * 32 + tq * 8);
                     mma_16816<__half>(acc[nt], a0, a1, a2, a3, q.x, q.y);
                 }
             }
@@ -423,14 +435,9 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
     // ---- the threshold: a key is taken if its digits so far are above `prefix`, or equal and among the first `need` of those
     if (ranks > 1) cluster_sync();
     else __syncthreads();
-    least = ends[0], most = ends[1];
-    if (ranks > 1) {
-        const uint32_t a = smem_u32(ends);
-        for (int r = 0; r < ranks; ++r) {
-            least = min(least, (uint32_t)ld_cluster_int(map_rank(a, r)));
-            most = max(most, (uint32_t)ld_cluster_int(map_rank(a + 4, r)));
-        }
-    }
+    const uint32_t ends_at = map_rank(smem_u32(ends), lane < ranks ? lane : 0);   // one CTA's per lane
+    least = __reduce_min_sync(0xffffffffu, (uint32_t)ld_cluster_int(ends_at));
+    most = __reduce_max_sync(0xffffffffu, (uint32_t)ld_cluster_int(ends_at + 4));
     int need = p.budget - (p.num_first + p.num_last);
     // what the CTAs before this one hold: above the threshold (the first blocks and, as the last CTA may, the last ones),
     // and at it
@@ -452,12 +459,11 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectParams 
         if (ranks > 1) {
             cluster_sync();
             const uint32_t src = smem_u32(h + bin);
-#pragma unroll 4
-            for (int r = 0; r < ranks; ++r) {
-                const int v = ld_cluster_int(map_rank(src, r));
-                sum += v;
-                before += r < rank ? v : 0;
-            }
+            int v[SEL_MAX_RANKS];                      // all on their way before the first is added
+#pragma unroll
+            for (int r = 0; r < SEL_MAX_RANKS; ++r) v[r] = r < ranks ? ld_cluster_int(map_rank(src, r)) : 0;
+#pragma unroll
+            for (int r = 0; r < SEL_MAX_RANKS; ++r) sum += v[r], before += r < rank ? v[r] : 0;
         } else {
             __syncthreads();
             sum = h[bin];
