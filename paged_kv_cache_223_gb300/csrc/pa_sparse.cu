@@ -93,7 +93,7 @@ pa_status pa_step_tables(pa_pool *pool, const pa_tables_args *a, void *stream) {
     p.status = pool->status;
     DeviceGuard g(c.device);
     if (!g.ok) return PA_ERR_CUDA;
-    return launched(launch_tables(p, static_cast<cudaStream_t>(stream)));
+    return launched(launch_tables(p, pool->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes) {

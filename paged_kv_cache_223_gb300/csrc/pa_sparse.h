@@ -22,6 +22,7 @@ struct TablesParams {
     int num_blocks;
     int max_len;                // longest context the tables hold
     bool vectors;               // positions and slots lie on 16-byte boundaries
+    bool tokens_apart;          // positions and slots are written by a kernel behind the one that makes the tables
     int *status;
 };
 
@@ -71,7 +72,7 @@ struct SelectedParams {
     int *status;
 };
 
-cudaError_t launch_tables(TablesParams p, cudaStream_t stream);
+cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream);
 cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, int sm_count, cudaStream_t stream);
 cudaError_t launch_select(SelectParams p, int dtype, int head_dim, int sm_count, cudaStream_t stream);
 cudaError_t launch_selected(SelectedParams p, int dtype, int head_dim, const CUtensorMap &tmk, const CUtensorMap &tmv,

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = ATT_WARPS * 32;
+constexpr int ATT_MAX_RANKS = 8;
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
 
 __host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
@@ -39,6 +40,14 @@ __host__ __device__ constexpr int att_join_bytes(int D, int nt) {
 }
 __host__ __device__ constexpr int att_body_bytes(int D, bool kv8, int nt) {
     return (att_ring_bytes(D, kv8, nt) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8, nt) : att_join_bytes(D, nt)) + 15 & ~15;
+}
+
+// Does a word of V hold a NaN or an infinity (E4M3 has NaN alone, all ones but for the sign)?
+template <typename T, bool KV8>
+__device__ __forceinline__ bool no_numbers(uint32_t x) {
+    if constexpr (KV8) return (__vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0;
+    constexpr uint32_t exp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    return (x & exp) == exp || ((x >> 16) & exp) == exp;
 }
 
 __device__ __forceinline__ float value16(uint16_t w, __half) { return __half2float(__ushort_as_half(w)); }
@@ -68,70 +77,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     const int gq = lane >> 2, tq = lane & 3;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int unit = (int)(blockIdx.x / ranks), g = unit % p.Hkv, b = unit / p.Hkv;
-    pdl_trigger();
-    pdl_wait();
-
-    int L = __ldg(p.context_lens + b);
-    if (L < 0 || L > p.max_len || (L > 0 && L < p.q_len)) {
-        if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
-        L = L < 0 ? 0 : min(L, p.max_len);
-    }
-
-    // ---- this warp's tiles: those of the listed blocks that hold tokens
-    int2 *list = lists + warp * p.warp_tiles;
-    int tiles = 0;
-    {
-        const int all = p.budget * (p.bs / TILE_TOKENS), step = ranks * W, blocks = (L + p.bs - 1) / p.bs;
-        for (int i0 = rank * W + warp; i0 < all; i0 += 32 * step) {
-            const int i = i0 + lane * step;
-            int row = 0, pos = -1;
-            if (i < all) {
-                const int tok = i * TILE_TOKENS, off = tok % p.bs;
-                const int j = __ldg(p.selected + (int64_t)unit * p.budget + tok / p.bs);
-                if (j >= blocks) set_status(p.status, STATUS_BOUNDS);
-                else if (j >= 0 && j * p.bs + off < L) {
-                    const int id = __ldg(p.block_tables + b * p.stride + j);
-                    if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
-                    else row = (id * p.Hkv + g) * p.bs + off, pos = j * p.bs + off;
-                }
-            }
-            const uint32_t have = __ballot_sync(0xffffffffu, pos >= 0);
-            if (pos >= 0) list[tiles + __popc(have & ((1u << lane) - 1u))] = make_int2(row, pos);
-            tiles += __popc(have);
-        }
-    }
     if (lane == 0) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
         for (int s = 0; s < STAGES; ++s) mbar_init(bars_u32 + (warp * STAGES + s) * 8, 1);
         fence_barrier_init();
     }
-    __syncwarp();
+    pdl_trigger();
+    pdl_wait();
 
-    const uint32_t ring_u32 = base_u32 + warp * STAGES * STAGE;
-    const uint32_t scales_u32 = base_u32 + W * STAGES * STAGE + warp * STAGES * 2 * TILE_TOKENS * 4;   // FP8 only
-    const uint64_t policy = l2_policy_evict_first();
-    auto issue = [&](int it) {
-        const int s = it % STAGES, row = list[it].x;
-        const uint32_t bar = bars_u32 + (warp * STAGES + s) * 8, dst = ring_u32 + s * STAGE;
-        fence_proxy_async_smem();
-        if constexpr (KV8) {
-            const uint32_t sdst = scales_u32 + s * 2 * TILE_TOKENS * 4;
-            mbar_arrive_expect_tx(bar, STAGE + 2 * TILE_TOKENS * 4);
-            tma_load_2d(dst, &tmk, 0, row, bar, policy);
-            tma_load_2d(dst + TILE, &tmv, 0, row, bar, policy);
-            bulk_load(sdst, p.k_scales + row, TILE_TOKENS * 4, bar, policy);
-            bulk_load(sdst + TILE_TOKENS * 4, p.v_scales + row, TILE_TOKENS * 4, bar, policy);
-        } else {
-            mbar_arrive_expect_tx(bar, STAGE);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                tma_load_2d(dst + h * SPAN, &tmk, h * 64, row, bar, policy);
-                tma_load_2d(dst + TILE + h * SPAN, &tmv, h * 64, row, bar, policy);
-            }
-        }
+    // the length, the first listed blocks and the query rows: on their way together
+    int L = __ldg(p.context_lens + b);
+    const int all = p.budget * (p.bs / TILE_TOKENS), step = ranks * W;
+    int j = -1, id = -1;
+    const auto look_up = [&](int i) {                  // the listed block of tile i and its id
+        j = i < all ? __ldg(p.selected + (int64_t)unit * p.budget + i * TILE_TOKENS / p.bs) : -1;
+        id = j >= 0 && j < p.stride ? __ldg(p.block_tables + b * p.stride + j) : -1;
     };
-    int issued = min(tiles, STAGES);
-    if (lane == 0)
-        for (int it = 0; it < issued; ++it) issue(it);
+    look_up(rank * W + warp + lane * step);
 
     // ---- query rows as the B operand. FP8 pools: a lane's four codes are consecutive dimensions, the contraction's order
     // is theirs, and a bf16 row is taken into fp16's range by a power of two that its scores get back.
@@ -154,7 +117,62 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) qf[nt][ks][0] = qf[nt][ks][1] = 0u;
         }
-        if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value) {
+    }
+    if (L < 0 || L > p.max_len || (L > 0 && L < p.q_len)) {
+        if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
+        L = L < 0 ? 0 : min(L, p.max_len);
+    }
+
+    // ---- this warp's tiles: those of the listed blocks that hold tokens
+    int2 *list = lists + warp * p.warp_tiles;
+    int tiles = 0;
+    {
+        const int blocks = (L + p.bs - 1) / p.bs;
+        for (int i0 = rank * W + warp; i0 < all; i0 += 32 * step) {
+            const int i = i0 + lane * step, off = i * TILE_TOKENS % p.bs;
+            if (i0 >= 32 * step) look_up(i);
+            int row = 0, pos = -1;
+            if (j >= blocks) set_status(p.status, STATUS_BOUNDS);
+            else if (j >= 0 && j * p.bs + off < L) {
+                if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
+                else row = (id * p.Hkv + g) * p.bs + off, pos = j * p.bs + off;
+            }
+            const uint32_t have = __ballot_sync(0xffffffffu, pos >= 0);
+            if (pos >= 0) list[tiles + __popc(have & ((1u << lane) - 1u))] = make_int2(row, pos);
+            tiles += __popc(have);
+        }
+    }
+    __syncwarp();
+
+    const uint32_t ring_u32 = base_u32 + warp * STAGES * STAGE;
+    const uint32_t scales_u32 = base_u32 + W * STAGES * STAGE + warp * STAGES * 2 * TILE_TOKENS * 4;   // FP8 only
+    const uint64_t policy = l2_policy_evict_first();
+    auto issue = [&](int it) {
+        const int s = it % STAGES, row = list[it].x;
+        const uint32_t bar = bars_u32 + (warp * STAGES + s) * 8, dst = ring_u32 + s * STAGE;
+        if constexpr (KV8) {
+            const uint32_t sdst = scales_u32 + s * 2 * TILE_TOKENS * 4;
+            mbar_arrive_expect_tx(bar, STAGE + 2 * TILE_TOKENS * 4);
+            tma_load_2d(dst, &tmk, 0, row, bar, policy);
+            tma_load_2d(dst + TILE, &tmv, 0, row, bar, policy);
+            bulk_load(sdst, p.k_scales + row, TILE_TOKENS * 4, bar, policy);
+            bulk_load(sdst + TILE_TOKENS * 4, p.v_scales + row, TILE_TOKENS * 4, bar, policy);
+        } else {
+            mbar_arrive_expect_tx(bar, STAGE);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                tma_load_2d(dst + h * SPAN, &tmk, h * 64, row, bar, policy);
+                tma_load_2d(dst + TILE + h * SPAN, &tmv, h * 64, row, bar, policy);
+            }
+        }
+    };
+    int issued = min(tiles, STAGES);
+    if (lane == 0)
+        for (int it = 0; it < issued; ++it) issue(it);
+
+    if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             uint32_t top = 0;                          // bf16 without its sign, as an integer: the exponent on top
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
@@ -306,13 +324,25 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     }
         }
 
-        // Values that not every row sees may be anything to the others, and what lies behind the context anything at all.
-        // The tiles at the end of the context: such values are added row by row in fp32, then their weights and words are 0.
+        // The tiles at the end of the context. What lies behind it may be anything: its words of V become 0, its weights are
+        // 0 already. So may the value of a token that not every row sees be to the rows that do not: where it is no number
+        // (or, FP8, far larger than the rest), the token is added in fp32 to the rows that see it, and its weights and words
+        // become 0 as well.
         const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
         if (whole < TILE_TOKENS) {
-            const int w0 = whole < 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos);
-            for (int kk = w0; kk < w1; ++kk) {
-                const int src = (kk & 7) * 4 + tq;     // the lane that holds this token's weights of the same columns
+            const int w0 = whole < 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos), some = w1 - w0;
+            uint8_t *vs = smem + (vb - base_u32);
+            uint32_t odd = 0;                          // such tokens
+            for (int c = lane; c < some * (TILE / TILE_TOKENS / 16); c += 32) {
+                const int row = w0 + c % some, chunk = c / some;
+                const uint4 x = *reinterpret_cast<const uint4 *>(vs + (chunk >> 3) * SPAN + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+                bool is = no_numbers<T, KV8>(x.x) || no_numbers<T, KV8>(x.y) || no_numbers<T, KV8>(x.z) || no_numbers<T, KV8>(x.w);
+                if constexpr (KV8) is |= !vset || !(fabsf(scale_v[row]) < __uint_as_float((uint32_t)(127 + vexp + 5) << 23));
+                odd |= (uint32_t)is << row;
+            }
+            odd = __reduce_or_sync(0xffffffffu, odd);
+            for (uint32_t left = odd; left; left &= left - 1) {
+                const int kk = __ffs(left) - 1, src = (kk & 7) * 4 + tq;   // the lane with this token's weights of the same columns
                 float pv[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -328,12 +358,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                         float v;
                         if constexpr (KV8) {
                             const int dim = md * 16 + 2 * gq + e;
-                            const uint8_t code = smem[(vb - base_u32) + kk * 128 + (((dim >> 4) ^ (kk & 7)) << 4) + (dim & 15)];
-                            const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)code);
+                            const uint32_t h2 = e4m3x2_to_f16x2(vs[kk * 128 + (((dim >> 4) ^ (kk & 7)) << 4) + (dim & 15)]);
                             v = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
                         } else {
                             const int dim = md * 16 + gq + 8 * e, c = dim >> 3;
-                            v = value16(*reinterpret_cast<const uint16_t *>(smem + (vb - base_u32) + (c >> 3) * SPAN + kk * 128 +
+                            v = value16(*reinterpret_cast<const uint16_t *>(vs + (c >> 3) * SPAN + kk * 128 +
                                                                             (((c & 7) ^ (kk & 7)) << 4) + (dim & 7) * 2), T());
                         }
 #pragma unroll
@@ -344,19 +373,18 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     }
             }
             __syncwarp();
-            const int zero = TILE_TOKENS - w0;
-            for (int c = lane; c < zero * 8 * (TILE / SPAN); c += 32) {
-                const int h = c / (zero * 8), rc = c - h * zero * 8;
-                *reinterpret_cast<uint4 *>(smem + (vb - base_u32) + h * SPAN + (w0 + rc / 8) * 128 + (rc % 8) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t gone = odd | (w1 < TILE_TOKENS ? 0xFFFFu << w1 : 0u);
+            for (int c = lane; c < TILE / 16; c += 32) {
+                const int row = (c >> 3) & (TILE_TOKENS - 1);
+                if (gone >> row & 1u) *reinterpret_cast<uint4 *>(vs + c * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             __syncwarp();
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (gq >= w0) sc[nt][j] = 0.f;
-                    if (gq + 8 >= w0) sc[nt][2 + j] = 0.f;
+                    if (gone >> gq & 1u) sc[nt][j] = 0.f;
+                    if (gone >> (gq + 8) & 1u) sc[nt][2 + j] = 0.f;
                 }
         }
 
@@ -411,7 +439,10 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         }
         __syncwarp();
         if (it + STAGES < tiles) {
-            if (lane == 0) issue(it + STAGES);
+            if (lane == 0) {
+                fence_proxy_async_smem();              // the stage's words that were zeroed, before the copy over them
+                issue(it + STAGES);
+            }
             ++issued;
         }
     }
@@ -504,22 +535,34 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 
     // ---- the CTAs' states, each CTA a share of the outputs
     cluster_sync();
-    int any_failed = 0;
-    for (int c = 0; c < ranks; ++c) any_failed |= ld_cluster_int(map_rank(smem_u32(failed), c));
+    // every CTA's words on their way before the first is used
+    const uint32_t at_failed = smem_u32(failed), at_mc = smem_u32(mc), at_oc = smem_u32(oc);
+    const bool any_failed = __any_sync(0xffffffffu, lane < ranks && ld_cluster_int(map_rank(at_failed, lane < ranks ? lane : 0)));
     if (!any_failed) {
         for (int idx = rank * ATT_THREADS + tid; idx < p.rows * D8; idx += ranks * ATT_THREADS) {
             const int r = idx / D8, d0 = (idx - r * D8) * 8;
+            float2 ms[ATT_MAX_RANKS];
+            float4 x[ATT_MAX_RANKS], y[ATT_MAX_RANKS];
+#pragma unroll
+            for (int c = 0; c < ATT_MAX_RANKS; ++c) {
+                ms[c] = make_float2(-INFINITY, 0.f);
+                x[c] = y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c < ranks) {
+                    ms[c] = ld_cluster_float2(map_rank(at_mc + r * 8, c));
+                    x[c] = ld_cluster_float4(map_rank(at_oc + (r * OS + d0) * 4, c));
+                    y[c] = ld_cluster_float4(map_rank(at_oc + (r * OS + d0 + 4) * 4, c));
+                }
+            }
             float top = -INFINITY, sum = 0.f, a[8] = {};
-            for (int c = 0; c < ranks; ++c) top = fmaxf(top, ld_cluster_float2(map_rank(smem_u32(mc + r), c)).x);
+#pragma unroll
+            for (int c = 0; c < ATT_MAX_RANKS; ++c) top = fmaxf(top, ms[c].x);
             const float ref = top == -INFINITY ? 0.f : top;
-            for (int c = 0; c < ranks; ++c) {
-                const float2 ms = ld_cluster_float2(map_rank(smem_u32(mc + r), c));
-                const uint32_t src = map_rank(smem_u32(oc + r * OS + d0), c);
-                const float4 x = ld_cluster_float4(src), y = ld_cluster_float4(src + 16);
-                const float f = exp2f(ms.x - ref);
-                sum += f * ms.y;
-                a[0] += f * x.x, a[1] += f * x.y, a[2] += f * x.z, a[3] += f * x.w;
-                a[4] += f * y.x, a[5] += f * y.y, a[6] += f * y.z, a[7] += f * y.w;
+#pragma unroll
+            for (int c = 0; c < ATT_MAX_RANKS; ++c) {
+                const float f = exp2f(ms[c].x - ref);
+                sum += f * ms[c].y;
+                a[0] += f * x[c].x, a[1] += f * x[c].y, a[2] += f * x[c].z, a[3] += f * x[c].w;
+                a[4] += f * y[c].x, a[5] += f * y[c].y, a[6] += f * y[c].z, a[7] += f * y[c].w;
             }
             store(r, d0, a, sum);
         }
@@ -532,9 +575,11 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
                                      cudaStream_t stream) {
     const int64_t units = (int64_t)p.num_seqs * p.Hkv;
     const int tiles = p.budget * (p.bs / TILE_TOKENS), nt = (p.rows + 7) / 8;
-    // CTAs of a cluster: enough for four rounds of resident CTAs, each with four tiles for every warp at least
     int ranks = 1;
-    while (ranks < 8 && units * ranks < 4LL * att_ctas(KV8, nt) * sm_count && tiles >= 2 * ranks * ATT_WARPS * 4) ranks *= 2;
+    while (ranks < ATT_MAX_RANKS &&
+           ((units * ranks < 2LL * sm_count && tiles >= 2 * ranks * ATT_WARPS) ||
+            (units * ranks < 4LL * att_ctas(KV8, nt) * sm_count && tiles >= 2 * ranks * ATT_WARPS * 16)))
+        ranks *= 2;
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
         const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8, n) * 8 + 16 +

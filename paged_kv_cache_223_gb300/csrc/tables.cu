@@ -12,6 +12,8 @@
 // comes to the same verdict, the CTAs share the returned blocks, meet at the cluster's barrier, and share the taken blocks,
 // the tokens and the new lengths. So the lengths, tables and the stack are changed in place by one launch without a
 // workspace, and a call that is refused changes nothing of them.
+#include <algorithm>
+
 #include "pa_cluster.cuh"
 #include "pa_device.cuh"
 #include "pa_sparse.h"
@@ -21,6 +23,8 @@ namespace pa {
 namespace {
 
 constexpr int TAB_THREADS = 512;
+constexpr int TOK_THREADS = 256;
+constexpr int TAB_MAX_TOKENS = 32768;                   // more of them get a kernel of their own
 
 struct Sums {
     long long tokens, back, taken;
@@ -46,6 +50,55 @@ __device__ __forceinline__ int owner(const int *start, int n, int i) {
     return lo;
 }
 
+// Positions and slots of the call's tokens, N at a time: four share the search and, as a rule, the block; in a call that has
+// threads for all its tokens one by one has the shorter chain (257 sequences of a few tokens: 6.0 us, four at a time 7.0).
+// block_of(b, kept, j): the id of the sequence's block j; kept_of(b): its tokens before the new ones.
+template <int N, typename Kept, typename Block>
+__device__ __forceinline__ void write_tokens(const TablesParams &p, const int *cu, int tokens, int first, int step, Kept kept_of,
+                                             Block block_of) {
+    const int bs = 1 << p.bs_shift;
+    for (int in = first; in < (p.num_tokens + N - 1) / N; in += step) {
+        int pos[N];
+        long long slot[N];
+        int b = N * in < tokens ? owner(cu, p.num_seqs, N * in) : 0, was = -1, id = -1, kept = N * in < tokens ? kept_of(b) : 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = N * in + e;
+            pos[e] = 0;
+            slot[e] = -1;
+            if (i >= tokens) continue;
+            if (cu[b + 1] <= i) {
+                do ++b;
+                while (cu[b + 1] <= i);
+                kept = kept_of(b);
+                was = -1;
+            }
+            pos[e] = kept + i - cu[b];
+            const int j = pos[e] >> p.bs_shift;
+            if (j != was) {
+                id = block_of(b, kept, j);
+                was = j;
+                if (id < 0 || id >= p.num_blocks) {
+                    set_status(p.status, STATUS_BOUNDS);
+                    id = -1;
+                }
+            }
+            if (id >= 0) slot[e] = ((long long)id << p.bs_shift) + (pos[e] & (bs - 1));
+        }
+        if constexpr (N == 4) {
+            if (p.vectors && 4 * in + 4 <= p.num_tokens) {
+                reinterpret_cast<int4 *>(p.positions)[in] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                reinterpret_cast<longlong2 *>(p.slots)[2 * in] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2 *>(p.slots)[2 * in + 1] = make_longlong2(slot[2], slot[3]);
+                continue;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (N * in + e < p.num_tokens) p.positions[N * in + e] = pos[e], p.slots[N * in + e] = slot[e];
+    }
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams p) {
@@ -65,12 +118,20 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     const int bs = 1 << p.bs_shift;
     const int n_free = __ldcg(p.num_free);
     Sums carry = {0, 0, 0};
+    int3 next = {0, 0, 0};                             // a sequence's length, what is kept of it, what is new: a round ahead
+    const auto fetch = [&](int b) {
+        if (b >= B) return;
+        next.x = __ldcg(p.context_lens + b);
+        next.y = p.keep_lens ? __ldcg(p.keep_lens + b) : 0x7FFFFFFF;
+        next.z = __ldcg(p.new_lens + b);
+    };
+    fetch(tid);
     for (int b0 = 0; b0 < B; b0 += threads) {
         const int b = b0 + tid;
         Sums v = {0, 0, 0};
+        const int len = next.x, keep = next.y, add = next.z;
+        fetch(b + threads);
         if (b < B) {
-            const int len = __ldcg(p.context_lens + b), add = __ldcg(p.new_lens + b);
-            const int keep = p.keep_lens ? __ldcg(p.keep_lens + b) : len;
             const int k = keep < len ? keep : len;
             if (len < 0 || len > p.max_len || add < 0 || keep < 0 || (long long)k + add > p.max_len) {
                 bad = 1;                               // every writer writes the same
@@ -108,7 +169,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     if (wrong || none_left) {                          // the same in every CTA: no table, length or block is touched
         if (gid == 0) set_status(p.status, wrong ? STATUS_BOUNDS : STATUS_NO_BLOCKS);
         for (int b = gid; b <= B; b += all) p.cu_q[b] = 0;
-        for (int i = gid; i < p.num_tokens; i += all) {
+        for (int i = gid; i < p.num_tokens && !p.tokens_apart; i += all) {
             p.positions[i] = 0;
             p.slots[i] = -1;
         }
@@ -139,43 +200,14 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
         if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
         p.block_tables[b * p.stride + j] = id;
     }
-    // four tokens at a time: they share the search and, as a rule, the block
-    for (int i4 = gid; i4 < (p.num_tokens + 3) / 4; i4 += all) {
-        int pos[4];
-        long long slot[4];
-        int b = 4 * i4 < tokens ? owner(cu, B, 4 * i4) : B, was = -1, id = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 4 * i4 + e;
-            pos[e] = 0;
-            slot[e] = -1;
-            if (i >= tokens) continue;
-            while (cu[b + 1] <= i) ++b, was = -1;
-            pos[e] = kept[b] + i - cu[b];
-            const int j = pos[e] >> p.bs_shift;
-            if (j != was) {
-                // a block that this call takes is read where it comes from, not from the table that it is written to
-                const int have = (kept[b] + bs - 1) >> p.bs_shift;
-                id = j < have ? __ldcg(p.block_tables + b * p.stride + j)
-                              : __ldcg(p.free_blocks + top - (taken[b] + j - have));
-                was = j;
-                if (id < 0 || id >= p.num_blocks) {
-                    set_status(p.status, STATUS_BOUNDS);
-                    id = -1;
-                }
-            }
-            if (id >= 0) slot[e] = ((long long)id << p.bs_shift) + (pos[e] & (bs - 1));
-        }
-        if (p.vectors && 4 * i4 + 4 <= p.num_tokens) {
-            reinterpret_cast<int4 *>(p.positions)[i4] = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            reinterpret_cast<longlong2 *>(p.slots)[2 * i4] = make_longlong2(slot[0], slot[1]);
-            reinterpret_cast<longlong2 *>(p.slots)[2 * i4 + 1] = make_longlong2(slot[2], slot[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (4 * i4 + e < p.num_tokens) p.positions[4 * i4 + e] = pos[e], p.slots[4 * i4 + e] = slot[e];
-        }
-    }
+    const auto kept_of = [&](int b) { return kept[b]; };
+    // a block that this call takes is read where it comes from, not from the table that it is written to
+    const auto block_of = [&](int b, int k, int j) {
+        const int have = (k + bs - 1) >> p.bs_shift;
+        return j < have ? __ldcg(p.block_tables + b * p.stride + j) : __ldcg(p.free_blocks + top - (taken[b] + j - have));
+    };
+    if (!p.tokens_apart && p.num_tokens <= 2 * all) write_tokens<1>(p, cu, tokens, gid, all, kept_of, block_of);
+    else if (!p.tokens_apart) write_tokens<4>(p, cu, tokens, gid, all, kept_of, block_of);
     for (int b = gid; b <= B; b += all) {
         p.cu_q[b] = cu[b];
         if (b < B) p.context_lens[b] = kept[b] + cu[b + 1] - cu[b];
@@ -183,16 +215,32 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     if (gid == 0) *p.num_free = n_free + F - T;
 }
 
-cudaError_t launch_tables(TablesParams p, cudaStream_t stream) {
+// The tokens of a large call, behind tables_kernel, on all SMs: from the tables as they are then.
+__global__ void __launch_bounds__(TOK_THREADS) tokens_kernel(const TablesParams p) {
+    extern __shared__ int cu_sm[];
+    pdl_trigger();
+    pdl_wait();
+    for (int b = threadIdx.x; b <= p.num_seqs; b += TOK_THREADS) cu_sm[b] = __ldg(p.cu_q + b);
+    __syncthreads();
+    write_tokens<4>(p, cu_sm, cu_sm[p.num_seqs], blockIdx.x * TOK_THREADS + threadIdx.x, gridDim.x * TOK_THREADS,
+                 [&](int b) { return __ldg(p.context_lens + b) - (cu_sm[b + 1] - cu_sm[b]); },
+                 [&](int b, int, int j) { return __ldg(p.block_tables + b * p.stride + j); });
+}
+
+cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream) {
     const size_t smem = (size_t)(4 * p.num_seqs + 3) * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     p.vectors = (reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
+    p.tokens_apart = p.num_tokens > TAB_MAX_TOKENS;
     // CTAs of the cluster: one for each two rounds of four tokens per thread
     int ranks = 1;
     while (ranks < 16 && p.num_tokens > ranks * TAB_THREADS * 8) ranks *= 2;
-    return launch_clusters(tables_kernel, ranks, TAB_THREADS, smem, ranks, stream, p);
+    e = launch_clusters(tables_kernel, ranks, TAB_THREADS, smem, ranks, stream, p);
+    if (e != cudaSuccess || !p.tokens_apart) return e;
+    const int ctas = std::min((p.num_tokens + 4 * TOK_THREADS - 1) / (4 * TOK_THREADS), 4 * sm_count);
+    return launch_pdl(tokens_kernel, dim3(ctas), dim3(TOK_THREADS), (size_t)(p.num_seqs + 1) * sizeof(int), stream, p);
 }
 
 }  // namespace pa
