@@ -74,10 +74,6 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
     return (uint32_t)(a & 0xFF) | (uint32_t)(b & 0xFF) << 8 | (uint32_t)(c & 0xFF) << 16 | (uint32_t)d << 24;
 }
 
-// max with NaN kept
-__device__ __forceinline__ float max_nan(float a, float b) { return a != a ? a : (a > b || b != b ? (b != b ? b : a) : b); }
-__device__ __forceinline__ float min_nan(float a, float b) { return a != a ? a : (a < b || b != b ? (b != b ? b : a) : b); }
-
 }  // namespace
 
 // ------------------------------------------------------------------ bounds
@@ -149,30 +145,36 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
         }
         const int64_t unit = (int64_t)id * p.Hkv + h;
         float vmax[EL], vmin[EL];
+        bool odd = false;                              // FP8: a NaN code, or a scale that is no number
         if constexpr (KV8) {
             const uint8_t *k = static_cast<const uint8_t *>(p.k_cache) + unit * p.bs * D + sub * 16;
             const float *sc = p.k_scales + unit * p.bs;
 #pragma unroll
             for (int e = 0; e < EL; ++e) vmax[e] = -INFINITY, vmin[e] = INFINITY;
+#pragma unroll 4
             for (int r = grp; r < rows; r += RPS) {
                 const uint4 w = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D));
                 const float f = __ldg(sc + r);
+                odd |= !(fabsf(f) < INFINITY);
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(ww[c >> 1] >> ((c & 1) * 16)));
-                    const float2 x = unpack2(h2, __half());
-                    const float a = x.x * f, b = x.y * f;
-                    vmax[2 * c] = max_nan(vmax[2 * c], a), vmin[2 * c] = min_nan(vmin[2 * c], a);
-                    vmax[2 * c + 1] = max_nan(vmax[2 * c + 1], b), vmin[2 * c + 1] = min_nan(vmin[2 * c + 1], b);
+                for (int c = 0; c < 4; ++c) {
+                    odd |= __vcmpeq4(ww[c] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 x = unpack2(e4m3x2_to_f16x2((uint16_t)(ww[c] >> (16 * e))), __half());
+                        const int i = 4 * c + 2 * e;
+                        vmax[i] = fmaxf(vmax[i], x.x * f), vmin[i] = fminf(vmin[i], x.x * f);
+                        vmax[i + 1] = fmaxf(vmax[i + 1], x.y * f), vmin[i + 1] = fminf(vmin[i + 1], x.y * f);
+                    }
                 }
             }
 #pragma unroll
             for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
                 for (int e = 0; e < EL; ++e) {
-                    vmax[e] = max_nan(vmax[e], __shfl_xor_sync(0xffffffffu, vmax[e], o));
-                    vmin[e] = min_nan(vmin[e], __shfl_xor_sync(0xffffffffu, vmin[e], o));
+                    vmax[e] = fmaxf(vmax[e], __shfl_xor_sync(0xffffffffu, vmax[e], o));
+                    vmin[e] = fminf(vmin[e], __shfl_xor_sync(0xffffffffu, vmin[e], o));
                 }
         } else {
             const uint16_t *k = static_cast<const uint16_t *>(p.k_cache) + unit * p.bs * D + sub * 8;
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
 #pragma unroll
         for (int e = 0; e < EL; ++e) top = max(top, max(abs_bits(vmax[e]), abs_bits(vmin[e])));
         top = __reduce_max_sync(0xffffffffu, top);
-        const bool number = top < INF_BITS;            // else: codes 0 and an infinite step, a block that is always wanted
+        // else: codes 0 and an infinite step, a block that is always wanted
+        const bool number = top < INF_BITS && !(KV8 && __any_sync(0xffffffffu, odd));
         const float step = number ? step_of(top) : INFINITY, inv = number ? inverse_of(step) : 0.f;
         if (grp < 2) {
             uint32_t out[EL / 4];
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
 cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, int sm_count, cudaStream_t stream) {
     // touched blocks: at most one for each new token, and the full ones plus two ends of each sequence
     const int64_t blocks = std::min<int64_t>(p.num_tokens, p.num_tokens / p.bs + 2LL * p.num_seqs);
-    const int64_t ctas = (blocks * p.Hkv + BND_WARPS - 1) / BND_WARPS, most = 8LL * sm_count;
+    const int64_t ctas = (blocks * p.Hkv + BND_WARPS - 1) / BND_WARPS, most = 16LL * sm_count;
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min(ctas, most));
     const size_t smem = (size_t)(2 * p.num_seqs + 1) * sizeof(int);
     const auto launch = [&](auto kernel) {
@@ -243,7 +246,7 @@ cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, in
 
 constexpr int SEL_WARPS = 8;
 constexpr int SEL_THREADS = SEL_WARPS * 32;
-constexpr int SEL_CTAS = 4;                           // per SM
+constexpr int SEL_CTAS = 4;                            // per SM
 constexpr int SEL_BINS = 256;
 static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
 constexpr int SEL_MAX_RANKS = 16;
@@ -289,6 +292,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // above and at the threshold comes out of the same histograms, so the indices are written in order without another round.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const SelectParams p) {
+    constexpr int W = SEL_WARPS, THREADS = SEL_THREADS;
     constexpr int RP = NT * 8, LOADS = D / 64;         // 128-byte pieces of [hi, lo]
     constexpr int QS = sel_q_stride(D);
     extern __shared__ __align__(16) uint8_t ssm[];
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     uint32_t *ends = reinterpret_cast<uint32_t *>(hist + 4 * SEL_BINS);   // least and largest key, of the CTA
     int *digit = reinterpret_cast<int *>(ends + 2);    // the digit, what is needed of its bin
     int *wtot = digit + 2;                             // [warps] sums; [warps][3] counts
-    uint32_t *keys = reinterpret_cast<uint32_t *>(wtot + SEL_WARPS * 4);   // the block ids, then the keys in their place
+    uint32_t *keys = reinterpret_cast<uint32_t *>(wtot + W * 4);   // the block ids, then the keys in their place
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int unit = (int)(blockIdx.x / ranks), g = unit % p.Hkv, b = unit / p.Hkv;
@@ -309,30 +313,40 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     // one CTA to a unit holds its blocks whatever the length is: their ids are on their way before it is known
     const int32_t *trow = p.block_tables + b * p.stride;
     if (ranks == 1)
-        for (int i = tid; i < min(p.chunk, (int)p.stride); i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i);
+        for (int i = tid; i < min(p.chunk, (int)p.stride); i += THREADS) keys[i] = (uint32_t)__ldg(trow + i);
 
     // ---- query rows
-    for (int r = warp; r < RP; r += SEL_WARPS) {
-        constexpr int PL = D / 32;
-        float x[PL];
-        uint32_t top = 0;
+    constexpr int PL = D / 32, QR = (RP + W - 1) / W;  // values per lane; rows per warp, on their way together
+    float x[QR][PL];
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+        const int r = warp + i * W;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) x[i][e] = 0.f;
         if (r < p.rows) {
             const int qi = r / p.G, hh = r - qi * p.G;
             const T *q = static_cast<const T *>(p.q) + (((int64_t)b * p.q_len + qi) * p.Hq + g * p.G + hh) * D;
 #pragma unroll
             for (int e = 0; e < PL; e += 2) {
                 const float2 v = unpack2(__ldg(reinterpret_cast<const uint32_t *>(q + lane * PL + e)), T());
-                x[e] = v.x, x[e + 1] = v.y;
-                top = max(top, max(abs_bits(v.x), abs_bits(v.y)));
+                x[i][e] = v.x, x[i][e + 1] = v.y;
             }
         }
+    }
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+        const int r = warp + i * W;
+        if (r >= RP) break;
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) top = max(top, abs_bits(x[i][e]));
         top = __reduce_max_sync(0xffffffffu, top);
         const bool counts_row = r < p.rows && top < INF_BITS;
         const float step = counts_row ? step_of(top) : 0.f, inv = inverse_of(step);
         __half *row = reinterpret_cast<__half *>(qsm + r * QS);
 #pragma unroll
         for (int e = 0; e < PL; ++e) {
-            const int c = counts_row ? code_of(x[e], step, inv) : 0;
+            const int c = counts_row ? code_of(x[i][e], step, inv) : 0;
             row[sel_q_at(lane * PL + e)] = __int2half_rn(max(c, 0));
             row[sel_q_at(D + lane * PL + e)] = __int2half_rn(min(c, 0));
         }
@@ -345,7 +359,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     const int n = (len + p.bs - 1) / p.bs;
     int32_t *out = p.selected + (int64_t)unit * p.budget;
     if (n <= p.budget) {                               // all of them (the same in every CTA of the cluster)
-        for (int i = rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) out[i] = i < n ? i : -1;
+        for (int i = rank * THREADS + tid; i < p.budget; i += ranks * THREADS) out[i] = i < n ? i : -1;
         return;
     }
     // blocks of this CTA, shared out evenly in tiles of 16; those of [lo, hi) are chosen by score, the others always
@@ -353,8 +367,8 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     const int i0 = rank * per, mine = max(0, min(per, n - i0));
     const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
     if (ranks > 1)
-        for (int i = tid; i < mine; i += SEL_THREADS) keys[i] = (uint32_t)__ldg(trow + i0 + i);
-    for (int i = tid; i < 4 * SEL_BINS; i += SEL_THREADS) hist[i] = 0;
+        for (int i = tid; i < mine; i += THREADS) keys[i] = (uint32_t)__ldg(trow + i0 + i);
+    for (int i = tid; i < 4 * SEL_BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) ends[0] = 0xFFFFFFFFu, ends[1] = 0u;
     __syncthreads();
 
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) mul[nt][e] = qmul[nt * 8 + 2 * tq + e], add[nt][e] = qadd[nt * 8 + 2 * tq + e];
-    for (int t = warp * 16; t < mine; t += SEL_WARPS * 16) {
+    for (int t = warp * 16; t < mine; t += W * 16) {
         int id[2];
         bool ok[2];
 #pragma unroll
@@ -450,7 +464,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
         const int shift = max(0, bits - 8);
         const uint32_t digits = (1u << (bits - shift)) - 1u;
         int *h = hist + pass * SEL_BINS;
-        for (int i = lo + tid; i < hi; i += SEL_THREADS) {
+        for (int i = lo + tid; i < hi; i += THREADS) {
             const uint32_t key = keys[i];
             if ((key & mask) == prefix) atomicAdd(h + ((key >> shift) & digits), 1);
         }
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
         __syncthreads();
         const int d = digit[0];
         // the bin's size, and what lies before this CTA in the bins above and in this one
-        int *cnt = wtot + SEL_WARPS;                   // [warps][3]
+        int *cnt = wtot + W;                   // [warps][3]
         const int up = __reduce_add_sync(0xffffffffu, bin > d ? before : 0);
         const int at = __reduce_add_sync(0xffffffffu, bin == d ? before : 0);
         const int size = __reduce_add_sync(0xffffffffu, bin == d ? sum : 0);
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
         int bin_size = 0;
         eq_before = 0;
 #pragma unroll
-        for (int w = 0; w < SEL_WARPS; ++w) gt_before += cnt[3 * w], eq_before += cnt[3 * w + 1], bin_size += cnt[3 * w + 2];
+        for (int w = 0; w < W; ++w) gt_before += cnt[3 * w], eq_before += cnt[3 * w + 1], bin_size += cnt[3 * w + 2];
         prefix |= (uint32_t)d << shift;
         mask = shift == 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << shift;
         bits = bin_size == need ? 0 : shift;           // a bin that is taken whole ends it
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     if (ranks > 1) cluster_arrive();                   // this CTA reads no other one's memory any more
 
     // ---- the indices, in order: a stretch of blocks per warp, counted and then written
-    const int stretch = (mine + SEL_THREADS - 1) / SEL_THREADS * 32, s0 = min(mine, warp * stretch), s1 = min(mine, s0 + stretch);
+    const int stretch = (mine + THREADS - 1) / THREADS * 32, s0 = min(mine, warp * stretch), s1 = min(mine, s0 + stretch);
     const auto taken = [&](int i, bool &is_gt, bool &is_eq) {
         const uint32_t key = i < s1 ? keys[i] & mask : 0u;
         const bool scored = i >= lo && i < hi;

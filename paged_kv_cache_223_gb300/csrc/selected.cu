@@ -27,6 +27,8 @@ constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maxi
 
 __host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
 __host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : !kv8 && nt == 1 ? 3 : 2; }
+// CTAs that fit an SM: by shared memory with one column of eight rows, by registers with more.
+constexpr int att_resident(bool kv8, int nt) { return kv8 && nt == 2 ? 3 : att_ctas(kv8, nt); }
 __host__ __device__ constexpr int att_tile_bytes(int D, bool kv8) { return TILE_TOKENS * (kv8 ? 128 : 2 * D); }
 __host__ __device__ constexpr int att_scale_bytes(bool kv8, int nt) {
     return kv8 ? (ATT_WARPS * att_stages(kv8, nt) * 2 * TILE_TOKENS * 4 + 1023) / 1024 * 1024 : 0;
@@ -575,11 +577,17 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
                                      cudaStream_t stream) {
     const int64_t units = (int64_t)p.num_seqs * p.Hkv;
     const int tiles = p.budget * (p.bs / TILE_TOKENS), nt = (p.rows + 7) / 8;
+    // CTAs of a cluster. A round of resident CTAs lasts as long as a warp's tiles and about three more for the start and the
+    // joining of its warps, another three where a cluster joins. Of 130 shapes (1 to 2048 units, lists of 16 to 1024 blocks,
+    // 4 to 32 rows, both formats) this picks the best of 1, 2, 4, 8 but for 1.2% on average, 24% at most; "at least two CTAs
+    // per SM" lost 8.5% and up to 83% (128 units, 16 blocks: 6.1 us as single CTAs, 11.0 as clusters of four).
+    const int64_t slots = (int64_t)att_resident(KV8, nt) * sm_count;
     int ranks = 1;
-    while (ranks < ATT_MAX_RANKS &&
-           ((units * ranks < 2LL * sm_count && tiles >= 2 * ranks * ATT_WARPS) ||
-            (units * ranks < 4LL * att_ctas(KV8, nt) * sm_count && tiles >= 2 * ranks * ATT_WARPS * 16)))
-        ranks *= 2;
+    int64_t best = 0;
+    for (int r = 1; r <= ATT_MAX_RANKS; r *= 2) {
+        const int64_t cost = (units * r + slots - 1) / slots * ((r > 1 ? 6 : 3) + (tiles + r * ATT_WARPS - 1) / (r * ATT_WARPS));
+        if (r == 1 || cost < best) best = cost, ranks = r;
+    }
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
         const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8, n) * 8 + 16 +

@@ -117,51 +117,47 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     __syncthreads();
     const int bs = 1 << p.bs_shift;
     const int n_free = __ldcg(p.num_free);
-    Sums carry = {0, 0, 0};
-    int3 next = {0, 0, 0};                             // a sequence's length, what is kept of it, what is new: a round ahead
-    const auto fetch = [&](int b) {
-        if (b >= B) return;
-        next.x = __ldcg(p.context_lens + b);
-        next.y = p.keep_lens ? __ldcg(p.keep_lens + b) : 0x7FFFFFFF;
-        next.z = __ldcg(p.new_lens + b);
-    };
-    fetch(tid);
-    for (int b0 = 0; b0 < B; b0 += threads) {
-        const int b = b0 + tid;
-        Sums v = {0, 0, 0};
-        const int len = next.x, keep = next.y, add = next.z;
-        fetch(b + threads);
-        if (b < B) {
-            const int k = keep < len ? keep : len;
-            if (len < 0 || len > p.max_len || add < 0 || keep < 0 || (long long)k + add > p.max_len) {
-                bad = 1;                               // every writer writes the same
-            } else {
-                const int have = (int)(((long long)k + bs - 1) >> p.bs_shift);
-                const int old = (int)(((long long)len + bs - 1) >> p.bs_shift);
-                const int want = (int)(((long long)k + add + bs - 1) >> p.bs_shift);
-                v = {add, old - have, want > have ? want - have : 0};
-                kept[b] = k;
-            }
+    for (int b = tid; b < B; b += threads) {
+        const int len = __ldcg(p.context_lens + b), add = __ldcg(p.new_lens + b);
+        const int keep = p.keep_lens ? __ldcg(p.keep_lens + b) : 0x7FFFFFFF;
+        const int k = keep < len ? keep : len;
+        cu[b] = back[b] = taken[b] = 0;
+        if (len < 0 || len > p.max_len || add < 0 || keep < 0 || (long long)k + add > p.max_len) {
+            bad = 1;                                   // every writer writes the same
+        } else {
+            const int have = (k + bs - 1) >> p.bs_shift, old = (len + bs - 1) >> p.bs_shift;
+            const int want = (k + add + bs - 1) >> p.bs_shift;
+            kept[b] = k;
+            cu[b] = add;
+            back[b] = old - have;
+            taken[b] = max(want - have, 0);
         }
-        Sums s = v;
+    }
+    // exclusive sums: a stretch of sequences per thread (its own ones where there are as many threads), whose totals are
+    // summed over the block
+    if (B > threads) __syncthreads();
+    const int per = (B + threads - 1) / threads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    Sums own = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) own = own + Sums{cu[b], back[b], taken[b]};
+    Sums s = own;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const Sums u = shfl_up(s, d);
-            if (lane >= d) s = s + u;
-        }
-        if (lane == 31) wsum[warp] = s;
-        __syncthreads();
-        Sums before = carry;
-        for (int w = 0; w < threads / 32; ++w) {
-            if (w < warp) before = before + wsum[w];
-            carry = carry + wsum[w];
-        }
-        if (b < B) {
-            cu[b] = (int)(before.tokens + s.tokens - v.tokens);
-            back[b] = (int)(before.back + s.back - v.back);
-            taken[b] = (int)(before.taken + s.taken - v.taken);
-        }
-        __syncthreads();
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sums u = shfl_up(s, d);
+        if (lane >= d) s = s + u;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    Sums run = {s.tokens - own.tokens, s.back - own.back, s.taken - own.taken}, carry = {0, 0, 0};
+    for (int w = 0; w < threads / 32; ++w) {
+        if (w < warp) run = run + wsum[w];
+        carry = carry + wsum[w];
+    }
+    for (int b = b0; b < b1; ++b) {
+        const Sums v = {cu[b], back[b], taken[b]};
+        cu[b] = (int)run.tokens;
+        back[b] = (int)run.back;
+        taken[b] = (int)run.taken;
+        run = run + v;
     }
     const bool wrong = bad || n_free < 0 || n_free > p.num_blocks || n_free + carry.back > p.num_blocks ||
                        carry.tokens > p.num_tokens;
