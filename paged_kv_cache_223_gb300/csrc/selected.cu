@@ -26,9 +26,9 @@ constexpr int ATT_MAX_RANKS = 8;
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
 
 __host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
+// CTAs per SM: by shared memory with one column of eight rows, by registers with more. FP8 pools with 16 rows at three CTAs
+// (168 registers, spills) lost as much as they won: 19 sequences of a verify 18.9 -> 23.0 us, 64 of 2048 tokens 68.2 -> 67.1.
 __host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : !kv8 && nt == 1 ? 3 : 2; }
-// CTAs that fit an SM: by shared memory with one column of eight rows, by registers with more.
-constexpr int att_resident(bool kv8, int nt) { return kv8 && nt == 2 ? 3 : att_ctas(kv8, nt); }
 __host__ __device__ constexpr int att_tile_bytes(int D, bool kv8) { return TILE_TOKENS * (kv8 ? 128 : 2 * D); }
 __host__ __device__ constexpr int att_scale_bytes(bool kv8, int nt) {
     return kv8 ? (ATT_WARPS * att_stages(kv8, nt) * 2 * TILE_TOKENS * 4 + 1023) / 1024 * 1024 : 0;
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 const int row = (c >> 3) & (TILE_TOKENS - 1);
                 if (gone >> row & 1u) *reinterpret_cast<uint4 *>(vs + c * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
+            fence_proxy_async_smem();                  // before the copy that comes over these words
             __syncwarp();
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -441,10 +442,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         }
         __syncwarp();
         if (it + STAGES < tiles) {
-            if (lane == 0) {
-                fence_proxy_async_smem();              // the stage's words that were zeroed, before the copy over them
-                issue(it + STAGES);
-            }
+            if (lane == 0) issue(it + STAGES);
             ++issued;
         }
     }
@@ -581,7 +579,7 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
     // joining of its warps, another three where a cluster joins. Of 130 shapes (1 to 2048 units, lists of 16 to 1024 blocks,
     // 4 to 32 rows, both formats) this picks the best of 1, 2, 4, 8 but for 1.2% on average, 24% at most; "at least two CTAs
     // per SM" lost 8.5% and up to 83% (128 units, 16 blocks: 6.1 us as single CTAs, 11.0 as clusters of four).
-    const int64_t slots = (int64_t)att_resident(KV8, nt) * sm_count;
+    const int64_t slots = (int64_t)att_ctas(KV8, nt) * sm_count;
     int ranks = 1;
     int64_t best = 0;
     for (int r = 1; r <= ATT_MAX_RANKS; r *= 2) {

@@ -494,13 +494,18 @@ class Pool:
             _need(keep_lens, "keep_lens", i32, index, (B,))
         if num_tokens < 0:
             raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
-        for name, t, dt, n in (("cu_q", cu_q, i32, B + 1), ("positions", positions, i32, num_tokens),
-                               ("slot_mapping", slot_mapping, torch.int64, num_tokens)):
-            if t is not None:
-                _need(t, name, dt, index, (n,))
-        cu_q = _new((B + 1,), i32, self.device, stream) if cu_q is None else cu_q
-        positions = _new((num_tokens,), i32, self.device, stream) if positions is None else positions
-        slot_mapping = _new((num_tokens,), torch.int64, self.device, stream) if slot_mapping is None else slot_mapping
+        if cu_q is None:
+            cu_q = _new((B + 1,), i32, self.device, stream)
+        else:
+            _need(cu_q, "cu_q", i32, index, (B + 1,))
+        if positions is None:
+            positions = _new((num_tokens,), i32, self.device, stream)
+        else:
+            _need(positions, "positions", i32, index, (num_tokens,))
+        if slot_mapping is None:
+            slot_mapping = _new((num_tokens,), torch.int64, self.device, stream)
+        else:
+            _need(slot_mapping, "slot_mapping", torch.int64, index, (num_tokens,))
         a = PaTablesArgs(B, num_tokens, stride, new_lens.data_ptr(), _ptr(keep_lens), context_lens.data_ptr(),
                          block_tables.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), cu_q.data_ptr(),
                          positions.data_ptr(), slot_mapping.data_ptr())
@@ -568,9 +573,9 @@ class Pool:
         stride, budget = self._rows(q, block_tables, context_lens), int(budget)
         self._bounds(bounds)
         B, q_len, Hq, _ = q.shape
-        shape = (B, self.geometry[1], budget)
+        shape = (B, self.geometry[1], max(budget, 0))
         if out is None:
-            out = _new((B, shape[1], max(budget, 0)), torch.int32, self.device, stream)
+            out = _new(shape, torch.int32, self.device, stream)
         else:
             _need(out, "out", torch.int32, self.device.index, shape)
         _check(_sparse_lib().pa_select_blocks(
