@@ -368,7 +368,8 @@ pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
  *   num_seqs       0 .. PA_TABLES_MAX_SEQS
  *   bounds         device, 32-byte aligned, pa_key_bounds_size() bytes
  * Lengths and block ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at
- * pa_pool_check), the sequence or block is skipped. Two sequences that name one
+ * pa_pool_check), the sequence or block is skipped, where cu_q decreases
+ * possibly every sequence. Two sequences that name one
  * block with different fillings: whose bounds land is unspecified.
  */
 pa_status pa_key_bounds(pa_pool *pool, const void *k_cache, const int32_t *cu_q, const int32_t *block_tables,
@@ -381,9 +382,10 @@ pa_status pa_key_bounds(pa_pool *pool, const void *k_cache, const int32_t *cu_q,
  * num_first and the last num_last blocks of the context are always among them.
  * The score of a block is the largest, over the query rows that read the KV head
  * (q_len rows of num_q_heads / num_kv_heads heads), of
- *   s * step * sum_d max(c[d] * hi[d], c[d] * lo[d])
+ *   s * step * (sum of c[d] * hi[d] where c[d] > 0 and of c[d] * lo[d] where c[d] < 0)
  * with the row as whole numbers c and a step s, made from q as the bounds' codes
- * are from the keys. Sums are of whole numbers and steps are powers of two, so
+ * are from the keys: the largest product that a key within the bounds could
+ * have with it. Sums are of whole numbers and steps are powers of two, so
  * scores are exact (in fp32's range); of equal scores the lowest block comes
  * first. A row of q with a NaN or an infinity does not count.
  *   q              device [num_seqs, q_len, num_q_heads, head_dim] of the pool's dtype
@@ -411,7 +413,7 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
  * blocks selected[b][h / (num_q_heads / num_kv_heads)][0 .. budget). The list is
  * pa_select_blocks's or any other, in any order; negative entries are skipped, a
  * block listed twice counts twice. A row that sees no listed token gives zeros
- * (so does a context of 0). Values at positions a row does not see do not reach
+ * (so does a context of 0); one whose scores are all -inf gives NaN. Values at positions a row does not see do not reach
  * it, whatever their words are. Softmax and sums are fp32; deterministic run to
  * run. 16-bit pools with heads of 64 or 128 and FP8 pools.
  *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping

@@ -87,16 +87,16 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
     extern __shared__ int bsm[];
     const int B = p.num_seqs;
     int *start = bsm, *first = start + B + 1;          // sums of B + 1; first touched block
-    __shared__ int wsum[BND_WARPS];
+    __shared__ long long wsum[BND_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    int carry = 0;
+    long long carry = 0;
     for (int b0 = 0; b0 < B; b0 += BND_WARPS * 32) {
         const int b = b0 + tid;
         int n = 0;
         if (b < B) {
-            const int lo = __ldg(p.cu_q + b), hi = __ldg(p.cu_q + b + 1), len = __ldg(p.context_lens + b);
+            const int lo = p.cu_q[b], hi = p.cu_q[b + 1], len = p.context_lens[b];
             if (lo < 0 || hi < lo || hi > p.num_tokens || len < hi - lo || len > p.max_len) {
                 if (blockIdx.x == 0) set_status(p.status, STATUS_BOUNDS);
             } else if (hi > lo) {
@@ -104,30 +104,33 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
                 n = (len - 1) / p.bs - first[b] + 1;
             }
         }
-        int s = n;
+        long long s = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, s, d);
+            const long long u = __shfl_up_sync(0xffffffffu, s, d);
             if (lane >= d) s += u;
         }
         if (lane == 31) wsum[warp] = s;
         __syncthreads();
-        int before = carry;
+        long long before = carry;
         for (int w = 0; w < BND_WARPS; ++w) {
             if (w < warp) before += wsum[w];
             carry += wsum[w];
         }
-        if (b < B) start[b] = before + s - n;
+        if (b < B) start[b] = (int)(before + s - n);
         __syncthreads();
     }
-    if (tid == 0) start[B] = carry;
+    // more than num_tokens tokens can touch: sequences share rows of cu_q (one decreases, which is flagged); the sums of 32
+    // bits and the work would have no bound
+    if (carry > p.num_tokens / p.bs + 2LL * B) return;
+    if (tid == 0) start[B] = (int)carry;
     __syncthreads();
 
     constexpr int LPR = KV8 ? D / 16 : D / 8;          // lanes per row
     constexpr int RPS = 32 / LPR;                      // rows a step
     constexpr int EL = KV8 ? 16 : 8;                   // dimensions per lane
     const int sub = lane % LPR, grp = lane / LPR;
-    const int64_t items = (int64_t)carry * p.Hkv;
+    const int64_t items = carry * p.Hkv;
     for (int64_t item = (int64_t)blockIdx.x * BND_WARPS + warp; item < items; item += (int64_t)gridDim.x * BND_WARPS) {
         const int i = (int)(item / p.Hkv), h = (int)(item - (int64_t)i * p.Hkv);
         int lo = 0, hi = B;                            // the last sequence that starts at or before i
@@ -137,8 +140,8 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
             else hi = mid;
         }
         const int j = first[lo] + i - start[lo];
-        const int rows = min(p.bs, __ldg(p.context_lens + lo) - j * p.bs);
-        const int id = __ldg(p.block_tables + lo * p.stride + j);
+        const int rows = min(p.bs, p.context_lens[lo] - j * p.bs);
+        const int id = p.block_tables[lo * p.stride + j];
         if (id < 0 || id >= p.num_blocks) {
             if (lane == 0) set_status(p.status, STATUS_BOUNDS);
             continue;
@@ -153,8 +156,8 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
             for (int e = 0; e < EL; ++e) vmax[e] = -INFINITY, vmin[e] = INFINITY;
 #pragma unroll 4
             for (int r = grp; r < rows; r += RPS) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D));
-                const float f = __ldg(sc + r);
+                const uint4 w = *reinterpret_cast<const uint4 *>(k + (int64_t)r * D);
+                const float f = sc[r];
                 odd |= !(fabsf(f) < INFINITY);
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -179,11 +182,11 @@ __global__ void __launch_bounds__(BND_WARPS * 32) bounds_kernel(const BoundsPara
         } else {
             const uint16_t *k = static_cast<const uint16_t *>(p.k_cache) + unit * p.bs * D + sub * 8;
             // rows behind the last repeat row 0, which every group may count
-            uint4 w = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)(grp < rows ? grp : 0) * D));
+            uint4 w = *reinterpret_cast<const uint4 *>(k + (int64_t)(grp < rows ? grp : 0) * D);
             uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll 4
             for (int r = grp + RPS; r < rows; r += RPS) {
-                w = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D));
+                w = *reinterpret_cast<const uint4 *>(k + (int64_t)r * D);
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) a[c] = max2(a[c], ww[c], T()), b[c] = min2(b[c], ww[c], T());
@@ -260,7 +263,7 @@ __host__ __device__ constexpr size_t sel_smem(int D, int NT, int chunk) {
 
 // 32 bytes that no other CTA of this call reads (the bounds of a step are larger than what L2 could keep for the next).
 __device__ __forceinline__ void ldg256(const void *p, uint32_t (&w)[8]) {
-    asm volatile("ld.global.nc.L1::evict_first.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p));
 }
@@ -309,11 +312,11 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     pdl_trigger();
     pdl_wait();
 
-    int len = __ldg(p.context_lens + b);
+    int len = p.context_lens[b];
     // one CTA to a unit holds its blocks whatever the length is: their ids are on their way before it is known
     const int32_t *trow = p.block_tables + b * p.stride;
     if (ranks == 1)
-        for (int i = tid; i < min(p.chunk, (int)p.stride); i += THREADS) keys[i] = (uint32_t)__ldg(trow + i);
+        for (int i = tid; i < min(p.chunk, (int)p.stride); i += THREADS) keys[i] = (uint32_t)trow[i];
 
     // ---- query rows
     constexpr int PL = D / 32, QR = (RP + W - 1) / W;  // values per lane; rows per warp, on their way together
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
             const T *q = static_cast<const T *>(p.q) + (((int64_t)b * p.q_len + qi) * p.Hq + g * p.G + hh) * D;
 #pragma unroll
             for (int e = 0; e < PL; e += 2) {
-                const float2 v = unpack2(__ldg(reinterpret_cast<const uint32_t *>(q + lane * PL + e)), T());
+                const float2 v = unpack2(*reinterpret_cast<const uint32_t *>(q + lane * PL + e), T());
                 x[i][e] = v.x, x[i][e + 1] = v.y;
             }
         }
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     const int i0 = rank * per, mine = max(0, min(per, n - i0));
     const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
     if (ranks > 1)
-        for (int i = tid; i < mine; i += THREADS) keys[i] = (uint32_t)__ldg(trow + i0 + i);
+        for (int i = tid; i < mine; i += THREADS) keys[i] = (uint32_t)trow[i0 + i];
     for (int i = tid; i < 4 * SEL_BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) ends[0] = 0xFFFFFFFFu, ends[1] = 0u;
     __syncthreads();
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
             const int8_t *src = p.codes + u * 2 * D + 32 * tq;
 #pragma unroll
             for (int l = 0; l < LOADS; ++l) ldg256(src + 128 * l, w[e][l]);
-            step[e] = __ldg(p.steps + u);
+            step[e] = p.steps[u];
         }
         float acc[NT][4];
 #pragma unroll

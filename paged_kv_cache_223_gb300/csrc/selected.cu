@@ -89,12 +89,12 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     pdl_wait();
 
     // the length, the first listed blocks and the query rows: on their way together
-    int L = __ldg(p.context_lens + b);
+    int L = p.context_lens[b];
     const int all = p.budget * (p.bs / TILE_TOKENS), step = ranks * W;
     int j = -1, id = -1;
     const auto look_up = [&](int i) {                  // the listed block of tile i and its id
-        j = i < all ? __ldg(p.selected + (int64_t)unit * p.budget + i * TILE_TOKENS / p.bs) : -1;
-        id = j >= 0 && j < p.stride ? __ldg(p.block_tables + b * p.stride + j) : -1;
+        j = i < all ? p.selected[(int64_t)unit * p.budget + i * TILE_TOKENS / p.bs] : -1;
+        id = j >= 0 && j < p.stride ? p.block_tables[b * p.stride + j] : -1;
     };
     look_up(rank * W + warp + lane * step);
 
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 static_cast<const T *>(p.q) + (((int64_t)b * p.q_len + qi) * p.Hq + g * p.G + hh) * D);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                qf[nt][ks][0] = __ldg(q + ks * 8 + (KV8 ? 2 * tq : tq));
-                qf[nt][ks][1] = __ldg(q + ks * 8 + (KV8 ? 2 * tq + 1 : 4 + tq));
+                qf[nt][ks][0] = q[ks * 8 + (KV8 ? 2 * tq : tq)];
+                qf[nt][ks][1] = q[ks * 8 + (KV8 ? 2 * tq + 1 : 4 + tq)];
             }
         } else {
 #pragma unroll
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
+        l[nt][0] = l[nt][1] = -0.f;
 #pragma unroll
         for (int md = 0; md < MT; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
     }
@@ -309,8 +309,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     moved = true;
                 }
                 const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
-                const float p0 = ex2_approx(s0 - ref), p1 = ex2_approx(s1 - ref);
-                l[nt][j] = l[nt][j] * alpha[nt][j] + p0 + p1;
+                // -0 for what is not seen: a sum of nothing keeps its sign, one of weights that are all 0 loses it
+                const float p0 = t0 <= last[nt][j] ? ex2_approx(s0 - ref) : -0.f, p1 = t1 <= last[nt][j] ? ex2_approx(s1 - ref) : -0.f;
+                l[nt][j] = __fadd_rn(__fadd_rn(__fmul_rn(l[nt][j], alpha[nt][j]), p0), p1);
                 sc[nt][j] = p0 * vs0;
                 sc[nt][2 + j] = p1 * vs1;
             }
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     }
     __syncthreads();
     for (int r = tid; r < p.rows; r += ATT_THREADS) {
-        float top = -INFINITY, sum = 0.f;
+        float top = -INFINITY, sum = -0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) top = fmaxf(top, mw[w * RP + r].x);
         const float ref = top == -INFINITY ? 0.f : top;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         for (int w = 0; w < W; ++w) {
             const float f = exp2f(mw[w * RP + r].x - ref);
             fw[r * W + w] = f;
-            sum += f * mw[w * RP + r].y;
+            sum = __fadd_rn(sum, __fmul_rn(f, mw[w * RP + r].y));
         }
         mc[r] = make_float2(top, sum);
     }
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     constexpr int D8 = D / 8;
     const auto store = [&](int r, int d0, const float (&a)[8], float sum) {
         const int qi = r / p.G, h = g * p.G + (r - qi * p.G);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing: zeros
+        const float inv = __float_as_uint(sum) == 0x80000000u ? 0.f : 1.f / sum;   // a row that sees nothing: zeros
         uint4 v;
         v.x = pack2<T>(a[0] * inv, a[1] * inv);
         v.y = pack2<T>(a[2] * inv, a[3] * inv);
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             float4 x[ATT_MAX_RANKS], y[ATT_MAX_RANKS];
 #pragma unroll
             for (int c = 0; c < ATT_MAX_RANKS; ++c) {
-                ms[c] = make_float2(-INFINITY, 0.f);
+                ms[c] = make_float2(-INFINITY, -0.f);
                 x[c] = y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c < ranks) {
                     ms[c] = ld_cluster_float2(map_rank(at_mc + r * 8, c));
@@ -553,14 +554,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     y[c] = ld_cluster_float4(map_rank(at_oc + (r * OS + d0 + 4) * 4, c));
                 }
             }
-            float top = -INFINITY, sum = 0.f, a[8] = {};
+            float top = -INFINITY, sum = -0.f, a[8] = {};
 #pragma unroll
             for (int c = 0; c < ATT_MAX_RANKS; ++c) top = fmaxf(top, ms[c].x);
             const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
             for (int c = 0; c < ATT_MAX_RANKS; ++c) {
                 const float f = exp2f(ms[c].x - ref);
-                sum += f * ms[c].y;
+                sum = __fadd_rn(sum, __fmul_rn(f, ms[c].y));
                 a[0] += f * x[c].x, a[1] += f * x[c].y, a[2] += f * x[c].z, a[3] += f * x[c].w;
                 a[4] += f * y[c].x, a[5] += f * y[c].y, a[6] += f * y[c].z, a[7] += f * y[c].w;
             }

@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(TOK_THREADS) tokens_kernel(const TablesParams 
     extern __shared__ int cu_sm[];
     pdl_trigger();
     pdl_wait();
-    for (int b = threadIdx.x; b <= p.num_seqs; b += TOK_THREADS) cu_sm[b] = __ldg(p.cu_q + b);
+    for (int b = threadIdx.x; b <= p.num_seqs; b += TOK_THREADS) cu_sm[b] = __ldcg(p.cu_q + b);
     __syncthreads();
     write_tokens<4>(p, cu_sm, cu_sm[p.num_seqs], blockIdx.x * TOK_THREADS + threadIdx.x, gridDim.x * TOK_THREADS,
-                 [&](int b) { return __ldg(p.context_lens + b) - (cu_sm[b + 1] - cu_sm[b]); },
-                 [&](int b, int, int j) { return __ldg(p.block_tables + b * p.stride + j); });
+                 [&](int b) { return __ldcg(p.context_lens + b) - (cu_sm[b + 1] - cu_sm[b]); },
+                 [&](int b, int, int j) { return __ldcg(p.block_tables + b * p.stride + j); });
 }
 
 cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream) {

@@ -199,6 +199,28 @@ def test_nothing_listed_and_nothing_seen():
     assert bool((got[0, :3] == 0).all()) and bool((got[0, 3:, :4] != 0).any())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_of_minus_infinity(fp8):
+    """Where some are, their tokens have no weight; where all are, a softmax has no value; where nothing is seen, zeros."""
+    lens = [64, 64, 64]
+    pool, tables, q = make(lens, 4, 1, 128, torch.float16, 16, 2, fp8=fp8)
+    q[..., 0] = 1.0
+    nb = pool.geometry[0]
+    for block in (tables[0, 1], tables[1, 1], tables[1, 3]):
+        i = int(block)
+        if fp8:                                           # one dimension of -1, the others 0 with a NaN scale's stead: -inf
+            pool.k_cache[nb * 16 * 128:].view(torch.float32)[i * 16:(i + 1) * 16] = 3e38
+            pool.k_cache[i * 16 * 128:(i + 1) * 16 * 128] = 0
+            pool.k_cache[i * 16 * 128:(i + 1) * 16 * 128].view(16, 128)[:, 0] = 0xFE      # -448
+        else:
+            pool.k_cache[i, 0, :, 0] = -math.inf
+    sel = i32([[[1, 2]], [[1, 3]], [[-1, -1]]])
+    got = pool.decode_selected(q, sel, tables, i32(lens), 1.0)
+    ref = reference(pool, q, i32([[[2, -1]], [[-1, -1]], [[-1, -1]]]), tables, lens, 1.0)
+    close(got[:1], [x[:1] for x in ref], sel, 16, True, 6.0)
+    assert bool(torch.isnan(got[1]).all()) and bool((got[2] == 0).all())
+
+
 def test_a_block_listed_twice_counts_twice():
     lens = [200]
     pool, tables, q = make(lens, 4, 1, 128, torch.float16, 16)

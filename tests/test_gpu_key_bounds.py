@@ -202,6 +202,14 @@ def test_what_does_not_fit_is_skipped(what):
     check(pool, bounds, (codes, steps))
 
 
+def test_sequences_that_share_rows_have_no_more_work_than_a_call():
+    """Every other sequence of 2000 names all rows: flagged, nothing done."""
+    pool, rows, bounds = make([1000], 1, 64, torch.float16, 16)
+    before, n = bounds.clone(), 2000
+    pool.key_bounds(bounds, i32([0, 1000] * (n // 2) + [0]), i32(rows).repeat(n, 1), i32([1000] * n), 1000)
+    assert pool.check() == pa.PA_ERR_DEVICE_BOUNDS and torch.equal(bounds, before)
+
+
 def test_refusals():
     pool, rows, bounds = make([40], 2, 64, torch.float16, 16)
     L, cu, tables, lens = pa._sparse_lib(), i32([0, 1]), i32(rows), i32([40])
