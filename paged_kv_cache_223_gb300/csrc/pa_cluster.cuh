@@ -53,4 +53,12 @@ __device__ __forceinline__ float4 ld_cluster_float4(uint32_t addr) {
     return v;
 }
 
+// Minimum and maximum into a word of another CTA's shared memory; there behind the cluster's next barrier.
+__device__ __forceinline__ void red_cluster_min(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_cluster_max(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 }  // namespace pa
