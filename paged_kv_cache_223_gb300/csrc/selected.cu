@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     }
 
     int vexp = 0;                                      // FP8: O is in units of 2^vexp
-    bool vset = false;
+    float vlimit = 0.f;                                // 2^(vexp + 5), once a token has set the unit
     bool ok = true;
     int it = 0;
     for (; it < tiles; ++it) {
@@ -265,19 +265,18 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             }
         }
 
-        // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8
+        // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8, which the
+        // warp asks for all its columns at once; the columns' maxima are looked for only then
         const int t0 = pos + gq, t1 = t0 + 8;
         float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
-        float alpha[NT][2];
-        bool moved = false;
         if constexpr (KV8) {
             ks0 = scale_k[gq], ks1 = scale_k[gq + 8], vs0 = scale_v[gq], vs1 = scale_v[gq + 8];
-            // weights times V scales go into the product as fp16: below 2^8 times 2^5 of the largest scale's power of two,
-            // of the tokens that every row sees (the others are added apart)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(t0 < seen_by_all ? __float_as_uint(vs0) & 0x7FFFFFFFu : 0u,
-                                                                    t1 < seen_by_all ? __float_as_uint(vs1) & 0x7FFFFFFFu : 0u));
-            const int e = min(max((int)(top >> 23) - 127, -60), 100);
-            if (top != 0 && (!vset || e > vexp + 4)) {
+            // weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
+            // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
+            const float v0 = t0 < seen_by_all ? fabsf(vs0) : 0.f, v1 = t1 < seen_by_all ? fabsf(vs1) : 0.f;
+            if (__any_sync(0xffffffffu, !(fmaxf(v0, v1) < vlimit) && seen_by_all > pos)) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v0), __float_as_uint(v1)));
+                const int e = min(max((int)(top >> 23) - 127, -60), 100);
                 const float f = ldexpf(1.f, vexp - e);
 #pragma unroll
                 for (int md = 0; md < MT; ++md)
@@ -286,46 +285,51 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
                         for (int k = 0; k < 4; ++k) o[md][nt][k] *= f;
                 vexp = e;
-                vset = true;
+                vlimit = __uint_as_float((uint32_t)(127 + e + 5) << 23);
             }
             const float unit_v = __uint_as_float((uint32_t)(127 - vexp) << 23);   // 2^-vexp
             vs0 *= unit_v, vs1 *= unit_v;
         }
+        bool passed = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // what a masked place holds (a score, a scale) is selected away, not multiplied
-                const float s0 = t0 <= last[nt][j] ? sc[nt][j] * (ks0 * qscale[nt][j]) : -INFINITY;
-                const float s1 = t1 <= last[nt][j] ? sc[nt][2 + j] * (ks1 * qscale[nt][j]) : -INFINITY;
-                float mx = fmaxf(s0, s1);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                alpha[nt][j] = 1.f;
-                if (mx > m[nt][j] + ATT_RESCALE_LOG2) {
-                    alpha[nt][j] = ex2_approx(m[nt][j] - mx);
-                    m[nt][j] = mx;
-                    moved = true;
-                }
-                const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
-                // -0 for what is not seen: a sum of nothing keeps its sign, one of weights that are all 0 loses it
-                const float p0 = t0 <= last[nt][j] ? ex2_approx(s0 - ref) : -0.f, p1 = t1 <= last[nt][j] ? ex2_approx(s1 - ref) : -0.f;
-                l[nt][j] = __fadd_rn(__fadd_rn(__fmul_rn(l[nt][j], alpha[nt][j]), p0), p1);
-                sc[nt][j] = p0 * vs0;
-                sc[nt][2 + j] = p1 * vs1;
+                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (ks0 * qscale[nt][j]) : -INFINITY;
+                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (ks1 * qscale[nt][j]) : -INFINITY;
+                passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
             }
-        if (__any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(sc[nt][j], sc[nt][2 + j]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    if (mx > m[nt][j] + ATT_RESCALE_LOG2) {   // also the first finite one (m = -inf)
+                        const float alpha = ex2_approx(m[nt][j] - mx);
+                        m[nt][j] = mx;
+                        l[nt][j] *= alpha;
 #pragma unroll
-                    for (int md = 0; md < MT; ++md) {
-                        o[md][nt][j] *= alpha[nt][j];
-                        o[md][nt][2 + j] *= alpha[nt][j];
+                        for (int md = 0; md < MT; ++md) o[md][nt][j] *= alpha, o[md][nt][2 + j] *= alpha;
                     }
+                }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+                // -0 for what is not seen: a sum of nothing keeps its sign, one of weights that are all 0 loses it
+                const float p0 = t0 <= last[nt][j] ? ex2_approx(sc[nt][j] - ref) : -0.f;
+                const float p1 = t1 <= last[nt][j] ? ex2_approx(sc[nt][2 + j] - ref) : -0.f;
+                l[nt][j] = __fadd_rn(__fadd_rn(l[nt][j], p0), p1);
+                sc[nt][j] = p0 * vs0;
+                sc[nt][2 + j] = p1 * vs1;
+            }
 
         // The tiles at the end of the context. What lies behind it may be anything: its words of V become 0, its weights are
         // 0 already. So may the value of a token that not every row sees be to the rows that do not: where it is no number
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 const int row = w0 + c % some, chunk = c / some;
                 const uint4 x = *reinterpret_cast<const uint4 *>(vs + (chunk >> 3) * SPAN + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
                 bool is = no_numbers<T, KV8>(x.x) || no_numbers<T, KV8>(x.y) || no_numbers<T, KV8>(x.z) || no_numbers<T, KV8>(x.w);
-                if constexpr (KV8) is |= !vset || !(fabsf(scale_v[row]) < __uint_as_float((uint32_t)(127 + vexp + 5) << 23));
+                if constexpr (KV8) is |= !(fabsf(scale_v[row]) < vlimit);
                 odd |= (uint32_t)is << row;
             }
             odd = __reduce_or_sync(0xffffffffu, odd);
