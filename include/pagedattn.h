@@ -320,9 +320,10 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
  * outside the pool is flagged, its tokens' slots are -1.
  */
 #define PA_TABLES_MAX_SEQS 8192
+#define PA_TABLES_MAX_TOKENS 536870912
 typedef struct pa_tables_args {
     int32_t num_seqs;            /* 0 .. PA_TABLES_MAX_SEQS */
-    int32_t num_tokens;          /* rows of positions and slot_mapping, >= 0 */
+    int32_t num_tokens;          /* rows of positions and slot_mapping, 0 .. PA_TABLES_MAX_TOKENS */
     int32_t block_table_stride;  /* entries of a table row, >= 1 */
     const int32_t *new_lens;     /* device [num_seqs], >= 0 */
     const int32_t *keep_lens;    /* device [num_seqs], >= 0, or NULL */

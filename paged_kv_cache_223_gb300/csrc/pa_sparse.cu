@@ -54,7 +54,7 @@ extern "C" {
 
 pa_status pa_step_tables(pa_pool *pool, const pa_tables_args *a, void *stream) {
     if (!pool || !a || a->num_seqs < 0 || a->num_tokens < 0 || a->block_table_stride < 1) return PA_ERR_INVALID_ARG;
-    if (a->num_seqs > PA_TABLES_MAX_SEQS) return PA_ERR_UNSUPPORTED;
+    if (a->num_seqs > PA_TABLES_MAX_SEQS || a->num_tokens > PA_TABLES_MAX_TOKENS) return PA_ERR_UNSUPPORTED;
     const pa_pool_config &c = pool->cfg;
     const uint64_t n = a->num_seqs, t = a->num_tokens;
     if (!a->cu_q || !a->num_free || !a->free_blocks || (n && (!a->new_lens || !a->context_lens || !a->block_tables)) ||

@@ -8,7 +8,7 @@
 // block i lies at n + F - 1 - i, taken block i comes from n + F - 1 - i. Cutting back what a step took and taking it
 // again therefore gives the same blocks.
 //
-// One cluster does all of it: every CTA makes the sums of all sequences for itself (they are few words), checks them and
+// One cluster does all of it (the tokens of large calls apart): every CTA makes the sums of all sequences for itself (they are few words), checks them and
 // comes to the same verdict, the CTAs share the returned blocks, meet at the cluster's barrier, and share the taken blocks,
 // the tokens and the new lengths. So the lengths, tables and the stack are changed in place by one launch without a
 // workspace, and a call that is refused changes nothing of them.
@@ -24,7 +24,8 @@ namespace {
 
 constexpr int TAB_THREADS = 512;
 constexpr int TOK_THREADS = 256;
-constexpr int TAB_MAX_TOKENS = 32768;                   // more of them get a kernel of their own
+// More tokens get a kernel of their own (65536: 10.3 us by the cluster's eight CTAs, 7.9 by two kernels; 32768: 6.8 and 7.1).
+constexpr int TAB_MAX_TOKENS = 32768;
 
 struct Sums {
     long long tokens, back, taken;
@@ -50,8 +51,9 @@ __device__ __forceinline__ int owner(const int *start, int n, int i) {
     return lo;
 }
 
-// Positions and slots of the call's tokens, N at a time: four share the search and, as a rule, the block; in a call that has
-// threads for all its tokens one by one has the shorter chain (257 sequences of a few tokens: 6.0 us, four at a time 7.0).
+// Positions and slots of the call's tokens, N at a time: four share the search and, as a rule, the block; a call that has at most
+// two rounds of threads for all its tokens one by one has the shorter chain (257 sequences of a few tokens in one CTA: 6.0 us,
+// four at a time 7.0; 8192 tokens in eight: 6.3, and 8.0 with four rounds one by one).
 // block_of(b, kept, j): the id of the sequence's block j; kept_of(b): its tokens before the new ones.
 template <int N, typename Kept, typename Block>
 __device__ __forceinline__ void write_tokens(const TablesParams &p, const int *cu, int tokens, int first, int step, Kept kept_of,
@@ -226,13 +228,14 @@ __global__ void __launch_bounds__(TOK_THREADS) tokens_kernel(const TablesParams 
 cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream) {
     const size_t smem = (size_t)(4 * p.num_seqs + 3) * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     p.vectors = (reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
     p.tokens_apart = p.num_tokens > TAB_MAX_TOKENS;
-    // CTAs of the cluster: one for each two rounds of four tokens per thread
-    int ranks = 1;
-    while (ranks < 16 && p.num_tokens > ranks * TAB_THREADS * 8) ranks *= 2;
+    // CTAs of the cluster: eight even for small steps, whose lengths are known on the device only (257 sequences: 5.6 us, a
+    // single CTA 6.5; one request 3.3 and 3.9), 16 in front of the tokens' kernel (2000 prompts: 14.0 us, eight 15.5)
+    const int ranks = p.tokens_apart ? 16 : 8;
+    if (ranks > 8) e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     e = launch_clusters(tables_kernel, ranks, TAB_THREADS, smem, ranks, stream, p);
     if (e != cudaSuccess || !p.tokens_apart) return e;
     const int ctas = std::min((p.num_tokens + 4 * TOK_THREADS - 1) / (4 * TOK_THREADS), 4 * sm_count);

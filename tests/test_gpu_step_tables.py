@@ -147,6 +147,41 @@ def test_an_id_outside_the_pool_is_flagged():
     assert slots.tolist()[14:] == [-1] * 7
 
 
+@pytest.mark.parametrize("spare", [0, 1, 2, 3, 40000])
+def test_many_tokens(spare):
+    """Above 32768 rows the tokens are written by a kernel of their own; refused steps and wrong ids there too."""
+    new = [12345, 0, 1, 20431, 7]
+    s = State([3, 100, 0, 17, 16], 1400, 2100, 16)
+    s.t["block_tables"][1, 0] = 2100                      # not this step's
+    s.rows[1][0] = 2100
+    got = s.call(new, sum(new) + spare)
+    s.check(got, s.expect(new, sum(new) + spare))
+    assert s.pool.check() == pa.PA_OK
+    before = {k: v.clone() for k, v in s.t.items()}
+    for bad, status in (([-1, 0, 0, 0, 0], pa.PA_ERR_DEVICE_BOUNDS), ([0, 0, 0, 0, 2000 * 8], pa.PA_ERR_OOM)):
+        cu, pos, slots = s.call(bad, 40001)
+        assert s.pool.check() == status and cu.tolist() == [0] * 6
+        assert not bool(pos.any()) and bool((slots == -1).all()) and all(torch.equal(before[k], v) for k, v in s.t.items())
+    cu, pos, slots = s.call([0, 5, 0, 0, 0], 40000)       # behind 100 tokens: a block that is in order
+    assert s.pool.check() == pa.PA_OK and slots[:5].tolist() == [s.rows[1][6] * 16 + i for i in range(4, 9)]
+    s.t["block_tables"][1, 6] = -3
+    cu, pos, slots = s.call([0, 5, 0, 0, 0], 40000, keep=[2 ** 30, 100, 2 ** 30, 2 ** 30, 2 ** 30])
+    assert s.pool.check() == pa.PA_ERR_DEVICE_BOUNDS and slots[:5].tolist() == [-1] * 5 and pos[:5].tolist() == list(range(100, 105))
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_outputs_off_the_vectors(off):
+    new = [700, 3, 9000]
+    s = State([3, 100, 0], 700, 900, 16)
+    buf = torch.full((9800,), -5, dtype=torch.int32, device=DEV)
+    buf64 = torch.full((9800,), -5, dtype=torch.int64, device=DEV)
+    n = sum(new) + 5
+    got = s.call(new, n, positions=buf[off:off + n], slot_mapping=buf64[off:off + n])
+    s.check(got, s.expect(new, n))
+    for b in (buf, buf64):
+        assert bool((b[:off] == -5).all()) and bool((b[off + n:] == -5).all())
+
+
 def test_no_sequences_and_no_tokens():
     s = State([], 3, 4, 16)
     cu, pos, slots = s.call([], 5)
@@ -193,8 +228,9 @@ def test_refusals():
     for c in changes:
         a = pa.PaTablesArgs(**{**good, **c})
         assert L.pa_step_tables(s.pool.handle, C.byref(a), None) == pa.PA_ERR_INVALID_ARG, c
-    a = pa.PaTablesArgs(**{**good, "num_seqs": 8193})
-    assert L.pa_step_tables(s.pool.handle, C.byref(a), None) == pa.PA_ERR_UNSUPPORTED
+    for c in (dict(num_seqs=8193), dict(num_tokens=2 ** 29 + 1), dict(num_tokens=2 ** 31 - 1)):
+        a = pa.PaTablesArgs(**{**good, **c})
+        assert L.pa_step_tables(s.pool.handle, C.byref(a), None) == pa.PA_ERR_UNSUPPORTED
     call = lambda **kw: s.pool.step_tables(**{**dict(new_lens=new, num_tokens=8), **t, **kw})  # noqa: E731
     for kw in (dict(new_lens=new.long()), dict(new_lens=new.cpu()), dict(new_lens=new[:1]), dict(num_tokens=-1),
                dict(cu_q=cu[:2]), dict(positions=pos[:7]), dict(slot_mapping=pos), dict(free_blocks=t["free_blocks"][:5]),

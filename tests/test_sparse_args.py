@@ -35,3 +35,11 @@ def test_the_arguments_are_the_headers(pa):
     names = re.findall(r"(\w+);", body)
     assert names == [n for n, _ in pa.PaTablesArgs._fields_]
     assert [C.sizeof(t) for _, t in pa.PaTablesArgs._fields_] == [4] * 3 + [8] * 9
+
+
+def test_the_limits_are_the_headers(pa):
+    """Beside the calls' own tests: the values that they use."""
+    text = open(os.path.join(_build.INCLUDE, "pagedattn.h")).read()
+    limits = {n: int(v) for n, v in re.findall(r"#define (PA_TABLES_\w+|PA_SELECT_\w+) (\d+)\n", text)}
+    assert limits == dict(PA_TABLES_MAX_SEQS=8192, PA_TABLES_MAX_TOKENS=2 ** 29, PA_SELECT_MAX_BUDGET=4096,
+                          PA_SELECT_MAX_BLOCKS=262144)
