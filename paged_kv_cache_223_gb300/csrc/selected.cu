@@ -25,6 +25,7 @@ constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_MAX_RANKS = 8;
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
 
+// Copies of a warp's pipeline in flight: two of 8 KB where three CTAs share an SM (192 KB in flight), else three.
 __host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
 // CTAs per SM: by shared memory with one column of eight rows, by registers with more. FP8 pools with 16 rows at three CTAs
 // (168 registers, spills) lost as much as they won: 19 sequences of a verify 18.9 -> 23.0 us, 64 of 2048 tokens 68.2 -> 67.1.
@@ -50,6 +51,13 @@ __device__ __forceinline__ bool no_numbers(uint32_t x) {
     if constexpr (KV8) return (__vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0;
     constexpr uint32_t exp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
     return (x & exp) == exp || ((x >> 16) & exp) == exp;
+}
+
+// Two 16-bit numbers of a register as floats (a bf16 is the top half of one).
+template <typename M>
+__device__ __forceinline__ float2 unpacked(uint32_t x) {
+    if constexpr (std::is_same<M, __half>::value) return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ float value16(uint16_t w, __half) { return __half2float(__ushort_as_half(w)); }
@@ -396,9 +404,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 }
         }
 
-        // P^T as the B operand, in V's type; bf16 has too few bits for one part, so it is carried as two (the nearest bf16
-        // and what is left of it), fp16's eleven do alone
-        constexpr bool TWO = std::is_same<M, __nv_bfloat16>::value;
+        // P^T as the B operand, in V's type. In 16-bit pools as two parts (the nearest number and what is left of it): bf16's
+        // eight bits would not do, and fp16's eleven alone made the error 1.3 times the last rounding's (64 sequences of 2048
+        // tokens 84.5 -> 85.8 us for the second part). FP8 pools, whose codes have four bits, take one part of fp16 (the
+        // second one 18.1 -> 19.7 us for 19 sequences of 16 rows, 109 -> 126 for 64 of 32).
+        constexpr bool TWO = !KV8;
         uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -407,8 +417,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 const float x = sc[nt][2 * k], y = sc[nt][2 * k + 1];
                 const uint32_t hi = pack2<M>(x, y);
                 ph[nt][k] = movmatrix_trans(hi);
-                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u)))
-                                : 0u;
+                const float2 near = unpacked<M>(hi);
+                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>(x - near.x, y - near.y)) : 0u;
             }
 
         // O^T += V^T P^T

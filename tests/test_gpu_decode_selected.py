@@ -1,9 +1,9 @@
 """decode_selected (pa_decode_selected) against attention over the listed blocks in 64 bits.
 
 Tolerance of an output, relative to sum p |v| but for the last rounding (eps / 2 of the value):
-- weights go into the product as fp16 (2^-11) or as two bf16 (2^-16); fp16 weights below 2^-14 lose up to 2^-25 each, of a
-  sum of weights that is at least 1 (FP8: times the V scale, in units of a power of two not above the largest scale):
-  N 2^-25 max |v|;
+- weights go into the product as two parts of 16 bits (2^-16 for bf16, less for fp16), in FP8 pools as one of fp16 (2^-11);
+  parts of fp16 below 2^-14 lose up to 2^-25 each, of a sum of weights that is at least 1 (FP8: times the V scale, in
+  units of a power of two not above the largest scale): N 2^-25 max |v|;
 - a score is a fp32 sum of products whose sizes add up to `big` (in units of e): 2^-20 big, twice (score and reference);
 - exponentials and sums of 32 bits: 2^-20;
 - a product's accumulator may drop the last bit of each of its N / 16 additions: N 2^-26.
@@ -80,12 +80,12 @@ def reference(pool, q, selected, tables, lens, scale, k_cache=None, v_cache=None
                   reader(pool, pool.v_cache if v_cache is None else v_cache, tables), selected, lens, scale)
 
 
-def close(got, ref, selected, bs, half_weights, vmax):
+def close(got, ref, selected, bs, fp8, vmax):
     out, mag, big = ref
     dt = got.dtype
     n = selected.shape[-1] * bs
-    rel = (2.0 ** -11 if half_weights else 2.0 ** -16) + big[..., None] * 2.0 ** -19 + 2.0 ** -20 + n * 2.0 ** -26
-    tol = out.abs() * torch.finfo(dt).eps / 2 + mag * rel + (n * 2.0 ** -25 * vmax if half_weights else 0)
+    rel = (2.0 ** -11 if fp8 else 2.0 ** -16) + big[..., None] * 2.0 ** -19 + 2.0 ** -20 + n * 2.0 ** -26
+    tol = out.abs() * torch.finfo(dt).eps / 2 + mag * rel + (n * 2.0 ** -25 * vmax if fp8 or dt == torch.float16 else 0)
     tol = tol + torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
     err = (got.double() - out).abs()
     assert bool((err <= tol).all()), f"{int((~(err <= tol)).sum())} outside, worst {float((err - tol).max()):.3g}"
@@ -97,7 +97,7 @@ def run(pool, tables, q, lens, selected, scale=None, vmax=None):
     got = pool.decode_selected(q, selected, tables, i32(lens), scale)
     fp8 = pool.kv_format == pa.PA_KV_FP8_E4M3
     vmax = vmax or (6.0 if fp8 else float(pool.v_cache.float().nan_to_num(0.0, 0.0, 0.0).abs().max()))
-    close(got, reference(pool, q, selected, tables, lens, scale), selected, bs, fp8 or pool.dtype == torch.float16, vmax)
+    close(got, reference(pool, q, selected, tables, lens, scale), selected, bs, fp8, vmax)
     return got
 
 
@@ -217,7 +217,7 @@ def test_scores_of_minus_infinity(fp8):
     sel = i32([[[1, 2]], [[1, 3]], [[-1, -1]]])
     got = pool.decode_selected(q, sel, tables, i32(lens), 1.0)
     ref = reference(pool, q, i32([[[2, -1]], [[-1, -1]], [[-1, -1]]]), tables, lens, 1.0)
-    close(got[:1], [x[:1] for x in ref], sel, 16, True, 6.0)
+    close(got[:1], [x[:1] for x in ref], sel, 16, fp8, 6.0)
     assert bool(torch.isnan(got[1]).all()) and bool((got[2] == 0).all())
 
 
@@ -339,7 +339,7 @@ def test_other_caches():
     k, v = torch.randn_like(pool.k_cache), torch.randn_like(pool.v_cache)
     sel = pick(lens, 2, 16, 4, 11)
     got = pool.decode_selected(q, sel, tables, i32(lens), 0.125, k_cache=k, v_cache=v)
-    close(got, reference(pool, q, sel, tables, lens, 0.125, k, v), sel, 16, True, 6.0)
+    close(got, reference(pool, q, sel, tables, lens, 0.125, k, v), sel, 16, False, 6.0)
 
 
 def test_refusals():
