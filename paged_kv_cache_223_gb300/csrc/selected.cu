@@ -10,6 +10,11 @@
 // and O^T += V^T P^T as warp-level products with the query rows as columns, softmax in fp32 between them. The states of a
 // CTA's warps are joined in its shared memory, those of the cluster's CTAs through each other's, each CTA writing a share
 // of the outputs: one launch, no workspace, a fixed order.
+//
+// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 84 to 86 us, 6.3 to 6.4 TB/s, 0.93
+// to 0.95 of the copy rate; one sequence of 64 blocks 7.4 us (in a graph 5.9): launch 2, lookups 1.5, two tiles a warp 1, joins 2;
+// 19 sequences of 50 blocks of 32 in an FP8 pool, 16 query rows: 18.1 us, bound by the latency of a warp's chain per tile
+// at eight warps an SM.
 #include <type_traits>
 
 #include "pa_cluster.cuh"
@@ -193,11 +198,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^-(e - 127 - 14): the largest magnitude below 2^15; rows of at most 2^15 stay as they are
-            const int e = (int)(top >> 7);
-            const bool large = e > 141 && e < 255;
-            const float down = large ? __uint_as_float((uint32_t)(127 + 141 - e) << 23) : 1.f;
-            const float up = large ? __uint_as_float((uint32_t)(127 + e - 141) << 23) : 1.f;
+            // times 2^(141 - e): the largest magnitude between 2^14 and 2^15, so that small ones keep their bits too
+            const int e = min(max((int)(top >> 7), 15), 254);
+            const float down = __uint_as_float((uint32_t)(127 + 141 - e) << 23), up = __uint_as_float((uint32_t)(127 + e - 141) << 23);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

@@ -169,6 +169,19 @@ def test_fp8_bf16_queries_beyond_fp16():
     run(pool, tables, q, lens, pick(lens, 2, 16, 8, 4))
 
 
+def test_fp8_small_bf16_queries():
+    """Queries below fp16's normal numbers against large keys."""
+    lens = [300]
+    pool, tables, q = make(lens, 8, 2, 128, torch.bfloat16, 16, 2, fp8=True)
+    q *= 2.0 ** -22
+    n = pool.geometry[0] * 2 * 16 * 128
+    pool.k_cache[n:].view(torch.float32).mul_(2.0 ** 22)
+    run(pool, tables, q, lens, pick(lens, 2, 16, 8, 4))
+    q *= 2.0 ** -90
+    pool.k_cache[n:].view(torch.float32).mul_(2.0 ** 90)
+    run(pool, tables, q, lens, pick(lens, 2, 16, 8, 4))
+
+
 def test_all_blocks_listed_is_decode():
     lens = [777, 64, 1]
     pool, tables, q = make(lens, 32, 8, 128, torch.bfloat16, 16)
