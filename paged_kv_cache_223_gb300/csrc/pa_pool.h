@@ -27,6 +27,7 @@ struct pa_pool {
     cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
     std::mutex mu;
     std::unordered_map<const void *, CUtensorMap> maps;
+    std::unordered_map<const void *, CUtensorMap> group_maps;   // the same caches by groups of eight rows
 };
 
 namespace pa {
@@ -51,5 +52,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 // The map of one of the pool's caches for copies of 16 token rows, kept per cache address.
 pa_status tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out);
+// One of a 16-bit pool's caches for copies of 16 token rows at once, as two groups of eight rows by halves of 64 dimensions.
+pa_status group_map(pa_pool *pool, const void *cache, CUtensorMap *out);
 
 }  // namespace pa

@@ -8,6 +8,31 @@
 
 using namespace pa;
 
+pa_status pa::group_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
+    std::lock_guard<std::mutex> lk(pool->mu);
+    const auto it = pool->group_maps.find(cache);
+    if (it != pool->group_maps.end()) {
+        *out = it->second;
+        return PA_OK;
+    }
+    const auto fn = encode_fn();
+    if (!fn) return PA_ERR_CUDA;
+    const pa_pool_config &c = pool->cfg;
+    const cuuint64_t row = (cuuint64_t)c.head_dim * 2, halves = (cuuint64_t)c.head_dim / 64;
+    const cuuint64_t dims[4] = {64, 8, halves, (cuuint64_t)c.num_blocks * c.num_kv_heads * c.block_size / 8};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)halves, TILE_TOKENS / 8}, estr[4] = {1, 1, 1, 1};
+    CUtensorMap m;
+    if (fn(&m, c.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+           const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PA_ERR_CUDA;
+    if (pool->group_maps.size() > 4096) pool->group_maps.clear();
+    pool->group_maps.emplace(cache, m);
+    *out = m;
+    return PA_OK;
+}
+
 namespace {
 
 constexpr int64_t MAX_CONTEXT = (int64_t)1 << 29;
@@ -239,7 +264,8 @@ pa_status pa_decode_selected(pa_pool *pool, const void *q, const void *k_cache, 
     DeviceGuard g(c.device);
     if (!g.ok) return PA_ERR_CUDA;
     CUtensorMap tmk, tmv;
-    if ((st = tensor_map(pool, k_cache, &tmk)) != PA_OK || (st = tensor_map(pool, v_cache, &tmv)) != PA_OK) return st;
+    const auto map = p.k_scales ? tensor_map : group_map;
+    if ((st = map(pool, k_cache, &tmk)) != PA_OK || (st = map(pool, v_cache, &tmv)) != PA_OK) return st;
     return launched(launch_selected(p, c.dtype, c.head_dim, tmk, tmv, pool->sm_count, static_cast<cudaStream_t>(stream)));
 }
 

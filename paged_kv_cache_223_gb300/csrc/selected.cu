@@ -11,10 +11,10 @@
 // CTA's warps are joined in its shared memory, those of the cluster's CTAs through each other's, each CTA writing a share
 // of the outputs: one launch, no workspace, a fixed order.
 //
-// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 84 to 86 us, 6.3 to 6.4 TB/s, 0.93
-// to 0.95 of the copy rate; one sequence of 64 blocks 7.4 us (in a graph 5.9): launch 2, lookups 1.5, two tiles a warp 1, joins 2;
-// 19 sequences of 50 blocks of 32 in an FP8 pool, 16 query rows: 18.1 us, bound by the latency of a warp's chain per tile
-// at eight warps an SM.
+// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 79 us, 6.8 TB/s, the copy rate; one
+// sequence of 64 blocks 6.7 us (in a graph 5.8): launch 2, lookups 1.5, two tiles a warp 1, joins 2; 19 sequences of 50 blocks
+// of 32 in an FP8 pool, 16 query rows: 17.5 us, bound by a warp's chain per tile (scores 300 cycles, softmax 360, weights 90,
+// values and the next copies 500) at eight warps an SM.
 #include <type_traits>
 
 #include "pa_cluster.cuh"
@@ -30,24 +30,40 @@ constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_MAX_RANKS = 8;
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
 
-// Copies of a warp's pipeline in flight: two of 8 KB where three CTAs share an SM (192 KB in flight), else three.
-__host__ __device__ constexpr int att_stages(bool kv8, int nt) { return kv8 ? 3 : nt == 1 ? 2 : 3; }
-// CTAs per SM: by shared memory with one column of eight rows, by registers with more. FP8 pools with 16 rows at three CTAs
-// (168 registers, spills) lost as much as they won: 19 sequences of a verify 18.9 -> 23.0 us, 64 of 2048 tokens 68.2 -> 67.1.
-__host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : !kv8 && nt == 1 ? 3 : 2; }
+// Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
+// 17.5 -> 17.7 us, 64 of 2048 tokens 44 -> 46), four CTAs with one column of eight rows, else two by registers (16 rows at
+// three CTAs, with spills: 18.9 -> 23.0). 16-bit pools, 8 KB: three copies, two CTAs. Three CTAs of two copies each keep as many
+// bytes in flight: 64 sequences of 128 blocks 86 us instead of 79.
+__host__ __device__ constexpr int att_stages(bool kv8) { return kv8 ? 2 : 3; }
+__host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : 2; }
 __host__ __device__ constexpr int att_tile_bytes(int D, bool kv8) { return TILE_TOKENS * (kv8 ? 128 : 2 * D); }
-__host__ __device__ constexpr int att_scale_bytes(bool kv8, int nt) {
-    return kv8 ? (ATT_WARPS * att_stages(kv8, nt) * 2 * TILE_TOKENS * 4 + 1023) / 1024 * 1024 : 0;
-}
-__host__ __device__ constexpr int att_ring_bytes(int D, bool kv8, int nt) {
-    return ATT_WARPS * att_stages(kv8, nt) * 2 * att_tile_bytes(D, kv8) + att_scale_bytes(kv8, nt);
+__host__ __device__ constexpr int att_ring_bytes(int D, bool kv8) {
+    return ATT_WARPS * att_stages(kv8) * 2 * att_tile_bytes(D, kv8);
 }
 // states of the warps [W][RP][D + 4] and (max, sum) [W][RP], the CTA's own [RP][D + 4] and (max, sum) [RP], factors [RP][W]
 __host__ __device__ constexpr int att_join_bytes(int D, int nt) {
     return 4 * nt * 8 * ((ATT_WARPS + 1) * (D + 4) + (ATT_WARPS + 1) * 2 + ATT_WARPS);
 }
 __host__ __device__ constexpr int att_body_bytes(int D, bool kv8, int nt) {
-    return (att_ring_bytes(D, kv8, nt) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8, nt) : att_join_bytes(D, nt)) + 15 & ~15;
+    return (att_ring_bytes(D, kv8) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8) : att_join_bytes(D, nt)) + 15 & ~15;
+}
+
+// Where 16 bytes (chunk c of a token's row r) of a tile lie: FP8 rows of 128 bytes; 16-bit ones in groups of eight rows, by
+// halves of 64 dimensions; swizzled by the copy.
+template <int D, bool KV8>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+    if constexpr (KV8) return r * 128 + ((c ^ (r & 7)) << 4);
+    return ((r >> 3) * (D / 64) + (c >> 3)) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// A tile of 16 rows as two groups of eight, the dimension halves and 64 dimensions: one copy, which a lane takes half as long
+// to issue as two of 64 dimensions (a warp waits for its lane: 250 cycles a tile of K and V by four copies).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int32_t group, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(bar), "l"(policy)
+        : "memory");
 }
 
 // Does a word of V hold a NaN or an infinity (E4M3 has NaN alone, all ones but for the sign)?
@@ -76,8 +92,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     const SelectedParams p) {
     static_assert(!KV8 || D == 128, "FP8 pools are built for head_dim 128");
     using M = typename std::conditional<KV8, __half, T>::type;   // E4M3 codes are exact in fp16
-    constexpr int W = ATT_WARPS, STAGES = att_stages(KV8, NT);
-    constexpr int TILE = att_tile_bytes(D, KV8), STAGE = 2 * TILE, SPAN = TILE_TOKENS * 128;   // 128-byte swizzle spans
+    constexpr int W = ATT_WARPS, STAGES = att_stages(KV8);
+    constexpr int TILE = att_tile_bytes(D, KV8), STAGE = 2 * TILE;
     constexpr int KS = D / 16, MT = D / 16, RP = NT * 8, OS = D + 4;
 
     extern __shared__ uint8_t smem_raw[];
@@ -160,25 +176,17 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     __syncwarp();
 
     const uint32_t ring_u32 = base_u32 + warp * STAGES * STAGE;
-    const uint32_t scales_u32 = base_u32 + W * STAGES * STAGE + warp * STAGES * 2 * TILE_TOKENS * 4;   // FP8 only
     const uint64_t policy = l2_policy_evict_first();
     auto issue = [&](int it) {
         const int s = it % STAGES, row = list[it].x;
         const uint32_t bar = bars_u32 + (warp * STAGES + s) * 8, dst = ring_u32 + s * STAGE;
+        mbar_arrive_expect_tx(bar, STAGE);
         if constexpr (KV8) {
-            const uint32_t sdst = scales_u32 + s * 2 * TILE_TOKENS * 4;
-            mbar_arrive_expect_tx(bar, STAGE + 2 * TILE_TOKENS * 4);
             tma_load_2d(dst, &tmk, 0, row, bar, policy);
             tma_load_2d(dst + TILE, &tmv, 0, row, bar, policy);
-            bulk_load(sdst, p.k_scales + row, TILE_TOKENS * 4, bar, policy);
-            bulk_load(sdst + TILE_TOKENS * 4, p.v_scales + row, TILE_TOKENS * 4, bar, policy);
         } else {
-            mbar_arrive_expect_tx(bar, STAGE);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                tma_load_2d(dst + h * SPAN, &tmk, h * 64, row, bar, policy);
-                tma_load_2d(dst + TILE + h * SPAN, &tmv, h * 64, row, bar, policy);
-            }
+            tma_load_4d(dst, &tmk, row / 8, bar, policy);
+            tma_load_4d(dst + TILE, &tmv, row / 8, bar, policy);
         }
     };
     int issued = min(tiles, STAGES);
@@ -231,6 +239,13 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 
     int vexp = 0;                                      // FP8: O is in units of 2^vexp
     float vlimit = 0.f;                                // 2^(vexp + 5), once a token has set the unit
+    // FP8: a tile's scales are loaded while the tile before it is worked on
+    const auto scales_of = [&](int i) {
+        const int row = list[i].x + gq;
+        return make_float4(p.k_scales[row], p.k_scales[row + 8], p.v_scales[row], p.v_scales[row + 8]);
+    };
+    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (KV8 && tiles > 0) ahead = scales_of(0);
     bool ok = true;
     int it = 0;
     for (; it < tiles; ++it) {
@@ -241,8 +256,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         }
         const int pos = list[it].y;
         const uint32_t kb = ring_u32 + s * STAGE, vb = kb + TILE;
-        const float *scale_k = reinterpret_cast<const float *>(smem + (scales_u32 - base_u32) + s * 2 * TILE_TOKENS * 4);
-        const float *scale_v = scale_k + TILE_TOKENS;
+        float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);   // FP8: of K and V of the tokens gq and gq + 8
+        if constexpr (KV8) {
+            scale = ahead;
+            if (it + 1 < tiles) ahead = scales_of(it + 1);
+        }
 
         // S^T = K Q^T: 16 keys, 8 NT query rows
         float sc[NT][4];
@@ -254,7 +272,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             for (int kp = 0; kp < KS / 2; ++kp) {
                 const int chunk = kp * 2 + (lane >> 4);
                 uint32_t r0, r1, r2, r3;
-                ldsm_x4(kb + krow * 128 + ((chunk ^ (krow & 7)) << 4), r0, r1, r2, r3);
+                ldsm_x4(kb + tile_at<D, KV8>(krow, chunk), r0, r1, r2, r3);
                 const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)r0), a2 = e4m3x2_to_f16x2((uint16_t)(r0 >> 16));
                 const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)r1), a3 = e4m3x2_to_f16x2((uint16_t)(r1 >> 16));
                 const uint32_t c0 = e4m3x2_to_f16x2((uint16_t)r2), c2 = e4m3x2_to_f16x2((uint16_t)(r2 >> 16));
@@ -270,7 +288,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             for (int ks = 0; ks < KS; ++ks) {
                 const int chunk = ks * 2 + (lane >> 4);
                 uint32_t a0, a1, a2, a3;
-                ldsm_x4(kb + (chunk >> 3) * SPAN + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), a0, a1, a2, a3);
+                ldsm_x4(kb + tile_at<D, KV8>(krow, chunk), a0, a1, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_16816<M>(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
             }
@@ -279,9 +297,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8, which the
         // warp asks for all its columns at once; the columns' maxima are looked for only then
         const int t0 = pos + gq, t1 = t0 + 8;
-        float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
+        float vs0 = scale.z, vs1 = scale.w;
         if constexpr (KV8) {
-            ks0 = scale_k[gq], ks1 = scale_k[gq + 8], vs0 = scale_v[gq], vs1 = scale_v[gq + 8];
             // weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
             // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
             const float v0 = t0 < seen_by_all ? fabsf(vs0) : 0.f, v1 = t1 < seen_by_all ? fabsf(vs1) : 0.f;
@@ -307,8 +324,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // what a masked place holds (a score, a scale) is selected away, not multiplied
-                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (ks0 * qscale[nt][j]) : -INFINITY;
-                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (ks1 * qscale[nt][j]) : -INFINITY;
+                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (scale.x * qscale[nt][j]) : -INFINITY;
+                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (scale.y * qscale[nt][j]) : -INFINITY;
                 passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
             }
         if (__any_sync(0xffffffffu, passed)) {
@@ -353,10 +370,13 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             uint32_t odd = 0;                          // such tokens
             for (int c = lane; c < some * (TILE / TILE_TOKENS / 16); c += 32) {
                 const int row = w0 + c % some, chunk = c / some;
-                const uint4 x = *reinterpret_cast<const uint4 *>(vs + (chunk >> 3) * SPAN + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-                bool is = no_numbers<T, KV8>(x.x) || no_numbers<T, KV8>(x.y) || no_numbers<T, KV8>(x.z) || no_numbers<T, KV8>(x.w);
-                if constexpr (KV8) is |= !(fabsf(scale_v[row]) < vlimit);
+                const uint4 x = *reinterpret_cast<const uint4 *>(vs + tile_at<D, KV8>(row, chunk));
+                const bool is = no_numbers<T, KV8>(x.x) || no_numbers<T, KV8>(x.y) || no_numbers<T, KV8>(x.z) || no_numbers<T, KV8>(x.w);
                 odd |= (uint32_t)is << row;
+            }
+            if constexpr (KV8) {
+                if (gq >= w0 && gq < w1) odd |= (uint32_t)!(fabsf(scale.z) < vlimit) << gq;
+                if (gq + 8 >= w0 && gq + 8 < w1) odd |= (uint32_t)!(fabsf(scale.w) < vlimit) << (gq + 8);
             }
             odd = __reduce_or_sync(0xffffffffu, odd);
             for (uint32_t left = odd; left; left &= left - 1) {
@@ -376,12 +396,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                         float v;
                         if constexpr (KV8) {
                             const int dim = md * 16 + 2 * gq + e;
-                            const uint32_t h2 = e4m3x2_to_f16x2(vs[kk * 128 + (((dim >> 4) ^ (kk & 7)) << 4) + (dim & 15)]);
+                            const uint32_t h2 = e4m3x2_to_f16x2(vs[tile_at<D, KV8>(kk, dim >> 4) + (dim & 15)]);
                             v = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
                         } else {
-                            const int dim = md * 16 + gq + 8 * e, c = dim >> 3;
-                            v = value16(*reinterpret_cast<const uint16_t *>(vs + (c >> 3) * SPAN + kk * 128 +
-                                                                            (((c & 7) ^ (kk & 7)) << 4) + (dim & 7) * 2), T());
+                            const int dim = md * 16 + gq + 8 * e;
+                            v = value16(*reinterpret_cast<const uint16_t *>(vs + tile_at<D, KV8>(kk, dim >> 3) + (dim & 7) * 2), T());
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -393,8 +412,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             __syncwarp();
             const uint32_t gone = odd | (w1 < TILE_TOKENS ? 0xFFFFu << w1 : 0u);
             for (int c = lane; c < TILE / 16; c += 32) {
-                const int row = (c >> 3) & (TILE_TOKENS - 1);
-                if (gone >> row & 1u) *reinterpret_cast<uint4 *>(vs + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const int row = c % TILE_TOKENS;
+                if (gone >> row & 1u)
+                    *reinterpret_cast<uint4 *>(vs + tile_at<D, KV8>(row, c / TILE_TOKENS)) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();                  // before the copy that comes over these words
             __syncwarp();
@@ -432,7 +452,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             for (int mp = 0; mp < MT / 2; ++mp) {
                 const int chunk = mp * 2 + (lane >> 4);
                 uint32_t r[4];
-                ldsm_x4_trans(vb + vrow * 128 + ((chunk ^ (vrow & 7)) << 4), r[0], r[1], r[2], r[3]);
+                ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), r[0], r[1], r[2], r[3]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t lo = r[2 * h], hi = r[2 * h + 1];
@@ -450,7 +470,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             for (int md = 0; md < MT; ++md) {
                 const int chunk = md * 2 + ((lane >> 3) & 1);
                 uint32_t a0, a1, a2, a3;
-                ldsm_x4_trans(vb + (chunk >> 3) * SPAN + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), a0, a1, a2, a3);
+                ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), a0, a1, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_16816<M>(o[md][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
@@ -595,7 +615,7 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
     const int tiles = p.budget * (p.bs / TILE_TOKENS), nt = (p.rows + 7) / 8;
     // CTAs of a cluster. A round of resident CTAs lasts as long as a warp's tiles and about three more for the start and the
     // joining of its warps, another three where a cluster joins. Of 130 shapes (1 to 2048 units, lists of 16 to 1024 blocks,
-    // 4 to 32 rows, both formats) this picks the best of 1, 2, 4, 8 but for 1.2% on average, 24% at most; "at least two CTAs
+    // 4 to 32 rows, both formats) this picks the best of 1, 2, 4, 8 but for 0.8% on average, 20% at most; "at least two CTAs
     // per SM" lost 8.5% and up to 83% (128 units, 16 blocks: 6.1 us as single CTAs, 11.0 as clusters of four).
     const int64_t slots = (int64_t)att_ctas(KV8, nt) * sm_count;
     int ranks = 1;
@@ -606,7 +626,7 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
     }
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
-        const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8, n) * 8 + 16 +
+        const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8) * 8 + 16 +
                             (size_t)ATT_WARPS * p.warp_tiles * 8;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e != cudaSuccess
