@@ -295,14 +295,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         }
 
         // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8, which the
-        // warp asks for all its columns at once; the columns' maxima are looked for only then
+        // warp asks for all its columns (and the V scales) at once; the columns' maxima are looked for only then
         const int t0 = pos + gq, t1 = t0 + 8;
-        float vs0 = scale.z, vs1 = scale.w;
-        if constexpr (KV8) {
-            // weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
-            // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
-            const float v0 = t0 < seen_by_all ? fabsf(vs0) : 0.f, v1 = t1 < seen_by_all ? fabsf(vs1) : 0.f;
-            if (__any_sync(0xffffffffu, !(fmaxf(v0, v1) < vlimit) && seen_by_all > pos)) {
+        // FP8: weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
+        // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
+        const float v0 = t0 < seen_by_all ? fabsf(scale.z) : 0.f, v1 = t1 < seen_by_all ? fabsf(scale.w) : 0.f;
+        const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && seen_by_all > pos;
+        bool passed = larger;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // what a masked place holds (a score, a scale) is selected away, not multiplied
+                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (scale.x * qscale[nt][j]) : -INFINITY;
+                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (scale.y * qscale[nt][j]) : -INFINITY;
+                passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
+            }
+        if (__any_sync(0xffffffffu, passed)) {
+            if (__any_sync(0xffffffffu, larger)) {
                 const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v0), __float_as_uint(v1)));
                 const int e = min(max((int)(top >> 23) - 127, -60), 100);
                 const float f = ldexpf(1.f, vexp - e);
@@ -315,20 +325,6 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 vexp = e;
                 vlimit = __uint_as_float((uint32_t)(127 + e + 5) << 23);
             }
-            const float unit_v = __uint_as_float((uint32_t)(127 - vexp) << 23);   // 2^-vexp
-            vs0 *= unit_v, vs1 *= unit_v;
-        }
-        bool passed = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                // what a masked place holds (a score, a scale) is selected away, not multiplied
-                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (scale.x * qscale[nt][j]) : -INFINITY;
-                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (scale.y * qscale[nt][j]) : -INFINITY;
-                passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
-            }
-        if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -346,6 +342,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     }
                 }
         }
+        const float unit_v = KV8 ? __uint_as_float((uint32_t)(127 - vexp) << 23) : 1.f;   // 2^-vexp
+        const float vs0 = scale.z * unit_v, vs1 = scale.w * unit_v;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
