@@ -222,7 +222,7 @@ def _serving_lib() -> C.CDLL:
     return L
 
 
-_sparse_ready = False
+_sparse_fns = None
 
 
 class PaTablesArgs(C.Structure):
@@ -233,21 +233,30 @@ class PaTablesArgs(C.Structure):
 
 
 def _sparse_lib() -> C.CDLL:
-    global _sparse_ready
-    if _sparse_ready:
-        return _lib
+    """The library with the sparse decode step's calls declared (and kept by name: this is on every call's path)."""
+    global _sparse_fns
     L = lib()
-    if not _sparse_ready:
+    if _sparse_fns is None:
         P, I32 = C.c_void_p, C.c_int32
         L.pa_step_tables.argtypes = [P, C.POINTER(PaTablesArgs), P]
         L.pa_key_bounds_size.argtypes = [P, C.POINTER(C.c_uint64)]
         L.pa_key_bounds.argtypes = [P, P, P, P, I32, P, I32, I32, P, P]
         L.pa_select_blocks.argtypes = [P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, P]
         L.pa_decode_selected.argtypes = [P, P, P, P, P, I32, P, I32, P, I32, I32, I32, C.c_float, P, P]
-        for f in ("pa_step_tables", "pa_key_bounds_size", "pa_key_bounds", "pa_select_blocks", "pa_decode_selected"):
-            getattr(L, f).restype = C.c_int
-        _sparse_ready = True
+        fns = {f: getattr(L, f) for f in ("pa_step_tables", "pa_key_bounds_size", "pa_key_bounds", "pa_select_blocks",
+                                          "pa_decode_selected")}
+        for f in fns.values():
+            f.restype = C.c_int
+        _sparse_fns = fns
     return L
+
+
+def _sparse_call(name: str, *args) -> None:
+    if _sparse_fns is None:
+        _sparse_lib()
+    status = _sparse_fns[name](*args)
+    if status:
+        raise PagedAttnError(status, name)
 
 
 class Pool:
@@ -509,13 +518,13 @@ class Pool:
         a = PaTablesArgs(B, num_tokens, stride, new_lens.data_ptr(), _ptr(keep_lens), context_lens.data_ptr(),
                          block_tables.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), cu_q.data_ptr(),
                          positions.data_ptr(), slot_mapping.data_ptr())
-        _check(_sparse_lib().pa_step_tables(self.handle, a, _stream_on(stream, self.device)), "pa_step_tables")
+        _sparse_call("pa_step_tables", self.handle, a, _stream_on(stream, self.device))
         return cu_q, positions, slot_mapping
 
     def bounds_size(self) -> int:
         """Bytes of the bounds of one cache of this pool's geometry (pa_key_bounds_size)."""
         n = C.c_uint64()
-        _check(_sparse_lib().pa_key_bounds_size(self.handle, n), "pa_key_bounds_size")
+        _sparse_call("pa_key_bounds_size", self.handle, n)
         return n.value
 
     def new_bounds(self) -> torch.Tensor:
@@ -545,24 +554,21 @@ class Pool:
         _need(context_lens, "context_lens", torch.int32, index, (lens,))
         if k_cache is not None:
             _need(k_cache, "k_cache", self.k_cache.dtype, index, self.k_cache.shape)
-        _check(_sparse_lib().pa_key_bounds(self.handle, _ptr(k_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
-                                           context_lens.data_ptr(), int(num_tokens), B, bounds.data_ptr(),
-                                           _stream_on(stream, self.device)), "pa_key_bounds")
+        _sparse_call("pa_key_bounds", self.handle, _ptr(k_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
+                     context_lens.data_ptr(), int(num_tokens), B, bounds.data_ptr(), _stream_on(stream, self.device))
         return bounds
 
-    def _rows(self, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor) -> int:
-        """Checks q [B, q_len, Hq, d] and what goes with it; returns the tables' stride."""
+    def _rows(self, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor) -> tuple:
+        """Checks q [B, q_len, Hq, d] and what goes with it; returns (device index, q's shape, the tables' stride)."""
         index, d = self.device.index, self.geometry[3]
-        if q.dim() != 4 or block_tables.dim() != 2 or context_lens.dim() != 1:
+        shape, tables, lens = q.shape, block_tables.shape, context_lens.shape
+        if len(shape) != 4 or len(tables) != 2 or len(lens) != 1 or tables[0] < shape[0] or lens[0] < shape[0]:
             raise ValueError(f"q must be [B, q_len, Hq, {d}], block_tables [>= B, stride], context_lens [>= B]: got "
-                             f"{tuple(q.shape)}, {tuple(block_tables.shape)}, {tuple(context_lens.shape)}")
-        B, (rows, stride), lens = q.shape[0], block_tables.shape, context_lens.shape[0]
-        if rows < B or lens < B:
-            raise ValueError(f"block_tables and context_lens must hold {B} sequences, got {rows} and {lens}")
-        _need(q, "q", self.dtype, index, (B, q.shape[1], q.shape[2], d))
-        _need(block_tables, "block_tables", torch.int32, index, (rows, stride))
-        _need(context_lens, "context_lens", torch.int32, index, (lens,))
-        return stride
+                             f"{tuple(shape)}, {tuple(tables)}, {tuple(lens)}")
+        _need(q, "q", self.dtype, index, (shape[0], shape[1], shape[2], d))
+        _need(block_tables, "block_tables", torch.int32, index, tables)
+        _need(context_lens, "context_lens", torch.int32, index, lens)
+        return index, shape, tables[1]
 
     def select_blocks(self, q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                       budget: int, num_first: int = 1, num_last: int = 2, out: Optional[torch.Tensor] = None,
@@ -570,17 +576,16 @@ class Pool:
         """The budget best blocks for each sequence and KV head of q [B, q_len, Hq, d] by the bounds' scores
         (pa_select_blocks), the first num_first and the last num_last always among them: int32 [B, Hkv, budget],
         ascending, -1 behind the last."""
-        stride, budget = self._rows(q, block_tables, context_lens), int(budget)
+        (index, (B, q_len, Hq, _), stride), budget = self._rows(q, block_tables, context_lens), int(budget)
         self._bounds(bounds)
-        B, q_len, Hq, _ = q.shape
         shape = (B, self.geometry[1], max(budget, 0))
         if out is None:
             out = _new(shape, torch.int32, self.device, stream)
         else:
-            _need(out, "out", torch.int32, self.device.index, shape)
-        _check(_sparse_lib().pa_select_blocks(
-            self.handle, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), stride, context_lens.data_ptr(), B, Hq,
-            q_len, budget, int(num_first), int(num_last), out.data_ptr(), _stream_on(stream, self.device)), "pa_select_blocks")
+            _need(out, "out", torch.int32, index, shape)
+        _sparse_call("pa_select_blocks", self.handle, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), stride,
+                     context_lens.data_ptr(), B, Hq, q_len, budget, int(num_first), int(num_last), out.data_ptr(),
+                     _stream_on(stream, self.device))
         return out
 
     def decode_selected(self, q: torch.Tensor, selected: torch.Tensor, block_tables: torch.Tensor,
@@ -589,25 +594,25 @@ class Pool:
                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """decode over the listed blocks only (pa_decode_selected): selected int32 [B, Hkv, budget] names blocks of
         each sequence by their place in its table, negative entries are skipped."""
-        stride = self._rows(q, block_tables, context_lens)
+        index, shape, stride = self._rows(q, block_tables, context_lens)
         if selected.dim() != 3:
             raise ValueError(f"selected must be [B, Hkv, budget], got {tuple(selected.shape)}")
-        B, q_len, Hq, _ = q.shape
-        budget = selected.shape[2]
-        _need(selected, "selected", torch.int32, self.device.index, (B, self.geometry[1], budget))
-        if out is None:
-            out = _new(q.shape, self.dtype, self.device, stream)
+        (B, q_len, Hq, _), budget = shape, selected.shape[2]
+        _need(selected, "selected", torch.int32, index, (B, self.geometry[1], budget))
+        if out is not None:
+            _need(out, "out", self.dtype, index, shape)
+        elif stream is None:
+            out = torch.empty_like(q)
         else:
-            _need(out, "out", self.dtype, self.device.index, q.shape)
+            out = _new(shape, self.dtype, self.device, stream)
         if (k_cache is None) != (v_cache is None):
             raise ValueError("pass both k_cache and v_cache, or neither")
         if k_cache is not None:
-            _need(k_cache, "k_cache", self.k_cache.dtype, self.device.index, self.k_cache.shape)
-            _need(v_cache, "v_cache", self.v_cache.dtype, self.device.index, self.v_cache.shape)
-        _check(_sparse_lib().pa_decode_selected(
-            self.handle, q.data_ptr(), _ptr(k_cache), _ptr(v_cache), selected.data_ptr(), budget, block_tables.data_ptr(),
-            stride, context_lens.data_ptr(), B, Hq, q_len, float(scale), out.data_ptr(), _stream_on(stream, self.device)),
-            "pa_decode_selected")
+            _need(k_cache, "k_cache", self.k_cache.dtype, index, self.k_cache.shape)
+            _need(v_cache, "v_cache", self.v_cache.dtype, index, self.v_cache.shape)
+        _sparse_call("pa_decode_selected", self.handle, q.data_ptr(), _ptr(k_cache), _ptr(v_cache), selected.data_ptr(), budget,
+                     block_tables.data_ptr(), stride, context_lens.data_ptr(), B, Hq, q_len, float(scale), out.data_ptr(),
+                     _stream_on(stream, self.device))
         return out
 
     def launches(self, block_table_stride: int, num_seqs: int, num_q_heads: int, q_len: int) -> int:
