@@ -278,12 +278,14 @@ constexpr int SEL_CTAS = 4;                            // per SM
 constexpr int SEL_BINS = 256;
 static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
 constexpr int SEL_MAX_RANKS = 16;
+// Words of shared memory in front of the keys: histograms, ends (4), the digit (4), sums and counts of the warps.
+constexpr int SEL_WORDS = 4 * SEL_BINS + 4 + 4 + SEL_WARPS * 3;
 
 __host__ __device__ constexpr int sel_q_stride(int D) { return 4 * D + 32; }   // bytes of a row [c+, c-] in fp16, and a pad
 // Where value i of a row lies: the four values of each of a quad's lanes in one step side by side.
 __device__ __forceinline__ int sel_q_at(int i) { return (((i >> 7) * 8 + ((i & 31) >> 2)) * 4 + ((i >> 5) & 3)) * 4 + (i & 3); }
 __host__ __device__ constexpr size_t sel_smem(int D, int NT, int chunk) {
-    return (size_t)NT * 8 * (sel_q_stride(D) + 8) + (4 * SEL_BINS + 6 + SEL_WARPS * 4) * 4 + (size_t)chunk * 4;
+    return (size_t)NT * 8 * (sel_q_stride(D) + 8) + SEL_WORDS * 4 + (size_t)chunk * 4;
 }
 
 // 32 bytes that no other CTA of this call reads (the bounds of a step are larger than what L2 could keep for the next).
@@ -332,9 +334,9 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     float *qmul = reinterpret_cast<float *>(qsm + RP * QS), *qadd = qmul + RP;   // a row's step; 0, or -inf: does not count
     int *hist = reinterpret_cast<int *>(qadd + RP);    // [4][256]
     uint32_t *ends = reinterpret_cast<uint32_t *>(hist + 4 * SEL_BINS);   // least and largest key, of the CTA and of the cluster
-    int *digit = reinterpret_cast<int *>(ends + 4);    // the digit, what is needed of its bin
-    int *wtot = digit + 2;                             // [warps] sums; [warps][3] counts
-    uint32_t *keys = reinterpret_cast<uint32_t *>(wtot + W * 4);   // the block ids, then the keys in their place
+    int *digit = reinterpret_cast<int *>(ends + 4);    // the digit, what is needed of its bin, the bin's size
+    int *wtot = digit + 4;                             // [warps] sums; [warps][2] counts
+    uint32_t *keys = reinterpret_cast<uint32_t *>(hist + SEL_WORDS);   // the block ids, then the keys in their place
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int unit = (int)(blockIdx.x / ranks), g = unit % p.Hkv, b = unit / p.Hkv;
@@ -532,24 +534,23 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
         above -= sum;
         __syncthreads();
         for (int w = 0; w < warp; ++w) above += wtot[w];
-        if (above < need && above + sum >= need) digit[0] = bin, digit[1] = need - above;
+        if (above < need && above + sum >= need) digit[0] = bin, digit[1] = need - above, digit[2] = sum;
         __syncthreads();
-        const int d = digit[0];
-        // the bin's size, and what lies before this CTA in the bins above and in this one
-        int *cnt = wtot + W;                   // [warps][3]
-        const int up = __reduce_add_sync(0xffffffffu, bin > d ? before : 0);
-        const int at = __reduce_add_sync(0xffffffffu, bin == d ? before : 0);
-        const int size = __reduce_add_sync(0xffffffffu, bin == d ? sum : 0);
-        if (lane == 0) cnt[3 * warp] = up, cnt[3 * warp + 1] = at, cnt[3 * warp + 2] = size;
+        const int d = digit[0], size = digit[2];
         need = digit[1];
-        __syncthreads();
-        int bin_size = 0;
-        eq_before = 0;
+        if (ranks > 1) {                               // what lies before this CTA in the bins above and in this one
+            int *cnt = wtot + SEL_WARPS;               // [warps][2]
+            const int up = __reduce_add_sync(0xffffffffu, bin > d ? before : 0);
+            const int at = __reduce_add_sync(0xffffffffu, bin == d ? before : 0);
+            if (lane == 0) cnt[2 * warp] = up, cnt[2 * warp + 1] = at;
+            __syncthreads();
+            eq_before = 0;
 #pragma unroll
-        for (int w = 0; w < W; ++w) gt_before += cnt[3 * w], eq_before += cnt[3 * w + 1], bin_size += cnt[3 * w + 2];
+            for (int w = 0; w < SEL_WARPS; ++w) gt_before += cnt[2 * w], eq_before += cnt[2 * w + 1];
+        }
         prefix |= (uint32_t)d << shift;
         mask = shift == 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << shift;
-        bits = bin_size == need ? 0 : shift;           // a bin that is taken whole ends it
+        bits = size == need ? 0 : shift;               // a bin that is taken whole ends it
     }
     if (ranks > 1) cluster_arrive();                   // this CTA reads no other one's memory any more
 
