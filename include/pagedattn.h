@@ -296,7 +296,7 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
 /*
  * The tables of a serving step, made on the device from the requests' lengths:
  * what pa_allocator_append does on the host for one sequence, for all of them
- * by one launch that a captured graph can repeat. In this order:
+ * by one call that a captured graph can repeat. In this order:
  *   every sequence b is cut back to kept = min(context_lens[b], keep_lens[b])
  *   tokens (0: its request has ended; rejected drafts; NULL: nothing is cut), the
  *   blocks that it no longer needs go back on the free stack;
@@ -361,7 +361,9 @@ pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
  * cu_q[b+1] - cu_q[b] tokens end at context_lens[b] (as for pa_prefill_packed;
  * their K is in the pool already); the bounds of every block that holds one of
  * them are made anew from all its tokens before context_lens[b]. Other blocks'
- * bounds are left as they are. 16-bit and FP8 pools.
+ * bounds are left as they are: a block filled without such a call (by
+ * pa_copy_blocks, say) keeps those that it had, until its next token. 16-bit and
+ * FP8 pools.
  *   k_cache        device pool, or NULL for the pool's own
  *   cu_q           device int32 [num_seqs + 1], 0 <= cu_q[b] <= cu_q[b+1] <= num_tokens
  *   block_tables   device int32 [num_seqs, block_table_stride]

@@ -322,7 +322,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // above and at the threshold comes out of the same histograms, so the indices are written in order without another round.
 //
 // Bound by memory while it scores (64 sequences of 1024 blocks, 64 / 8 heads of 128: 132 MB in 18 us), with 2 us before it
-// and 4 us behind it in which all CTAs, resident at once, are at the same point: 27 us, 4.9 TB/s. One sequence of 8192 blocks:
+// and 4 us behind it in which all CTAs, resident at once, are at the same point: 26.4 us, 5.0 TB/s. One sequence of 8192 blocks:
 // 14.8 us, of which the barriers and histograms of 16 CTAs take 7. L2 is told to let the codes go first: 31.4 -> 29.9 us.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const SelectParams p) {
@@ -589,7 +589,7 @@ static cudaError_t launch_select_t(SelectParams p, int sm_count, cudaStream_t st
     const int blocks = (p.max_len + p.bs - 1) / p.bs, tiles = (blocks + 15) / 16;
     const int64_t units = (int64_t)p.num_seqs * p.Hkv;
     // CTAs of a cluster: enough for two on each SM, each with a tile for every warp; more where the keys need the room. By 1, 2,
-    // 4, 8, 16 CTAs, us: one sequence of 8192 blocks 71, 40, 23, 16, 14.7; 64 of 1024 27, 37, 51, 86, 240; 13 of up to 1875
+    // 4, 8, 16 CTAs, us: one sequence of 8192 blocks 71, 40, 23, 16, 14.8; 64 of 1024 26, 37, 51, 86, 240; 13 of up to 1875
     // 13.7, 13.5, 12.1, 12.3, 18.
     int ranks = 1;
     while (ranks < SEL_MAX_RANKS && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * 1024)) ranks *= 2;

@@ -11,7 +11,7 @@
 // CTA's warps are joined in its shared memory, those of the cluster's CTAs through each other's, each CTA writing a share
 // of the outputs: one launch, no workspace, a fixed order.
 //
-// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 79 us, 6.8 TB/s, the copy rate; one
+// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 78 to 81 us, 6.7 to 6.9 TB/s, the copy rate; one
 // sequence of 64 blocks 6.7 us (in a graph 5.8): launch 2, lookups 1.5, two tiles a warp 1, joins 2; 19 sequences of 50 blocks
 // of 32 in an FP8 pool, 16 query rows: 17.5 us, bound by a warp's chain per tile (scores 300 cycles, softmax 360, weights 90,
 // values and the next copies 500) at eight warps an SM.
