@@ -47,6 +47,17 @@ __host__ __device__ constexpr int att_join_bytes(int D, int nt) {
 __host__ __device__ constexpr int att_body_bytes(int D, bool kv8, int nt) {
     return (att_ring_bytes(D, kv8) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8) : att_join_bytes(D, nt)) + 15 & ~15;
 }
+// The query rows' fragments lie in shared memory from three columns of eight on, where they would not fit the registers: 64
+// sequences of 2048 tokens, 32 rows, FP8 110 -> 86 us, bf16 102 -> 98; with two columns (16 rows) the loads lengthen the chain:
+// 19 sequences of a verify, FP8, 17.5 -> 21.4.
+__host__ __device__ constexpr bool att_q_shared(int nt) { return nt > 2; }
+__host__ __device__ constexpr int att_q_bytes(int D, int nt) { return att_q_shared(nt) ? nt * (D / 16) * 32 * 8 : 0; }
+// Ring or states, barriers, the flag of a lost copy, the query rows; the tile lists follow.
+__host__ __device__ constexpr int att_flag_at(int D, bool kv8, int nt) {
+    return att_body_bytes(D, kv8, nt) + ATT_WARPS * att_stages(kv8) * 8;
+}
+__host__ __device__ constexpr int att_q_at(int D, bool kv8, int nt) { return att_flag_at(D, kv8, nt) + 16; }
+__host__ __device__ constexpr int att_lists_at(int D, bool kv8, int nt) { return att_q_at(D, kv8, nt) + att_q_bytes(D, nt); }
 
 // Where 16 bytes (chunk c of a token's row r) of a tile lie: FP8 rows of 128 bytes; 16-bit ones in groups of eight rows, by
 // halves of 64 dimensions; swizzled by the copy.
@@ -101,8 +112,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     uint8_t *smem = smem_raw + (base_u32 - smem_u32(smem_raw));
     constexpr int BODY = att_body_bytes(D, KV8, NT);
     const uint32_t bars_u32 = base_u32 + BODY;
-    int *failed = reinterpret_cast<int *>(smem + BODY + W * STAGES * 8);
-    int2 *lists = reinterpret_cast<int2 *>(smem + BODY + W * STAGES * 8 + 16);     // [W][warp_tiles]: pool row, position
+    int *failed = reinterpret_cast<int *>(smem + att_flag_at(D, KV8, NT));
+    uint2 *q_sm = reinterpret_cast<uint2 *>(smem + att_q_at(D, KV8, NT));          // [NT][KS][32]
+    int2 *lists = reinterpret_cast<int2 *>(smem + att_lists_at(D, KV8, NT));       // [W][warp_tiles]: pool row, position
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;
@@ -221,6 +233,19 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         }
     }
 
+    if constexpr (att_q_shared(NT)) {                  // every warp holds the same: one of them lays them down
+        if (warp == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) q_sm[(nt * KS + ks) * 32 + lane] = make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
+        }
+        __syncthreads();
+    }
+    const auto q_of = [&](int nt, int ks) {
+        return att_q_shared(NT) ? q_sm[(nt * KS + ks) * 32 + lane] : make_uint2(qf[nt][ks][0], qf[nt][ks][1]);
+    };
+
     int last[NT][2];                                   // positions of the columns' rows: the newest token that they see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -279,8 +304,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 const uint32_t c1 = e4m3x2_to_f16x2((uint16_t)r3), c3 = e4m3x2_to_f16x2((uint16_t)(r3 >> 16));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816<M>(sc[nt], a0, a1, a2, a3, qf[nt][2 * kp][0], qf[nt][2 * kp][1]);
-                    mma_16816<M>(sc[nt], c0, c1, c2, c3, qf[nt][2 * kp + 1][0], qf[nt][2 * kp + 1][1]);
+                    const uint2 q0 = q_of(nt, 2 * kp), q1 = q_of(nt, 2 * kp + 1);
+                    mma_16816<M>(sc[nt], a0, a1, a2, a3, q0.x, q0.y);
+                    mma_16816<M>(sc[nt], c0, c1, c2, c3, q1.x, q1.y);
                 }
             }
         } else {
@@ -290,7 +316,10 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 uint32_t a0, a1, a2, a3;
                 ldsm_x4(kb + tile_at<D, KV8>(krow, chunk), a0, a1, a2, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_16816<M>(sc[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint2 qv = q_of(nt, ks);
+                    mma_16816<M>(sc[nt], a0, a1, a2, a3, qv.x, qv.y);
+                }
             }
         }
 
@@ -624,8 +653,7 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
     }
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
-        const size_t smem = 1024 + att_body_bytes(D, KV8, n) + ATT_WARPS * att_stages(KV8) * 8 + 16 +
-                            (size_t)ATT_WARPS * p.warp_tiles * 8;
+        const size_t smem = 1024 + att_lists_at(D, KV8, n) + (size_t)ATT_WARPS * p.warp_tiles * 8;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e != cudaSuccess
                    ? e
