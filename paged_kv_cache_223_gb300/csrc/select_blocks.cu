@@ -262,7 +262,9 @@ cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, in
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min(ctas, most));
     const size_t smem = (size_t)(2 * p.num_seqs + 1) * sizeof(int);
     const auto launch = [&](auto kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the most that any call takes: the attribute is the kernel's, and other threads' calls set it too
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (2 * PA_TABLES_MAX_SEQS + 1) * (int)sizeof(int));
         return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(BND_WARPS * 32), smem, stream, p);
     };
     if (p.k_scales) return launch(bounds_kernel<__half, 128, true>);
@@ -278,6 +280,7 @@ constexpr int SEL_CTAS = 4;                            // per SM
 constexpr int SEL_BINS = 256;
 static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
 constexpr int SEL_MAX_RANKS = 16;
+constexpr int SEL_MAX_TILES = PA_SELECT_MAX_BLOCKS / 16 / SEL_MAX_RANKS;   // of 16 blocks, per CTA: 64 KB of keys
 // Words of shared memory in front of the keys: histograms, ends (4), the digit (4), sums and counts of the warps.
 constexpr int SEL_WORDS = 4 * SEL_BINS + 4 + 4 + SEL_WARPS * 3;
 
@@ -592,11 +595,14 @@ static cudaError_t launch_select_t(SelectParams p, int sm_count, cudaStream_t st
     // 4, 8, 16 CTAs, us: one sequence of 8192 blocks 71, 40, 23, 16, 14.8; 64 of 1024 26, 37, 51, 86, 240; 13 of up to 1875
     // 13.7, 13.5, 12.1, 12.3, 18.
     int ranks = 1;
-    while (ranks < SEL_MAX_RANKS && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * 1024)) ranks *= 2;
+    while (ranks < SEL_MAX_RANKS && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * SEL_MAX_TILES)) ranks *= 2;
     p.chunk = (tiles + ranks - 1) / ranks * 16;
     const auto launch = [&](auto kernel, int nt) {
+        static_assert(sel_smem(D, 4, SEL_MAX_TILES * 16) <= MAX_SMEM_PER_CTA, "the keys of the longest row");
         const size_t smem = sel_smem(D, nt, p.chunk);
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the most that any call takes: the attribute is the kernel's, and other threads' calls set it too
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sel_smem(D, nt, SEL_MAX_TILES * 16));
         if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return e != cudaSuccess ? e : launch_clusters(kernel, (unsigned)(units * ranks), SEL_THREADS, smem, ranks, stream, p);
     };

@@ -28,6 +28,7 @@ namespace {
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_MAX_RANKS = 8;
+constexpr int ATT_MAX_TILES = PA_SELECT_MAX_BUDGET * (32 / TILE_TOKENS);   // of a list, in blocks of 32 tokens
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
 
 // Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
@@ -58,6 +59,10 @@ __host__ __device__ constexpr int att_flag_at(int D, bool kv8, int nt) {
 }
 __host__ __device__ constexpr int att_q_at(int D, bool kv8, int nt) { return att_flag_at(D, kv8, nt) + 16; }
 __host__ __device__ constexpr int att_lists_at(int D, bool kv8, int nt) { return att_q_at(D, kv8, nt) + att_q_bytes(D, nt); }
+
+constexpr size_t att_smem(int D, bool kv8, int nt, int warp_tiles) {
+    return 1024 + att_lists_at(D, kv8, nt) + (size_t)ATT_WARPS * warp_tiles * 8;
+}
 
 // Where 16 bytes (chunk c of a token's row r) of a tile lie: FP8 rows of 128 bytes; 16-bit ones in groups of eight rows, by
 // halves of 64 dimensions; swizzled by the copy.
@@ -653,8 +658,11 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
     }
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
-        const size_t smem = 1024 + att_lists_at(D, KV8, n) + (size_t)ATT_WARPS * p.warp_tiles * 8;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static_assert(att_smem(D, KV8, 4, ATT_MAX_TILES / ATT_WARPS) <= MAX_SMEM_PER_CTA, "a list of the largest budget by one CTA");
+        const size_t smem = att_smem(D, KV8, n, p.warp_tiles);
+        // the most that any call takes: the attribute is the kernel's, and other threads' calls set it too
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)att_smem(D, KV8, n, ATT_MAX_TILES / ATT_WARPS));
         return e != cudaSuccess
                    ? e
                    : launch_clusters(kernel, (unsigned)(units * ranks), ATT_THREADS, smem, ranks, stream, tmk, tmv, p);

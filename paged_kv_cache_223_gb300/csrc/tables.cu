@@ -230,7 +230,10 @@ __global__ void __launch_bounds__(TOK_THREADS) tokens_kernel(const TablesParams 
 
 cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream) {
     const size_t smem = (size_t)(4 * p.num_seqs + 3) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The attribute belongs to the kernel on this device, not to a call: always the most that any call takes, so that a call of
+    // another thread between here and the launch cannot lower it.
+    cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (4 * PA_TABLES_MAX_SEQS + 3) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     p.vectors = (reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
     p.tokens_apart = p.num_tokens > TAB_MAX_TOKENS;
