@@ -421,7 +421,7 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
  * run. 16-bit pools with heads of 64 or 128 and FP8 pools.
  *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping
  *   selected       device int32 [num_seqs, num_kv_heads, budget]; budget 1 .. PA_SELECT_MAX_BUDGET
- *   scale          softmax scale, finite
+ *   scale          softmax scale; finite, and so times log2(e)
  * the others as pa_select_blocks. Entries beyond the context, lengths and block
  * ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at pa_pool_check); such
  * an entry is skipped, such a length is clamped.

@@ -216,7 +216,8 @@ pa_status pa_decode_selected(pa_pool *pool, const void *q, const void *k_cache, 
                              const int32_t *selected, int32_t budget, const int32_t *block_tables,
                              int32_t block_table_stride, const int32_t *context_lens, int32_t num_seqs,
                              int32_t num_q_heads, int32_t q_len, float scale, void *out, void *stream) {
-    if (!pool || !std::isfinite(scale) || (k_cache == nullptr) != (v_cache == nullptr)) return PA_ERR_INVALID_ARG;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!pool || !std::isfinite(scale_log2) || (k_cache == nullptr) != (v_cache == nullptr)) return PA_ERR_INVALID_ARG;
     const pa_pool_config &c = pool->cfg;
     pa_status st = row_sizes(c, block_table_stride, num_seqs, num_q_heads, q_len, budget);
     if (st != PA_OK) return st;
@@ -258,7 +259,7 @@ pa_status pa_decode_selected(pa_pool *pool, const void *q, const void *k_cache, 
     p.bs = c.block_size;
     p.num_blocks = c.num_blocks;
     p.max_len = max_len_of(c, block_table_stride);
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.wait_ns = pool->wait_ns;
     p.status = pool->status;
     DeviceGuard g(c.device);
