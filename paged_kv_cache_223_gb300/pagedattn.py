@@ -259,6 +259,14 @@ def _sparse_call(name: str, *args) -> None:
         raise PagedAttnError(status, name)
 
 
+def _int32(x: int, name: str) -> int:
+    """A count as the C call takes it: ctypes would drop the bits above 32."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 class Pool:
     """One paged KV pool (pa_pool_create) with its caches.
 
@@ -489,7 +497,7 @@ class Pool:
         tokens and the blocks that these need. context_lens [B], block_tables [B, stride], free_blocks
         [num_blocks] (a stack of num_free[0] ids) and num_free [1] are changed in place (all int32). Returns
         cu_q int32 [B + 1], positions int32 and slot_mapping int64 [num_tokens]: 0 and -1 behind the last token."""
-        index, i32, num_tokens = self.device.index, torch.int32, int(num_tokens)
+        index, i32, num_tokens = self.device.index, torch.int32, _int32(num_tokens, "num_tokens")
         if new_lens.dim() != 1 or block_tables.dim() != 2:
             raise ValueError(f"new_lens must be [B], block_tables [B, stride]: got {tuple(new_lens.shape)}, "
                              f"{tuple(block_tables.shape)}")
@@ -555,7 +563,8 @@ class Pool:
         if k_cache is not None:
             _need(k_cache, "k_cache", self.k_cache.dtype, index, self.k_cache.shape)
         _sparse_call("pa_key_bounds", self.handle, _ptr(k_cache), cu_q.data_ptr(), block_tables.data_ptr(), stride,
-                     context_lens.data_ptr(), int(num_tokens), B, bounds.data_ptr(), _stream_on(stream, self.device))
+                     context_lens.data_ptr(), _int32(num_tokens, "num_tokens"), B, bounds.data_ptr(),
+                     _stream_on(stream, self.device))
         return bounds
 
     def _rows(self, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor) -> tuple:
@@ -576,7 +585,7 @@ class Pool:
         """The budget best blocks for each sequence and KV head of q [B, q_len, Hq, d] by the bounds' scores
         (pa_select_blocks), the first num_first and the last num_last always among them: int32 [B, Hkv, budget],
         ascending, -1 behind the last."""
-        (index, (B, q_len, Hq, _), stride), budget = self._rows(q, block_tables, context_lens), int(budget)
+        (index, (B, q_len, Hq, _), stride), budget = self._rows(q, block_tables, context_lens), _int32(budget, "budget")
         self._bounds(bounds)
         shape = (B, self.geometry[1], max(budget, 0))
         if out is None:
@@ -584,8 +593,8 @@ class Pool:
         else:
             _need(out, "out", torch.int32, index, shape)
         _sparse_call("pa_select_blocks", self.handle, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), stride,
-                     context_lens.data_ptr(), B, Hq, q_len, budget, int(num_first), int(num_last), out.data_ptr(),
-                     _stream_on(stream, self.device))
+                     context_lens.data_ptr(), B, Hq, q_len, budget, _int32(num_first, "num_first"),
+                     _int32(num_last, "num_last"), out.data_ptr(), _stream_on(stream, self.device))
         return out
 
     def decode_selected(self, q: torch.Tensor, selected: torch.Tensor, block_tables: torch.Tensor,

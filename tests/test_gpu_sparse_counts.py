@@ -20,6 +20,20 @@ def step():
     return pool, torch.zeros(1, 1, 4, 64, dtype=torch.float16, device=DEV), i32([[3, 1, 2, 0]]), i32([64])
 
 
+@pytest.mark.parametrize("n", [2 ** 32 + 4, 2 ** 31, -2 ** 31 - 1])
+def test_counts_beyond_32_bits_are_refused(step, n):
+    pool, q, tables, lens = step
+    bounds, one = pool.new_bounds(), torch.zeros(0, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="num_tokens must fit"):
+        pool.step_tables(i32([0]), lens, tables, torch.zeros(8, dtype=torch.int32, device=DEV), i32([0]), n, positions=one)
+    with pytest.raises(ValueError, match="num_tokens must fit"):
+        pool.key_bounds(bounds, i32([0, 4]), tables, lens, n)
+    for kw in ("budget", "num_first", "num_last"):
+        with pytest.raises(ValueError, match=kw + " must fit"):
+            pool.select_blocks(q, bounds, tables, lens, **{**dict(budget=4), kw: n})
+    assert pool.check() == pa.PA_OK and not bool(bounds.any()) and lens.tolist() == [64]
+
+
 @pytest.mark.parametrize("scale", [2.2e38, -2.2e38, 2.5e38, 3.4e38, -3.4e38])
 def test_scales_near_the_largest_number(step, scale):
     """Scores of 0 whatever the scale: the mean of V, as long as scale times log2(e) is a number (log2(e) 2.2e38 = 3.17e38,
