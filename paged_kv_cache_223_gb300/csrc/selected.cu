@@ -280,10 +280,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     int it = 0;
     for (; it < tiles; ++it) {
         const int s = it % STAGES;
-        if (!mbar_wait_bounded(bars_u32 + (warp * STAGES + s) * 8, (uint32_t)(it / STAGES) & 1u, p.wait_ns)) {
-            ok = false;
-            break;
-        }
+        // false: the copy did not land in time. A lane may see it land as another gives up, so the warp leaves by a vote (below).
+        const bool landed = mbar_wait_bounded(bars_u32 + (warp * STAGES + s) * 8, (uint32_t)(it / STAGES) & 1u, p.wait_ns);
         const int pos = list[it].y;
         const uint32_t kb = ring_u32 + s * STAGE, vb = kb + TILE;
         float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);   // FP8: of K and V of the tokens gq and gq + 8
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
         const float v0 = t0 < seen_by_all ? fabsf(scale.z) : 0.f, v1 = t1 < seen_by_all ? fabsf(scale.w) : 0.f;
         const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && seen_by_all > pos;
-        bool passed = larger;
+        bool passed = larger || !landed;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -346,6 +344,10 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
             }
         if (__any_sync(0xffffffffu, passed)) {
+            if (__any_sync(0xffffffffu, !landed)) {
+                ok = false;
+                break;
+            }
             if (__any_sync(0xffffffffu, larger)) {
                 const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v0), __float_as_uint(v1)));
                 const int e = min(max((int)(top >> 23) - 127, -60), 100);
