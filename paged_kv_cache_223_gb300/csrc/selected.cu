@@ -331,18 +331,32 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         const int t0 = pos + gq, t1 = t0 + 8;
         // FP8: weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
         // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
-        const float v0 = t0 < seen_by_all ? fabsf(scale.z) : 0.f, v1 = t1 < seen_by_all ? fabsf(scale.w) : 0.f;
-        const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && seen_by_all > pos;
+        const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
+        float v0 = fabsf(scale.z), v1 = fabsf(scale.w);
+        if (whole < TILE_TOKENS) v0 = gq < whole ? v0 : 0.f, v1 = gq + 8 < whole ? v1 : 0.f;
+        const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && whole > 0;
         bool passed = larger || !landed;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                // what a masked place holds (a score, a scale) is selected away, not multiplied
-                sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] * (scale.x * qscale[nt][j]) : -INFINITY;
-                sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] * (scale.y * qscale[nt][j]) : -INFINITY;
-                passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
+                sc[nt][j] *= scale.x * qscale[nt][j];
+                sc[nt][2 + j] *= scale.y * qscale[nt][j];
             }
+        if (whole < TILE_TOKENS) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // what a masked place holds (a score, a scale) is selected away, not multiplied
+                    sc[nt][j] = t0 <= last[nt][j] ? sc[nt][j] : -INFINITY;
+                    sc[nt][2 + j] = t1 <= last[nt][j] ? sc[nt][2 + j] : -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) passed |= fmaxf(sc[nt][j], sc[nt][2 + j]) > m[nt][j] + ATT_RESCALE_LOG2;
         if (__any_sync(0xffffffffu, passed)) {
             if (__any_sync(0xffffffffu, !landed)) {
                 ok = false;
@@ -386,8 +400,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             for (int j = 0; j < 2; ++j) {
                 const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
                 // -0 for what is not seen: a sum of nothing keeps its sign, one of weights that are all 0 loses it
-                const float p0 = t0 <= last[nt][j] ? ex2_approx(sc[nt][j] - ref) : -0.f;
-                const float p1 = t1 <= last[nt][j] ? ex2_approx(sc[nt][2 + j] - ref) : -0.f;
+                float p0 = ex2_approx(sc[nt][j] - ref), p1 = ex2_approx(sc[nt][2 + j] - ref);
+                if (whole < TILE_TOKENS) p0 = t0 <= last[nt][j] ? p0 : -0.f, p1 = t1 <= last[nt][j] ? p1 : -0.f;
                 l[nt][j] = __fadd_rn(__fadd_rn(l[nt][j], p0), p1);
                 sc[nt][j] = p0 * vs0;
                 sc[nt][2 + j] = p1 * vs1;
@@ -397,7 +411,6 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         // 0 already. So may the value of a token that not every row sees be to the rows that do not: where it is no number
         // (or, FP8, far larger than the rest), the token is added in fp32 to the rows that see it, and its weights and words
         // become 0 as well.
-        const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
         if (whole < TILE_TOKENS) {
             const int w0 = whole < 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos), some = w1 - w0;
             uint8_t *vs = smem + (vb - base_u32);
