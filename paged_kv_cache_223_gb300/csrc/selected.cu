@@ -13,7 +13,7 @@
 //
 // Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 78 to 81 us, 6.7 to 6.9 TB/s, the copy rate; one
 // sequence of 64 blocks 6.7 us (in a graph 5.8): launch 2, lookups 1.5, two tiles a warp 1, joins 2; 19 sequences of 50 blocks
-// of 32 in an FP8 pool, 16 query rows: 17.5 us, bound by a warp's chain per tile (scores 300 cycles, softmax 360, weights 90,
+// of 32 in an FP8 pool, 16 query rows: 17.2 us, bound by a warp's chain per tile (scores 300 cycles, softmax 360, weights 90,
 // values and the next copies 500) at eight warps an SM.
 #include <type_traits>
 
@@ -33,7 +33,7 @@ constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maxi
 
 // Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
 // 17.5 -> 17.7 us, 64 of 2048 tokens 44 -> 46), four CTAs with one column of eight rows, else two by registers (16 rows at
-// three CTAs, with spills: 18.9 -> 23.0). 16-bit pools, 8 KB: three copies, two CTAs. Three CTAs of two copies each keep as many
+// three CTAs, with spills: 18.9 -> 23.0; as pairs of warps on a pipeline, eight rows each, 16 warps an SM: 17.6 -> 21.4). 16-bit pools, 8 KB: three copies, two CTAs. Three CTAs of two copies each keep as many
 // bytes in flight: 64 sequences of 128 blocks 86 us instead of 79.
 __host__ __device__ constexpr int att_stages(bool kv8) { return kv8 ? 2 : 3; }
 __host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : 2; }
@@ -49,7 +49,7 @@ __host__ __device__ constexpr int att_body_bytes(int D, bool kv8, int nt) {
     return (att_ring_bytes(D, kv8) > att_join_bytes(D, nt) ? att_ring_bytes(D, kv8) : att_join_bytes(D, nt)) + 15 & ~15;
 }
 // The query rows' fragments lie in shared memory from three columns of eight on, where they would not fit the registers: 64
-// sequences of 2048 tokens, 32 rows, FP8 110 -> 86 us, bf16 102 -> 98; with two columns (16 rows) the loads lengthen the chain:
+// sequences of 2048 tokens, 32 rows, FP8 110 -> 86 us, bf16 102 -> 97; with two columns (16 rows) the loads lengthen the chain:
 // 19 sequences of a verify, FP8, 17.5 -> 21.4.
 __host__ __device__ constexpr bool att_q_shared(int nt) { return nt > 2; }
 __host__ __device__ constexpr int att_q_bytes(int D, int nt) { return att_q_shared(nt) ? nt * (D / 16) * 32 * 8 : 0; }
