@@ -298,6 +298,8 @@ __device__ __forceinline__ void ldg256(const void *p, uint32_t (&w)[8]) {
                  : "l"(p));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Whole numbers of four bytes as two pairs of fp16: the byte plus 128, under the exponent of 1024, less 1152.
 __device__ __forceinline__ void bytes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
     const uint32_t u = x ^ 0x80808080u;
@@ -325,7 +327,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // above and at the threshold comes out of the same histograms, so the indices are written in order without another round.
 //
 // Bound by memory while it scores (64 sequences of 1024 blocks, 64 / 8 heads of 128: 132 MB in 18 us), with 2 us before it
-// and 4 us behind it in which all CTAs, resident at once, are at the same point: 26.4 us, 5.0 TB/s. One sequence of 8192 blocks:
+// and 4 us behind it in which all CTAs, resident at once, are at the same point: 25.7 us, 5.1 TB/s. One sequence of 8192 blocks:
 // 14.8 us, of which the barriers and histograms of 16 CTAs take 7. L2 is told to let the codes go first: 31.4 -> 29.9 us.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const SelectParams p) {
@@ -347,47 +349,32 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     pdl_wait();
 
     int len = p.context_lens[b];
-    // one CTA to a unit holds its blocks whatever the length is: their ids are on their way before it is known
-    const int32_t *trow = p.block_tables + b * p.stride;
-    if (ranks == 1)
-        for (int i = tid; i < min(p.chunk, (int)p.stride); i += THREADS) keys[i] = (uint32_t)trow[i];
-
-    // ---- query rows
-    constexpr int PL = D / 32, QR = (RP + W - 1) / W;  // values per lane; rows per warp, on their way together
-    float x[QR][PL];
+    // ---- query rows, on their way together
+    constexpr int PL = D / 32, QR = (RP + W - 1) / W;  // values per lane; rows per warp
+    uint32_t x[QR][PL / 2];
 #pragma unroll
     for (int i = 0; i < QR; ++i) {
         const int r = warp + i * W;
 #pragma unroll
-        for (int e = 0; e < PL; ++e) x[i][e] = 0.f;
+        for (int e = 0; e < PL / 2; ++e) x[i][e] = 0u;
         if (r < p.rows) {
             const int qi = r / p.G, hh = r - qi * p.G;
             const T *q = static_cast<const T *>(p.q) + (((int64_t)b * p.q_len + qi) * p.Hq + g * p.G + hh) * D;
 #pragma unroll
-            for (int e = 0; e < PL; e += 2) {
-                const float2 v = unpack2(*reinterpret_cast<const uint32_t *>(q + lane * PL + e), T());
-                x[i][e] = v.x, x[i][e + 1] = v.y;
-            }
+            for (int e = 0; e < PL / 2; ++e) x[i][e] = *reinterpret_cast<const uint32_t *>(q + lane * PL + 2 * e);
         }
     }
-#pragma unroll
-    for (int i = 0; i < QR; ++i) {
-        const int r = warp + i * W;
-        if (r >= RP) break;
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < PL; ++e) top = max(top, abs_bits(x[i][e]));
-        top = __reduce_max_sync(0xffffffffu, top);
-        const bool counts_row = r < p.rows && top < INF_BITS;
-        const float step = counts_row ? step_of(top) : 0.f, inv = inverse_of(step);
-        __half *row = reinterpret_cast<__half *>(qsm + r * QS);
-#pragma unroll
-        for (int e = 0; e < PL; ++e) {
-            const int c = counts_row ? code_of(x[i][e], step, inv) : 0;
-            row[sel_q_at(lane * PL + e)] = __int2half_rn(max(c, 0));
-            row[sel_q_at(D + lane * PL + e)] = __int2half_rn(min(c, 0));
-        }
-        if (lane == 0) qmul[r] = step, qadd[r] = counts_row ? 0.f : -INFINITY;
+    // One CTA to a unit holds its blocks whatever the length is: their ids, and the codes of a warp's first tile as far as L2, a
+    // line of 128 bytes a lane, are on their way before the query rows are taken to whole numbers (64 sequences 26.4 -> 25.7
+    // us, in a graph 28.6 -> 26.6; two tiles 26.5; in clusters, where the memory is not what bounds it, 11.15 -> 11.3).
+    const int32_t *trow = p.block_tables + b * p.stride;
+    if (ranks == 1) {
+        const int count = min(p.chunk, (int)p.stride);
+        for (int i = tid; i < count; i += THREADS) keys[i] = (uint32_t)trow[i];
+        const int i = warp * 16 + lane / 2;
+        const int id = i < count ? trow[i] : -1;
+        if (id >= 0 && id < p.num_blocks && (lane & 1) * 128 < 2 * D)
+            prefetch_l2(p.codes + ((int64_t)id * p.Hkv + g) * 2 * D + (lane & 1) * 128);
     }
     if (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)) {
         if (tid == 0 && rank == 0) set_status(p.status, STATUS_BOUNDS);
@@ -405,6 +392,30 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     const int lo = min(max(0, p.num_first - i0), mine), hi = max(lo, min(mine, n - p.num_last - i0));
     if (ranks > 1)
         for (int i = tid; i < mine; i += THREADS) keys[i] = (uint32_t)trow[i0 + i];
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+        const int r = warp + i * W;
+        if (r >= RP) break;
+        float v[PL];
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < PL / 2; ++e) {
+            const float2 f = unpack2(x[i][e], T());
+            v[2 * e] = f.x, v[2 * e + 1] = f.y;
+            top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool counts_row = r < p.rows && top < INF_BITS;
+        const float step = counts_row ? step_of(top) : 0.f, inv = inverse_of(step);
+        __half *row = reinterpret_cast<__half *>(qsm + r * QS);
+#pragma unroll
+        for (int e = 0; e < PL; ++e) {
+            const int c = counts_row ? code_of(v[e], step, inv) : 0;
+            row[sel_q_at(lane * PL + e)] = __int2half_rn(max(c, 0));
+            row[sel_q_at(D + lane * PL + e)] = __int2half_rn(min(c, 0));
+        }
+        if (lane == 0) qmul[r] = step, qadd[r] = counts_row ? 0.f : -INFINITY;
+    }
     for (int i = tid; i < 4 * SEL_BINS; i += THREADS) hist[i] = 0;
     if (tid < 2) ends[2 * tid] = 0xFFFFFFFFu, ends[2 * tid + 1] = 0u;
     __syncthreads();
