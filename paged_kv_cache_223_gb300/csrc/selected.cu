@@ -97,6 +97,12 @@ __device__ __forceinline__ float2 unpacked(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
 }
 
+// Two fp16 numbers by 2^-11.
+__device__ __forceinline__ uint32_t by_2_11(uint32_t x) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x1000)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 __device__ __forceinline__ float value16(uint16_t w, __half) { return __half2float(__ushort_as_half(w)); }
 __device__ __forceinline__ float value16(uint16_t w, __nv_bfloat16) { return __bfloat162float(__ushort_as_bfloat16(w)); }
 
@@ -474,11 +480,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 }
         }
 
-        // P^T as the B operand, in V's type. In 16-bit pools as two parts (the nearest number and what is left of it): bf16's
-        // eight bits would not do, and fp16's eleven alone made the error 1.3 times the last rounding's (64 sequences of 2048
-        // tokens 84.5 -> 85.8 us for the second part). FP8 pools, whose codes have four bits, take one part of fp16 (the
-        // second one 18.1 -> 19.7 us for 19 sequences of 16 rows, 109 -> 126 for 64 of 32).
-        constexpr bool TWO = !KV8;
+        // P^T as the B operand, in V's type, as two parts: the nearest number and what is left of it. bf16's eight bits would not
+        // do, and fp16's eleven alone made the error of fp16 outputs 1.3 to 1.4 times the last rounding's (16-bit pools, 64
+        // sequences of 2048 tokens: 84.5 -> 85.8 us for the second part; FP8, 8, 16, 32 rows: 44.2, 59.6, 86.4 -> 46.8, 70.6,
+        // 100.5 us). The bf16 outputs of FP8 pools keep eight bits, 2^-9 beside the weights' 2^-12: one part. FP8 pools take the
+        // second part 2^11 times as large, against V by 2^-11 (exact: codes are multiples of 2^-9), so that it keeps its bits
+        // where the weight itself is near the end of fp16's range.
+        constexpr bool TWO = !KV8 || std::is_same<T, __half>::value;
+        constexpr float REST = KV8 ? 2048.f : 1.f;
         uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                 const uint32_t hi = pack2<M>(x, y);
                 ph[nt][k] = movmatrix_trans(hi);
                 const float2 near = unpacked<M>(hi);
-                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>(x - near.x, y - near.y)) : 0u;
+                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>((x - near.x) * REST, (y - near.y) * REST)) : 0u;
             }
 
         // O^T += V^T P^T
@@ -509,6 +518,11 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
                     const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4431));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                    if constexpr (TWO) {
+                        const uint32_t b0 = by_2_11(a0), b1 = by_2_11(a1), b2 = by_2_11(a2), b3 = by_2_11(a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], b0, b1, b2, b3, pl[nt][0], pl[nt][1]);
+                    }
                 }
             }
         } else {
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_16816<M>(o[md][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                    if constexpr (TWO) mma_16816<M>(o[md][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                    mma_16816<M>(o[md][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                 }
             }
         }
