@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 
     const uint32_t ring_u32 = base_u32 + warp * STAGES * STAGE;
     const uint64_t policy = l2_policy_evict_first();
+    int base = 0;                                      // copies before those of this look at the tiles: 0 in the first look
     auto issue = [&](int it) {
-        const int s = it % STAGES, row = list[it].x;
+        const int s = (base + it) % STAGES, row = list[it].x;
         const uint32_t bar = bars_u32 + (warp * STAGES + s) * 8, dst = ring_u32 + s * STAGE;
         mbar_arrive_expect_tx(bar, STAGE);
         if constexpr (KV8) {
@@ -265,6 +266,21 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     const int seen_by_all = L - p.q_len + 1;           // tokens before this one
 
     float m[NT][2], l[NT][2], o[MT][NT][4];
+    int vexp;                                          // FP8: O is in units of 2^vexp
+    float vlimit;                                      // 2^(vexp + 5), once a token has set the unit
+    // FP8: a tile's scales are loaded while the tile before it is worked on
+    const auto scales_of = [&](int i) {
+        const int row = list[i].x + gq;
+        return make_float4(p.k_scales[row], p.k_scales[row + 8], p.v_scales[row], p.v_scales[row + 8]);
+    };
+    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    // A second look at the tiles where the first leaves an O that is no number. Infinities among V may have done it, whose
+    // products with two parts of a weight (the second 0 or of either sign) need not be theirs with the weight: this time the
+    // tokens that hold no numbers are added apart, in fp32. Looking for them in every tile would cost each call what this costs
+    // none but those.
+    bool ok = true;
+    int it;
+again:
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -272,22 +288,13 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
 #pragma unroll
         for (int md = 0; md < MT; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
     }
-
-    int vexp = 0;                                      // FP8: O is in units of 2^vexp
-    float vlimit = 0.f;                                // 2^(vexp + 5), once a token has set the unit
-    // FP8: a tile's scales are loaded while the tile before it is worked on
-    const auto scales_of = [&](int i) {
-        const int row = list[i].x + gq;
-        return make_float4(p.k_scales[row], p.k_scales[row + 8], p.v_scales[row], p.v_scales[row + 8]);
-    };
-    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    vexp = 0;
+    vlimit = 0.f;
     if (KV8 && tiles > 0) ahead = scales_of(0);
-    bool ok = true;
-    int it = 0;
-    for (; it < tiles; ++it) {
-        const int s = it % STAGES;
+    for (it = 0; it < tiles; ++it) {
+        const int s = (base + it) % STAGES;
         // false: the copy did not land in time. A lane may see it land as another gives up, so the warp leaves by a vote (below).
-        const bool landed = mbar_wait_bounded(bars_u32 + (warp * STAGES + s) * 8, (uint32_t)(it / STAGES) & 1u, p.wait_ns);
+        const bool landed = mbar_wait_bounded(bars_u32 + (warp * STAGES + s) * 8, (uint32_t)((base + it) / STAGES) & 1u, p.wait_ns);
         const int pos = list[it].y;
         const uint32_t kb = ring_u32 + s * STAGE, vb = kb + TILE;
         float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);   // FP8: of K and V of the tokens gq and gq + 8
@@ -340,6 +347,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
         float v0 = fabsf(scale.z), v1 = fabsf(scale.w);
         if (whole < TILE_TOKENS) v0 = gq < whole ? v0 : 0.f, v1 = gq + 8 < whole ? v1 : 0.f;
+        if (KV8 && base > 0) v0 = v0 < INFINITY ? v0 : 0.f, v1 = v1 < INFINITY ? v1 : 0.f;
         const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && whole > 0;
         bool passed = larger || !landed;
 #pragma unroll
@@ -416,9 +424,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
         // The tiles at the end of the context. What lies behind it may be anything: its words of V become 0, its weights are
         // 0 already. So may the value of a token that not every row sees be to the rows that do not: where it is no number
         // (or, FP8, far larger than the rest), the token is added in fp32 to the rows that see it, and its weights and words
-        // become 0 as well.
-        if (whole < TILE_TOKENS) {
-            const int w0 = whole < 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos), some = w1 - w0;
+        // become 0 as well. On the second look that goes for every token.
+        if (whole < TILE_TOKENS || base > 0) {
+            const int w0 = whole < 0 || base > 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos), some = w1 - w0;
             uint8_t *vs = smem + (vb - base_u32);
             uint32_t odd = 0;                          // such tokens
             for (int c = lane; c < some * (TILE / TILE_TOKENS / 16); c += 32) {
@@ -545,9 +553,26 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
             ++issued;
         }
     }
+    if (ok && base == 0) {
+        float odd = 0.f;
+#pragma unroll
+        for (int md = 0; md < MT; ++md)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) odd = fmaf(o[md][nt][k], 0.f, odd);
+        if (__any_sync(0xffffffffu, odd != 0.f)) {
+            base = tiles;
+            issued = min(tiles, STAGES);
+            __syncwarp();
+            if (lane == 0)
+                for (int k = 0; k < issued; ++k) issue(k);
+            goto again;
+        }
+    }
     if (!ok && lane == 0)                              // no copy lands behind the end of the pipeline
         for (int k = it; k < issued; ++k)
-            mbar_wait_bounded(bars_u32 + (warp * STAGES + (k % STAGES)) * 8, (uint32_t)(k / STAGES) & 1u, p.wait_ns);
+            mbar_wait_bounded(bars_u32 + (warp * STAGES + (base + k) % STAGES) * 8, (uint32_t)((base + k) / STAGES) & 1u, p.wait_ns);
 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
