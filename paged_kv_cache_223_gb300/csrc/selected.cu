@@ -30,6 +30,14 @@ constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_MAX_RANKS = 8;
 constexpr int ATT_MAX_TILES = PA_SELECT_MAX_BUDGET * (32 / TILE_TOKENS);   // of a list, in blocks of 32 tokens
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
+// Many small weights beside a large one. fp16 pools: weights (and the sums that they are divided by) are 2^7 as large, below 2^15,
+// so that they keep bits down to 2^-32 of the large one instead of 2^-25. And a product's accumulator drops what lies below its
+// own last bit, so a warp takes 256 tiles at most where a cluster can be made larger, as it can for every list: 4096 tokens below
+// 2^-25 are 2^-13 of the output. (32768 to a warp: 2^-10; equal weights lost as much.) With the limit and without it: 608 lists of
+// 4096 blocks of 32 tokens, shared by all, 2640 and 4340 us (FP8 2600 and 3230), 300 lists of 2048 blocks 757 and 1090 (739 and 658).
+constexpr float ATT_LIFT_LOG2 = 7.f;
+constexpr int ATT_WARP_TILES = 256;
+static_assert(ATT_MAX_TILES <= ATT_WARP_TILES * ATT_WARPS * ATT_MAX_RANKS, "the longest list");
 
 // Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
 // 17.5 -> 17.7 us, 64 of 2048 tokens 44 -> 46), four CTAs with one column of eight rows, else two by registers (16 rows at
@@ -117,6 +125,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     constexpr int W = ATT_WARPS, STAGES = att_stages(KV8);
     constexpr int TILE = att_tile_bytes(D, KV8), STAGE = 2 * TILE;
     constexpr int KS = D / 16, MT = D / 16, RP = NT * 8, OS = D + 4;
+    constexpr float LIFT = std::is_same<M, __half>::value && !KV8 ? ATT_LIFT_LOG2 : 0.f;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -412,7 +421,7 @@ again:
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+                const float ref = (m[nt][j] == -INFINITY ? 0.f : m[nt][j]) - LIFT;
                 // -0 for what is not seen: a sum of nothing keeps its sign, one of weights that are all 0 loses it
                 float p0 = ex2_approx(sc[nt][j] - ref), p1 = ex2_approx(sc[nt][2 + j] - ref);
                 if (whole < TILE_TOKENS) p0 = t0 <= last[nt][j] ? p0 : -0.f, p1 = t1 <= last[nt][j] ? p1 : -0.f;
@@ -710,13 +719,14 @@ static cudaError_t launch_selected_t(SelectedParams p, const CUtensorMap &tmk, c
         const int64_t cost = (units * r + slots - 1) / slots * ((r > 1 ? 6 : 3) + (tiles + r * ATT_WARPS - 1) / (r * ATT_WARPS));
         if (r == 1 || cost < best) best = cost, ranks = r;
     }
+    while (tiles > ranks * ATT_WARPS * ATT_WARP_TILES) ranks *= 2;
     p.warp_tiles = (tiles + ranks * ATT_WARPS - 1) / (ranks * ATT_WARPS);
     const auto launch = [&](auto kernel, int n) {
-        static_assert(att_smem(D, KV8, 4, ATT_MAX_TILES / ATT_WARPS) <= MAX_SMEM_PER_CTA, "a list of the largest budget by one CTA");
+        static_assert(att_smem(D, KV8, 4, ATT_WARP_TILES) <= MAX_SMEM_PER_CTA, "the most tiles of four warps");
         const size_t smem = att_smem(D, KV8, n, p.warp_tiles);
         // the most that any call takes: the attribute is the kernel's, and other threads' calls set it too
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)att_smem(D, KV8, n, ATT_MAX_TILES / ATT_WARPS));
+                                                   (int)att_smem(D, KV8, n, ATT_WARP_TILES));
         return e != cudaSuccess
                    ? e
                    : launch_clusters(kernel, (unsigned)(units * ranks), ATT_THREADS, smem, ranks, stream, tmk, tmv, p);
