@@ -418,8 +418,10 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
  * block listed twice counts twice. A row that sees no listed token gives zeros
  * (so does a context of 0); one whose scores are all -inf gives NaN. Values at positions a row does not see do not reach
  * it, whatever their words are. Softmax and sums are fp32; weights go into the
- * product with V as two parts of 16 bits (2^-17 at most), in FP8 pools with bf16
- * outputs as one (2^-12 of a weight, where the output keeps 2^-9); deterministic
+ * product with V as two parts of 16 bits (2^-16 at most), in FP8 pools with bf16
+ * outputs as one (2^-11 of a weight, where the output keeps 2^-8), whatever the
+ * V scales are as long as they are at most 2^100 and those of a list lie within
+ * 2^100 of each other (or are 0); deterministic
  * run to run. 16-bit pools with heads of 64 or 128 and FP8 pools.
  *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping
  *   selected       device int32 [num_seqs, num_kv_heads, budget]; budget 1 .. PA_SELECT_MAX_BUDGET

@@ -30,13 +30,21 @@ constexpr int ATT_THREADS = ATT_WARPS * 32;
 constexpr int ATT_MAX_RANKS = 8;
 constexpr int ATT_MAX_TILES = PA_SELECT_MAX_BUDGET * (32 / TILE_TOKENS);   // of a list, in blocks of 32 tokens
 constexpr float ATT_RESCALE_LOG2 = 8.f;                // a row's reference maximum moves when it is passed by 2^8
-// Many small weights beside a large one. fp16 pools: weights (and the sums that they are divided by) are 2^7 as large, below 2^15,
+// Many small weights beside a large one. fp16 and FP8 pools: weights (and the sums that they are divided by) are 2^7 as large, below 2^15,
 // so that they keep bits down to 2^-32 of the large one instead of 2^-25. And a product's accumulator drops what lies below its
 // own last bit, so a warp takes 256 tiles at most where a cluster can be made larger, as it can for every list: 4096 tokens below
 // 2^-25 are 2^-13 of the output. (32768 to a warp: 2^-10; equal weights lost as much.) With the limit and without it: 608 lists of
 // 4096 blocks of 32 tokens, shared by all, 2640 and 4340 us (FP8 2600 and 3230), 300 lists of 2048 blocks 757 and 1090 (739 and 658).
 constexpr float ATT_LIFT_LOG2 = 7.f;
 constexpr int ATT_WARP_TILES = 256;
+// FP8: a weight goes into the product times its V scale, as fp16 (below 2^15), in a unit 2^vexp that follows the scales. The
+// largest one of a tile sets it, with 2^2 of room above, and sets it anew where a scale passes it or lies below its 2^-6 (weights
+// in one part of fp16) or 2^-14 (two parts); tokens that then still lie below are added apart, in fp32. So a weight is off by 2^-11
+// of itself in one part and 2^-22 in two, or by 2^-26 and 2^-29 of the row's largest, and no token's scale costs another one its
+// bits, whatever their weights are. The unit stays within 2^80 of the largest that it was, so that O stays in fp32's range. Of
+// scales near each other, 8, 16, 32 rows of 64 sequences: bf16 44.9, 60.8, 86.3 -> 46.5, 61.4, 85.6 us, fp16 47.2, 70.9, 109 -> 47.5,
+// 70.4, 107.
+constexpr int ATT_ROOM_ABOVE = 2, ATT_ROOM_ONE = 6, ATT_ROOM_TWO = 14, ATT_MIN_UNIT = -110, ATT_MAX_UNIT = 119, ATT_UNIT_SPAN = 80;
 static_assert(ATT_MAX_TILES <= ATT_WARP_TILES * ATT_WARPS * ATT_MAX_RANKS, "the longest list");
 
 // Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
@@ -125,7 +133,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     constexpr int W = ATT_WARPS, STAGES = att_stages(KV8);
     constexpr int TILE = att_tile_bytes(D, KV8), STAGE = 2 * TILE;
     constexpr int KS = D / 16, MT = D / 16, RP = NT * 8, OS = D + 4;
-    constexpr float LIFT = std::is_same<M, __half>::value && !KV8 ? ATT_LIFT_LOG2 : 0.f;
+    constexpr float LIFT = std::is_same<M, __half>::value ? ATT_LIFT_LOG2 : 0.f;
+    constexpr bool TWO = !KV8 || std::is_same<T, __half>::value;   // weights in two parts in every tile
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -275,8 +284,8 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(KV8, NT))
     const int seen_by_all = L - p.q_len + 1;           // tokens before this one
 
     float m[NT][2], l[NT][2], o[MT][NT][4];
-    int vexp;                                          // FP8: O is in units of 2^vexp
-    float vlimit;                                      // 2^(vexp + 5), once a token has set the unit
+    int vexp, vmost;                                   // FP8: O is in units of 2^vexp, at most 2^vmost
+    uint32_t vlow;                                     // the smallest V scale in the unit's room, as bits; the sign's: no unit yet
     // FP8: a tile's scales are loaded while the tile before it is worked on
     const auto scales_of = [&](int i) {
         const int row = list[i].x + gq;
@@ -297,8 +306,8 @@ again:
 #pragma unroll
         for (int md = 0; md < MT; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
     }
-    vexp = 0;
-    vlimit = 0.f;
+    vexp = 0, vmost = ATT_MIN_UNIT;
+    vlow = 0x80000000u;
     if (KV8 && tiles > 0) ahead = scales_of(0);
     for (it = 0; it < tiles; ++it) {
         const int s = (base + it) % STAGES;
@@ -351,14 +360,15 @@ again:
         // softmax, in powers of two: weights are relative to a reference that moves only when it is passed by 2^8, which the
         // warp asks for all its columns (and the V scales) at once; the columns' maxima are looked for only then
         const int t0 = pos + gq, t1 = t0 + 8;
-        // FP8: weights times V scales go into the product as fp16, in units of a power of two: below 2^8 times 2^5; the unit
-        // follows the scales of the tokens that every row sees (the others are added apart where they are larger)
         const int whole = seen_by_all - pos;           // tokens of the tile that every row sees
-        float v0 = fabsf(scale.z), v1 = fabsf(scale.w);
-        if (whole < TILE_TOKENS) v0 = gq < whole ? v0 : 0.f, v1 = gq + 8 < whole ? v1 : 0.f;
-        if (KV8 && base > 0) v0 = v0 < INFINITY ? v0 : 0.f, v1 = v1 < INFINITY ? v1 : 0.f;
-        const bool larger = KV8 && !(fmaxf(v0, v1) < vlimit) && whole > 0;
-        bool passed = larger || !landed;
+        // FP8: does one of their V scales lie outside of the unit's room? Their order is that of their bits.
+        constexpr uint32_t ROOM = (uint32_t)(TWO ? ATT_ROOM_TWO : ATT_ROOM_ONE) << 23;
+        uint32_t v0 = __float_as_uint(scale.z) & 0x7FFFFFFFu, v1 = __float_as_uint(scale.w) & 0x7FFFFFFFu;
+        if (whole < TILE_TOKENS) v0 = gq < whole ? v0 : vlow, v1 = gq + 8 < whole ? v1 : vlow;
+        const bool outside = KV8 && max(v0 - vlow, v1 - vlow) >= ROOM && whole > 0;
+        uint32_t apart = 0;                            // tokens to be added apart
+        bool rest = TWO;                               // a second part of the weights
+        bool passed = outside || !landed;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -385,18 +395,26 @@ again:
                 ok = false;
                 break;
             }
-            if (__any_sync(0xffffffffu, larger)) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v0), __float_as_uint(v1)));
-                const int e = min(max((int)(top >> 23) - 127, -60), 100);
-                const float f = ldexpf(1.f, vexp - e);
+            if (__any_sync(0xffffffffu, outside)) {
+                v0 = gq < whole && v0 < 0x7F800000u ? v0 : 0u, v1 = gq + 8 < whole && v1 < 0x7F800000u ? v1 : 0u;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(v0, v1));
+                int e = min(max((int)(top >> 23) - 126 + ATT_ROOM_ABOVE, ATT_MIN_UNIT), ATT_MAX_UNIT);
+                e = max(e, vmost - ATT_UNIT_SPAN);
+                if (top && (e < vexp || top - vlow >= ROOM)) {
+                    const float f = ldexpf(1.f, vexp - e);
 #pragma unroll
-                for (int md = 0; md < MT; ++md)
+                    for (int md = 0; md < MT; ++md)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[md][nt][k] *= f;
-                vexp = e;
-                vlimit = __uint_as_float((uint32_t)(127 + e + 5) << 23);
+                            for (int k = 0; k < 4; ++k) o[md][nt][k] *= f;
+                    vexp = e, vmost = max(vmost, e);
+                    vlow = ((uint32_t)(127 + e) << 23) - ROOM;
+                }
+                // a scale of 0 has nothing to lose
+                const uint32_t two = vlow + ROOM - ((uint32_t)ATT_ROOM_ONE << 23), none = vlow + ROOM - ((uint32_t)ATT_ROOM_TWO << 23);
+                rest = TWO || __any_sync(0xffffffffu, v0 - 1 < two - 1 || v1 - 1 < two - 1);
+                apart = __reduce_or_sync(0xffffffffu, (uint32_t)(v0 - 1 < none - 1) << gq | (uint32_t)(v1 - 1 < none - 1) << (gq + 8));
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -432,12 +450,12 @@ again:
 
         // The tiles at the end of the context. What lies behind it may be anything: its words of V become 0, its weights are
         // 0 already. So may the value of a token that not every row sees be to the rows that do not: where it is no number
-        // (or, FP8, far larger than the rest), the token is added in fp32 to the rows that see it, and its weights and words
-        // become 0 as well. On the second look that goes for every token.
-        if (whole < TILE_TOKENS || base > 0) {
+        // (or, FP8, has a scale outside of the unit's room), the token is added in fp32 to the rows that see it, and its weights
+        // and words become 0 as well. On the second look that goes for every token.
+        if (whole < TILE_TOKENS || base > 0 || apart) {
             const int w0 = whole < 0 || base > 0 ? 0 : whole, w1 = min(TILE_TOKENS, L - pos), some = w1 - w0;
             uint8_t *vs = smem + (vb - base_u32);
-            uint32_t odd = 0;                          // such tokens
+            uint32_t odd = apart;                      // such tokens
             for (int c = lane; c < some * (TILE / TILE_TOKENS / 16); c += 32) {
                 const int row = w0 + c % some, chunk = c / some;
                 const uint4 x = *reinterpret_cast<const uint4 *>(vs + tile_at<D, KV8>(row, chunk));
@@ -445,8 +463,8 @@ again:
                 odd |= (uint32_t)is << row;
             }
             if constexpr (KV8) {
-                if (gq >= w0 && gq < w1) odd |= (uint32_t)!(fabsf(scale.z) < vlimit) << gq;
-                if (gq + 8 >= w0 && gq + 8 < w1) odd |= (uint32_t)!(fabsf(scale.w) < vlimit) << (gq + 8);
+                if (gq >= w0 && gq < w1) odd |= (uint32_t)((__float_as_uint(scale.z) & 0x7FFFFFFFu) - vlow >= ROOM) << gq;
+                if (gq + 8 >= w0 && gq + 8 < w1) odd |= (uint32_t)((__float_as_uint(scale.w) & 0x7FFFFFFFu) - vlow >= ROOM) << (gq + 8);
             }
             odd = __reduce_or_sync(0xffffffffu, odd);
             for (uint32_t left = odd; left; left &= left - 1) {
@@ -497,64 +515,72 @@ again:
                 }
         }
 
-        // P^T as the B operand, in V's type, as two parts: the nearest number and what is left of it. bf16's eight bits would not
-        // do, and fp16's eleven alone made the error of fp16 outputs 1.3 to 1.4 times the last rounding's (16-bit pools, 64
-        // sequences of 2048 tokens: 84.5 -> 85.8 us for the second part; FP8, 8, 16, 32 rows: 44.2, 59.6, 86.4 -> 46.8, 70.6,
-        // 100.5 us). The bf16 outputs of FP8 pools keep eight bits, 2^-9 beside the weights' 2^-12: one part. FP8 pools take the
-        // second part 2^11 times as large, against V by 2^-11 (exact: codes are multiples of 2^-9), so that it keeps its bits
-        // where the weight itself is near the end of fp16's range.
-        constexpr bool TWO = !KV8 || std::is_same<T, __half>::value;
-        constexpr float REST = KV8 ? 2048.f : 1.f;
-        uint32_t ph[NT][2], pl[NT][2];
+        // O^T += V^T P^T with P^T as the B operand, in V's type, as two parts: the nearest number and what is left of it. bf16's eight
+        // bits would not do, and fp16's eleven alone made the error of fp16 outputs 1.3 to 1.4 times the last rounding's (16-bit
+        // pools, 64 sequences of 2048 tokens: 84.5 -> 85.8 us for the second part; FP8, 8, 16, 32 rows: 44.2, 59.6, 86.4 -> 46.8,
+        // 70.6, 100.5 us). The bf16 outputs of FP8 pools keep eight bits, 2^-8 beside the weights' 2^-11: one part, but in tiles
+        // whose V scales lie far apart. FP8 pools take the second part 2^11 times as large, against V by 2^-11 (exact: codes are
+        // multiples of 2^-9), so that it keeps its bits where the weight itself is near the end of fp16's range.
+        // parts: 1 the nearest numbers, 2 what is left of the weights, 3 both
+        const auto product = [&](auto parts) {
+            constexpr bool NEAR = decltype(parts)::value & 1, REST = decltype(parts)::value & 2;
+            constexpr float LARGER = KV8 ? 2048.f : 1.f;
+            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float x = sc[nt][2 * k], y = sc[nt][2 * k + 1];
-                const uint32_t hi = pack2<M>(x, y);
-                ph[nt][k] = movmatrix_trans(hi);
-                const float2 near = unpacked<M>(hi);
-                pl[nt][k] = TWO ? movmatrix_trans(pack2<M>((x - near.x) * REST, (y - near.y) * REST)) : 0u;
-            }
-
-        // O^T += V^T P^T
-        if constexpr (KV8) {
-            // a lane gets two keys of two neighbouring dimensions: the even ones are rows 0-7 of the fragment, the odd 8-15
-            const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+                for (int k = 0; k < 2; ++k) {
+                    const float x = sc[nt][2 * k], y = sc[nt][2 * k + 1];
+                    const uint32_t hi = pack2<M>(x, y);
+                    ph[nt][k] = NEAR ? movmatrix_trans(hi) : 0u;
+                    const float2 near = unpacked<M>(hi);
+                    pl[nt][k] = REST ? movmatrix_trans(pack2<M>((x - near.x) * LARGER, (y - near.y) * LARGER)) : 0u;
+                }
+            if constexpr (KV8) {
+                // a lane gets two keys of two neighbouring dimensions: the even ones are rows 0-7 of the fragment, the odd 8-15
+                const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-            for (int mp = 0; mp < MT / 2; ++mp) {
-                const int chunk = mp * 2 + (lane >> 4);
-                uint32_t r[4];
-                ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), r[0], r[1], r[2], r[3]);
+                for (int mp = 0; mp < MT / 2; ++mp) {
+                    const int chunk = mp * 2 + (lane >> 4);
+                    uint32_t r[4];
+                    ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), r[0], r[1], r[2], r[3]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t lo = r[2 * h], hi = r[2 * h + 1];
-                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4420));
-                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4431));
-                    const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4420));
-                    const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4431));
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t lo = r[2 * h], hi = r[2 * h + 1];
+                        const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4420));
+                        const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)__byte_perm(lo, 0u, 0x4431));
+                        const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4420));
+                        const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(hi, 0u, 0x4431));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                    if constexpr (TWO) {
-                        const uint32_t b0 = by_2_11(a0), b1 = by_2_11(a1), b2 = by_2_11(a2), b3 = by_2_11(a3);
+                        for (int nt = 0; nt < NT; ++nt)
+                            if constexpr (NEAR) mma_16816<M>(o[2 * mp + h][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                        if constexpr (REST) {
+                            const uint32_t b0 = by_2_11(a0), b1 = by_2_11(a1), b2 = by_2_11(a2), b3 = by_2_11(a3);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], b0, b1, b2, b3, pl[nt][0], pl[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma_16816<M>(o[2 * mp + h][nt], b0, b1, b2, b3, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+                }
+            } else {
+                const int vrow = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+                for (int md = 0; md < MT; ++md) {
+                    const int chunk = md * 2 + ((lane >> 3) & 1);
+                    uint32_t a0, a1, a2, a3;
+                    ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), a0, a1, a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816<M>(o[md][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                        if constexpr (REST) mma_16816<M>(o[md][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                     }
                 }
             }
+        };
+        if constexpr (TWO) {
+            product(std::integral_constant<int, 3>());
         } else {
-            const int vrow = (lane & 7) + (lane >> 4) * 8;
-#pragma unroll
-            for (int md = 0; md < MT; ++md) {
-                const int chunk = md * 2 + ((lane >> 3) & 1);
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4_trans(vb + tile_at<D, KV8>(vrow, chunk), a0, a1, a2, a3);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816<M>(o[md][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                    mma_16816<M>(o[md][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-                }
-            }
+            if (rest) product(std::integral_constant<int, 2>());
+            product(std::integral_constant<int, 1>());
         }
         __syncwarp();
         if (it + STAGES < tiles) {
