@@ -315,9 +315,10 @@ pa_status pa_prefill_packed(pa_pool *pool, const void *q, const void *k_cache, c
  * A negative length, a sequence longer than its table row (or 2^29 tokens),
  * more new tokens than num_tokens, or *num_free outside what the pool's blocks
  * allow is flagged (PA_ERR_DEVICE_BOUNDS at pa_pool_check), more blocks than are
- * free is flagged as PA_ERR_OOM: tables, lengths and stack are then left as they
- * are, and the step has no tokens (cu_q all 0, positions 0, slots -1). A block id
- * outside the pool is flagged, its tokens' slots are -1.
+ * free is flagged as PA_ERR_OOM: tables, lengths and the stack's blocks are then
+ * left as they are, and the step has no tokens (cu_q all 0, positions 0, slots -1).
+ * So is a step that would return a block id outside the pool (PA_ERR_DEVICE_BOUNDS).
+ * Another one outside the pool is flagged, its tokens' slots are -1.
  */
 #define PA_TABLES_MAX_SEQS 8192
 #define PA_TABLES_MAX_TOKENS 536870912

@@ -8,13 +8,15 @@
 // block i lies at n + F - 1 - i, taken block i comes from n + F - 1 - i. Cutting back what a step took and taking it
 // again therefore gives the same blocks.
 //
-// One cluster does all of it (the tokens of large calls apart): every CTA makes the sums of all sequences for itself (they are few words), checks them and
-// comes to the same verdict, the CTAs share the returned blocks, meet at the cluster's barrier, and share the taken blocks,
-// the tokens and the new lengths. So the lengths, tables and the stack are changed in place by one launch without a
-// workspace, and a call that is refused changes nothing of them.
+// One cluster does all of it (the tokens of large calls apart): every CTA makes the sums of all sequences for itself (they are
+// few words), checks them and comes to the same verdict, the CTAs share the returned blocks, meet at the cluster's barrier
+// (twice, for a verdict on the returned ids), and share the taken blocks, the tokens and the new lengths. So the lengths,
+// tables and the stack are changed in place by one launch without a workspace, and a call that is refused changes nothing of
+// them.
 //
-// Bound by latency: one request 3.3 us (launch, two trips to memory); 257 sequences of a verify with cuts and ended requests 5.6
-// us (four trips, two searches, the barrier); 2000 prompts of 292000 tokens, 40000 blocks moved: 15.5 us, two launches.
+// Bound by latency: one request 3.4 us (launch, two trips to memory); 257 sequences of a verify with cuts and ended requests 6.2
+// us (four trips, two searches, the barriers); 2000 prompts of 292000 tokens, 40000 blocks moved: 16.1 us, two launches, 14.4 in
+// a graph.
 #include <algorithm>
 
 #include "pa_cluster.cuh"
@@ -112,13 +114,14 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     int *cu = tsm, *back = cu + B + 1, *taken = back + B + 1, *kept = taken + B + 1;   // sums of B + 1, then [B]
     __shared__ Sums wsum[TAB_THREADS / 32];
     __shared__ int bad;
+    __shared__ uint32_t bad_id;                        // set by any CTA of the cluster
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int all = threads * ranks, gid = rank * threads + tid;
     pdl_trigger();
     pdl_wait();
 
-    if (tid == 0) bad = 0;
+    if (tid == 0) bad = 0, bad_id = 0;
     __syncthreads();
     const int bs = 1 << p.bs_shift;
     const int n_free = __ldcg(p.num_free);
@@ -167,15 +170,18 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     const bool wrong = bad || n_free < 0 || n_free > p.num_blocks || n_free + carry.back > p.num_blocks ||
                        carry.tokens > p.num_tokens;
     const bool none_left = !wrong && carry.taken > n_free + carry.back;
-    if (wrong || none_left) {                          // the same in every CTA: no table, length or block is touched
-        if (gid == 0) set_status(p.status, wrong ? STATUS_BOUNDS : STATUS_NO_BLOCKS);
+    const auto refuse = [&] {                          // by the same verdict in every CTA: no table, length or block is touched
         for (int b = gid; b <= B; b += all) p.cu_q[b] = 0;
         for (int i = gid; i < p.num_tokens && !p.tokens_apart; i += all) {
             p.positions[i] = 0;
             p.slots[i] = -1;
         }
-        return;
+    };
+    if (wrong || none_left) {
+        if (gid == 0) set_status(p.status, wrong ? STATUS_BOUNDS : STATUS_NO_BLOCKS);
+        return refuse();
     }
+    cluster_arrive();                                  // this CTA has read the lengths and set its word
     const int tokens = (int)carry.tokens, F = (int)carry.back, T = (int)carry.taken, top = n_free + F - 1;
     if (tid == 0) {
         cu[B] = tokens;
@@ -184,15 +190,28 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesParams 
     }
     __syncthreads();
 
-    // returned blocks onto the stack
-    for (int i = gid; i < F; i += all) {
-        const int b = owner(back, B, i);
-        const int j = ((kept[b] + bs - 1) >> p.bs_shift) + i - back[b];
-        const int id = __ldcg(p.block_tables + b * p.stride + j);
-        if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
-        __stcg(p.free_blocks + top - i, id);
+    // returned blocks onto the stack, above *num_free, where nothing is lost if the step is refused after all: an id outside the
+    // pool would go from one sequence to the next. Whoever finds one tells every CTA, which takes a barrier more (257 sequences
+    // of a verify 5.6 -> 6.2 us; a step that returns nothing has one barrier as before).
+    if (F > 0) {
+        bool odd = false;
+        for (int i = gid; i < F; i += all) {
+            const int b = owner(back, B, i);
+            const int j = ((kept[b] + bs - 1) >> p.bs_shift) + i - back[b];
+            const int id = __ldcg(p.block_tables + b * p.stride + j);
+            odd |= id < 0 || id >= p.num_blocks;
+            __stcg(p.free_blocks + top - i, id);
+        }
+        cluster_wait();
+        if (odd) {
+            set_status(p.status, STATUS_BOUNDS);
+            for (int r = 0; r < ranks; ++r) red_cluster_max(map_rank(smem_u32(&bad_id), r), 1u);
+        }
+        __syncwarp();
+        cluster_arrive();
     }
-    cluster_sync();                                    // every CTA has read the lengths; the stack is whole
+    cluster_wait();                                    // every CTA has read the lengths; the stack is whole
+    if (bad_id) return refuse();
 
     for (int i = gid; i < T; i += all) {
         const int b = owner(taken, B, i);
@@ -237,8 +256,9 @@ cudaError_t launch_tables(TablesParams p, int sm_count, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     p.vectors = (reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
     p.tokens_apart = p.num_tokens > TAB_MAX_TOKENS;
-    // CTAs of the cluster: eight even for small steps, whose lengths are known on the device only (257 sequences: 5.6 us, a
-    // single CTA 6.5; one request 3.3 and 3.9), 16 in front of the tokens' kernel (2000 prompts: 14.0 us, eight 15.5)
+    // CTAs of the cluster: eight even for small steps, whose lengths are known on the device only (257 sequences, before the
+    // barrier for returned ids: 5.6 us, a single CTA 6.5; one request 3.3 and 3.9), 16 in front of the tokens' kernel (2000
+    // prompts in a graph: 14.4 us, eight 16.0; in a stream 16.1 and 16.2)
     const int ranks = p.tokens_apart ? 16 : 8;
     if (ranks > 8) e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
