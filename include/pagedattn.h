@@ -43,7 +43,7 @@ typedef enum pa_status {
     PA_ERR_INVALID_ARG = 1,    /* bad pointer, size, alignment or geometry; nothing launched */
     PA_ERR_UNSUPPORTED = 2,    /* valid but not built (e.g. head_dim not in {64, 128}) */
     PA_ERR_CUDA = 3,           /* a CUDA runtime or driver call failed */
-    PA_ERR_OOM = 4,            /* pa_pool_create could not allocate */
+    PA_ERR_OOM = 4,            /* pa_pool_create could not allocate; too few free blocks (pa_allocator_*, pa_step_tables) */
     PA_ERR_DEVICE_BOUNDS = 5,  /* pa_pool_check: a kernel saw an out-of-range block id, slot or length */
     PA_ERR_TIMEOUT = 6         /* pa_pool_check: a kernel gave up waiting on a copy (bounded wait) */
 } pa_status;
@@ -439,7 +439,8 @@ pa_status pa_decode_selected(pa_pool *pool, const void *q, const void *k_cache, 
 /*
  * Synchronise the device, read and clear the pool's status word.
  * Returns PA_OK, PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT, PA_ERR_OOM (pa_step_tables:
- * a step needed more blocks than were free) or PA_ERR_CUDA.
+ * a step needed more blocks than were free) or PA_ERR_CUDA. Of a step without
+ * blocks beside one of the first two, the next call tells.
  */
 pa_status pa_pool_check(pa_pool *pool, void *stream);
 

@@ -82,7 +82,7 @@ const char *pa_status_string(pa_status s) {
         case PA_ERR_INVALID_ARG: return "invalid argument";
         case PA_ERR_UNSUPPORTED: return "unsupported configuration";
         case PA_ERR_CUDA: return "CUDA error";
-        case PA_ERR_OOM: return "out of device memory";
+        case PA_ERR_OOM: return "out of device memory or of free blocks";
         case PA_ERR_DEVICE_BOUNDS: return "device saw an out-of-range block id, slot or context length";
         case PA_ERR_TIMEOUT: return "device gave up waiting on a copy";
     }
@@ -501,8 +501,12 @@ pa_status pa_pool_check(pa_pool *pool, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int h = 0;
     if (cudaMemcpyAsync(&h, pool->status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess || cudaMemsetAsync(pool->status, 0, sizeof(int), s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
+        return PA_ERR_CUDA;
+    // a step without blocks stays in the word (its low byte) beside what is told first
+    const int rest = h & (STATUS_TIMEOUT | STATUS_BOUNDS) ? h & STATUS_NO_BLOCKS : 0;
+    if (cudaMemsetAsync(pool->status, 0, sizeof(int), s) != cudaSuccess ||
+        (rest && cudaMemsetAsync(pool->status, rest, 1, s) != cudaSuccess) || cudaStreamSynchronize(s) != cudaSuccess)
         return PA_ERR_CUDA;
     if (h & STATUS_TIMEOUT) return PA_ERR_TIMEOUT;
     if (h & STATUS_BOUNDS) return PA_ERR_DEVICE_BOUNDS;

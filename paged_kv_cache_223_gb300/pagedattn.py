@@ -632,7 +632,8 @@ class Pool:
         _check(lib().pa_pool_selftest_wait(self.handle, limit_ns, _stream(stream)), "pa_pool_selftest_wait")
 
     def check(self, stream: Optional[torch.cuda.Stream] = None) -> int:
-        """Synchronise and return (and clear) the device status: PA_OK, PA_ERR_DEVICE_BOUNDS or PA_ERR_TIMEOUT."""
+        """Synchronise and return (and clear) the device status: PA_OK, PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT or PA_ERR_OOM (a step
+        of step_tables without blocks; beside one of the others the next call tells it)."""
         return lib().pa_pool_check(self.handle, _stream(stream))
 
 
