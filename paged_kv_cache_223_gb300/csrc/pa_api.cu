@@ -48,8 +48,7 @@ pa_status pa::tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
     CUresult r = fn(&m, ty, 2, const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return PA_ERR_CUDA;
-    if (pool->maps.size() > 4096) pool->maps.clear();
-    pool->maps.emplace(cache, m);
+    keep_map(pool->maps, cache, m);
     *out = m;
     return PA_OK;
 }

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <new>
 #include <unordered_map>
 
 #include "pa_internal.h"
@@ -49,6 +50,15 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // cuTensorMapEncodeTiled, looked up once (nullptr: the driver has none).
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+// Keeps a map for the next call. Without memory for that it is made anew then: no exception leaves a C entry.
+inline void keep_map(std::unordered_map<const void *, CUtensorMap> &maps, const void *cache, const CUtensorMap &m) {
+    if (maps.size() > 4096) maps.clear();
+    try {
+        maps.emplace(cache, m);
+    } catch (const std::bad_alloc &) {
+    }
+}
 
 // The map of one of the pool's caches for copies of 16 token rows, kept per cache address.
 pa_status tensor_map(pa_pool *pool, const void *cache, CUtensorMap *out);

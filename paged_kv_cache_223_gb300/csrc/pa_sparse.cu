@@ -27,8 +27,7 @@ pa_status pa::group_map(pa_pool *pool, const void *cache, CUtensorMap *out) {
            const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return PA_ERR_CUDA;
-    if (pool->group_maps.size() > 4096) pool->group_maps.clear();
-    pool->group_maps.emplace(cache, m);
+    keep_map(pool->group_maps, cache, m);
     *out = m;
     return PA_OK;
 }
