@@ -383,7 +383,11 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_kernel(const Sel
     const int n = (len + p.bs - 1) / p.bs;
     int32_t *out = p.selected + (int64_t)unit * p.budget;
     if (n <= p.budget) {                               // all of them (the same in every CTA of the cluster)
-        for (int i = rank * THREADS + tid; i < p.budget; i += ranks * THREADS) out[i] = i < n ? i : -1;
+        for (int i = rank * THREADS + tid; i < p.budget; i += ranks * THREADS) {
+            out[i] = i < n ? i : -1;
+            const int id = i >= n ? 0 : ranks == 1 ? (int)keys[i] : trow[i];   // keys[i]: this thread's own
+            if (id < 0 || id >= p.num_blocks) set_status(p.status, STATUS_BOUNDS);
+        }
         return;
     }
     // blocks of this CTA, shared out evenly in tiles of 16; those of [lo, hi) are chosen by score, the others always
