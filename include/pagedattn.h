@@ -363,8 +363,9 @@ pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
  * their K is in the pool already); the bounds of every block that holds one of
  * them are made anew from all its tokens before context_lens[b]. Other blocks'
  * bounds are left as they are: a block filled without such a call (by
- * pa_copy_blocks, say) keeps those that it had, until its next token. 16-bit and
- * FP8 pools.
+ * pa_copy_blocks, say) keeps those that it had, until its next token or a call that
+ * counts its tokens among the newest (as many as the context holds, new or not).
+ * 16-bit and FP8 pools.
  *   k_cache        device pool, or NULL for the pool's own
  *   cu_q           device int32 [num_seqs + 1], 0 <= cu_q[b] <= cu_q[b+1] <= num_tokens
  *   block_tables   device int32 [num_seqs, block_table_stride]
@@ -373,8 +374,9 @@ pa_status pa_key_bounds_size(const pa_pool *pool, uint64_t *bytes);
  *   bounds         device, 32-byte aligned, pa_key_bounds_size() bytes
  * Lengths and block ids that do not fit are flagged (PA_ERR_DEVICE_BOUNDS at
  * pa_pool_check), the sequence or block is skipped, where cu_q decreases
- * possibly every sequence. Two sequences that name one
- * block with different fillings: whose bounds land is unspecified.
+ * possibly every sequence. Where two sequences name one block with different
+ * fillings, its codes and step may be a mixture of both, the bounds of neither: one
+ * of them makes them anew before they are used.
  */
 pa_status pa_key_bounds(pa_pool *pool, const void *k_cache, const int32_t *cu_q, const int32_t *block_tables,
                         int32_t block_table_stride, const int32_t *context_lens, int32_t num_tokens, int32_t num_seqs,
@@ -417,13 +419,14 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
  * blocks selected[b][h / (num_q_heads / num_kv_heads)][0 .. budget). The list is
  * pa_select_blocks's or any other, in any order; negative entries are skipped, a
  * block listed twice counts twice. A row that sees no listed token gives zeros
- * (so does a context of 0); one whose scores are all -inf gives NaN. Values at positions a row does not see do not reach
- * it, whatever their words are. Softmax and sums are fp32; weights go into the
- * product with V as two parts of 16 bits (2^-16 at most), in FP8 pools with bf16
- * outputs as one (2^-11 of a weight, where the output keeps 2^-8), whatever the
- * V scales are as long as they are at most 2^100 and those of a list lie within
- * 2^100 of each other (or are 0); deterministic
- * run to run. 16-bit pools with heads of 64 or 128 and FP8 pools.
+ * (so does a context of 0); one whose scores are all -inf gives NaN. An infinity
+ * among the values that a row sees gives it that infinity. Values at positions a
+ * row does not see do not reach it, whatever their words are. Softmax and sums are
+ * fp32; weights go into the product with V as two parts of 16 bits (off by 2^-16 of
+ * themselves at most), in FP8 pools with bf16 outputs as one (2^-11, where the output
+ * keeps 2^-8), whatever the V scales are as long as they are at most 2^100 and those
+ * of a list lie within 2^100 of each other (or are 0). Deterministic run to run.
+ * 16-bit pools with heads of 64 or 128 and FP8 pools.
  *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping
  *   selected       device int32 [num_seqs, num_kv_heads, budget]; budget 1 .. PA_SELECT_MAX_BUDGET
  *   scale          softmax scale; finite, and so times log2(e)
