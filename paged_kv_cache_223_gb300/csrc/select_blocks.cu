@@ -276,7 +276,9 @@ cudaError_t launch_key_bounds(const BoundsParams &p, int dtype, int head_dim, in
 
 constexpr int SEL_WARPS = 8;
 constexpr int SEL_THREADS = SEL_WARPS * 32;
-constexpr int SEL_CTAS = 4;                            // per SM
+// Per SM: 64 registers a thread, of which heads of 128 spill 4 bytes with up to 8 query rows, 16 with 17 to 24 and 72 with more,
+// heads of 64 12 bytes with 17 to 24. Three CTAs, which spill nothing: 64 sequences of 1024 blocks 27.0 -> 36.5 us.
+constexpr int SEL_CTAS = 4;
 constexpr int SEL_BINS = 256;
 static_assert(SEL_BINS == SEL_THREADS, "one bin per thread");
 constexpr int SEL_MAX_RANKS = 16;
@@ -606,11 +608,20 @@ template <typename T, int D>
 static cudaError_t launch_select_t(SelectParams p, int sm_count, cudaStream_t stream) {
     const int blocks = (p.max_len + p.bs - 1) / p.bs, tiles = (blocks + 15) / 16;
     const int64_t units = (int64_t)p.num_seqs * p.Hkv;
-    // CTAs of a cluster: enough for two on each SM, each with a tile for every warp; more where the keys need the room. By 1, 2,
-    // 4, 8, 16 CTAs, us: one sequence of 8192 blocks 71, 40, 23, 16, 14.8; 64 of 1024 26, 37, 51, 86, 240; 13 of up to 1875
-    // 13.7, 13.5, 12.1, 12.3, 18.
-    int ranks = 1;
-    while (ranks < SEL_MAX_RANKS && ((units * ranks < 2LL * sm_count && tiles > ranks * SEL_WARPS) || tiles > ranks * SEL_MAX_TILES)) ranks *= 2;
+    // CTAs of a cluster, by what one takes, in units of 5 ns: a warp's tiles of 16 blocks, 1 us each, for every round of resident
+    // CTAs; 2 us for the barriers and histograms of a cluster; and what the CTAs that start and meet cost, of all units and of one.
+    // Over 290 shapes (8 to 512 units, 130 to 8192 blocks, 4 to 32 rows, heads of 64 and 128) this picks the best of 1, 2, 4, 8, 16
+    // but for 1.2% on average, 22% at most. "Two CTAs on each SM, each with a tile for every warp" lost 15% and up to 72%: 128
+    // units of 160 blocks take 7.2 us as single CTAs, 10.7 as clusters of two; 64 of 4096 48 and, of eight, 23.6; 8 of 8192 71
+    // and, of sixteen, 14.8.
+    int ranks = SEL_MAX_RANKS;
+    int64_t best = -1;
+    for (int r = 1; r <= SEL_MAX_RANKS; r *= 2) {
+        if (tiles > r * SEL_MAX_TILES) continue;       // no room for the keys
+        const int64_t rounds = (units * r + SEL_CTAS * sm_count - 1) / (SEL_CTAS * sm_count);
+        const int64_t cost = 200 * rounds * ((tiles + r * SEL_WARPS - 1) / (r * SEL_WARPS)) + (r > 1 ? 400 : 0) + (units + 24) * r;
+        if (best < 0 || cost < best) best = cost, ranks = r;
+    }
     p.chunk = (tiles + ranks - 1) / ranks * 16;
     const auto launch = [&](auto kernel, int nt) {
         static_assert(sel_smem(D, 4, SEL_MAX_TILES * 16) <= MAX_SMEM_PER_CTA, "the keys of the longest row");
