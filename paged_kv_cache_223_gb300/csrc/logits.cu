@@ -33,6 +33,7 @@
 // to 20 us more), the logits prefetched into L2 one round of blocks ahead and loaded behind the lists (150 us), the
 // lists read once for six rows that a cluster takes in turn (161 us), asynchronous copies of the listed logits and
 // of the biases into shared memory (160 us).
+#include "pa_cluster.cuh"
 #include "pa_device.cuh"
 #include "pa_serving.h"
 
@@ -177,11 +178,6 @@ __device__ __forceinline__ void send_part(RowPart (*parts)[LG_THREADS / 32], int
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4), "f"(x.s) : "memory");
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there + 8), "r"(x.best) : "memory");
 }
-
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // NG groups of four values per thread. VEC: the four are consecutive (16- or 8-byte loads, 16-byte stores);
 // else LG_THREADS apart, each access coalesced on its own (rows that start between vectors).
