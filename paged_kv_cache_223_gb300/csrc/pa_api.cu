@@ -1,7 +1,7 @@
 // pa_api.cu -- the C ABI declared in include/pagedattn.h: pool lifecycle, argument
 // validation, TMA descriptor encoding and kernel launches (the serving operators'
-// in pa_serving.cu, the sparse decode step's in pa_sparse.cu). No computation happens here; every step of the path runs in the
-// kernels of cache_write.cu and decode.cu.
+// in pa_serving.cu, the sparse decode step's in pa_sparse.cu). No computation happens here;
+// every step of the path runs in the kernels of cache_write.cu and decode.cu.
 #include <cmath>
 
 #include "pa_pool.h"
