@@ -424,7 +424,7 @@ pa_status pa_select_blocks(pa_pool *pool, const void *q, const void *bounds, con
  * row does not see do not reach it, whatever their words are. Softmax and sums are
  * fp32; weights go into the product with V as two parts of 16 bits (off by 2^-16 of
  * themselves at most), in FP8 pools with bf16 outputs as one (2^-11, where the output
- * keeps 2^-8), whatever the V scales are as long as they are at most 2^100 and those
+ * keeps 2^-8), whatever the V scales are as long as they are at most 2^90 and those
  * of a list lie within 2^100 of each other (or are 0). Deterministic run to run.
  * 16-bit pools with heads of 64 or 128 and FP8 pools.
  *   q, out         device [num_seqs, q_len, num_q_heads, head_dim], not overlapping

@@ -11,10 +11,10 @@
 // CTA's warps are joined in its shared memory, those of the cluster's CTAs through each other's, each CTA writing a share
 // of the outputs: one launch, no workspace, a fixed order.
 //
-// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 78 to 81 us, 6.7 to 6.9 TB/s, the copy rate; one
-// sequence of 64 blocks 6.7 us (in a graph 5.8): launch 2, lookups 1.5, two tiles a warp 1, joins 2; 19 sequences of 50 blocks
-// of 32 in an FP8 pool, 16 query rows: 17.2 us, bound by a warp's chain per tile (scores 300 cycles, softmax 360, weights 90,
-// values and the next copies 500) at eight warps an SM.
+// Measured: 64 sequences of 128 blocks of 16 tokens, 64 / 8 heads of 128, bf16 (539 MB): 78 to 81 us, 6.7 to 6.9 TB/s, the copy
+// rate; one sequence of 64 blocks 6.9 us (in a graph 5.9): launch 2, lookups 1.5, two tiles a warp 1, joins 2; 19 sequences of
+// 50 blocks of 32 in an FP8 pool, 16 query rows, fp16: 20.4 us, bound by a warp's chain per tile at eight warps an SM (with
+// weights in one part 17.2: scores 300 cycles, softmax 360, weights 90, values and the next copies 500).
 #include <type_traits>
 
 #include "pa_cluster.cuh"
@@ -49,8 +49,9 @@ static_assert(ATT_MAX_TILES <= ATT_WARP_TILES * ATT_WARPS * ATT_MAX_RANKS, "the 
 
 // Copies of a warp's pipeline in flight, and CTAs per SM. FP8 pools, tiles of 4 KB: two copies (three: 19 sequences of a verify
 // 17.5 -> 17.7 us, 64 of 2048 tokens 44 -> 46), four CTAs with one column of eight rows, else two by registers (16 rows at
-// three CTAs, with spills: 18.9 -> 23.0; as pairs of warps on a pipeline, eight rows each, 16 warps an SM: 17.6 -> 21.4). 16-bit pools, 8 KB: three copies, two CTAs. Three CTAs of two copies each keep as many
-// bytes in flight: 64 sequences of 128 blocks 86 us instead of 79.
+// three CTAs, with spills: 18.9 -> 23.0; as pairs of warps on a pipeline, eight rows each, 16 warps an SM: 17.6 -> 21.4). 16-bit
+// pools, 8 KB: three copies, two CTAs. Three CTAs of two copies each keep as many bytes in flight: 64 sequences of 128 blocks 86
+// us instead of 79.
 __host__ __device__ constexpr int att_stages(bool kv8) { return kv8 ? 2 : 3; }
 __host__ __device__ constexpr int att_ctas(bool kv8, int nt) { return kv8 && nt == 1 ? 4 : 2; }
 __host__ __device__ constexpr int att_tile_bytes(int D, bool kv8) { return TILE_TOKENS * (kv8 ? 128 : 2 * D); }
