@@ -28,6 +28,10 @@ def test_infinities_and_nan_that_every_row_sees(dt, d, hq, hkv, q_len):
     v[later, 0, 2, 9] = math.nan
     v[last, hkv - 1, 2, 11] = -math.inf                    # beside tokens that not every row sees
     v[int(tables[1, 0]), 0, :, 2] = math.inf               # a whole block
+    for cache in (pool.k_cache, v):                        # behind the context, where the tiles are looked at again
+        cache[last, :, 12:] = math.nan
+    if q_len > 1:
+        v[last, 0, 11] = math.inf                          # the newest draft's, beside them
     sel[0, :, :3] = i32([0, 20, 43])
     sel[0, :, 3:] = i32([j for j in range(44) if j not in (0, 20, 43)][:37])
     out = definition(pool, q, sel, tables, lens, 0.1)[0]
@@ -35,11 +39,12 @@ def test_infinities_and_nan_that_every_row_sees(dt, d, hq, hkv, q_len):
     run(pool, tables, q, lens, sel, 0.1)
 
 
+@pytest.mark.parametrize("hq", [2, 8, 16, 24, 32])
 @pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
-def test_fp8_scales_that_are_no_numbers(dt):
+def test_fp8_scales_that_are_no_numbers(dt, hq):
     """A token of an infinite V scale: infinity by its code's sign (its codes are no zeros), a NaN code or scale: NaN."""
     lens = [600, 100]
-    pool, tables, q = make(lens, 8, 2, 128, dt, 16, 2, fp8=True, seed=4)
+    pool, tables, q = make(lens, hq, 2, 128, dt, 16, 2, fp8=True, seed=4)
     sel = pick(lens, 2, 16, 38, 6)
     nb, hkv, bs, d = pool.geometry
     codes = pool.v_cache[:nb * hkv * bs * d].view(nb, hkv, bs, d)
@@ -49,6 +54,9 @@ def test_fp8_scales_that_are_no_numbers(dt):
     scales[a, 0, 4] = math.inf
     codes[a, 1, 9, 77] = 0x7F
     scales[b, 1, 0] = math.nan
+    last = int(tables[1, 6])                               # tokens 96 to 99, the last of them a draft of one row
+    scales[last, :, 4:], codes[last, :, 5:] = math.nan, 0x7F
+    scales[last, 0, 3] = math.inf
     out = definition(pool, q, sel, tables, lens, 0.1)[0]
     assert bool(out.isinf().any()) and bool(out.isnan().any()) and bool(out.isfinite().any())
     run(pool, tables, q, lens, sel, 0.1)
